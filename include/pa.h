@@ -37,6 +37,7 @@
  *   k, v (new tokens) [num_tokens][num_kv_heads][head_dim]
  *   slot_mapping      [num_tokens] int64, slot = block * block_size + offset
  *   src_dst_pairs     [num_pairs][2] int64 (src block, dst block)
+ * (the 4-bit caches of the *_q4 calls have a layout of their own, below)
  * Query head h attends with KV head h / (num_q_heads / num_kv_heads).
  */
 #ifndef PA_H_
@@ -70,6 +71,7 @@ extern "C" {
                                        write) not the slot of the sequence's last position */
 #define PA_STATUS_BAD_PAIR 8        /* copy pair out of range, or its dst is another pair's src/dst */
 #define PA_STATUS_WAIT_TIMEOUT 16   /* a bounded wait for staged data gave up */
+#define PA_STATUS_SHORT_LIST 32     /* pa_build_tables: fewer block ids or token rows than the lengths need */
 
 /* ---- decode attention --------------------------------------------------
  * [P3] "Jak dziala" / "Komponenty": the attention kernel reads the K/V cache
@@ -172,6 +174,30 @@ int pa_decode(void *out, const void *q, const void *k_cache, const void *v_cache
  * split of long contexts, so this call has no counterpart there. */
 size_t pa_decode_workspace_size(int num_seqs, int num_q_heads, int head_dim,
                                 int max_context_len, int partition_size);
+
+/* ---- decode attention with a sliding window ------------------------------
+ * pa_decode over a part of each sequence: with n = context_lens[i], only
+ * positions t >= n - window (the last `window` tokens, the newest included)
+ * and t < num_sinks (the first tokens, which stay visible) take part; the rest
+ * have weight zero, whatever their cache slots hold (NaN included).  window >=
+ * 1 (PA_ERR_INVALID_ARG otherwise; a window of n or more attends to
+ * everything), num_sinks >= 0.  No counterpart in the pages.
+ *
+ * Only blocks that hold a visible position are looked up and read, so the
+ * blocks between the sinks and the window may have been given back: their
+ * table entries may hold anything.  The fused cache write works as in
+ * pa_decode.  args->simt must be 0 for PA_BF16 (PA_ERR_UNSUPPORTED).
+ * Everything else, types, layouts, checks, determinism, as pa_decode; the
+ * workspace is sized by what is visible. */
+int pa_decode_window(void *out, const void *q, const void *k_cache, const void *v_cache,
+                     const int32_t *block_tables, const int32_t *context_lens,
+                     int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                     float scale, int window, int num_sinks, const pa_decode_args *args);
+
+/* Bytes of workspace pa_decode_window needs (0 when no sequence can show it
+ * more than one partition, and for a window or sink count it refuses). */
+size_t pa_decode_window_workspace_size(int num_seqs, int num_q_heads, int head_dim, int max_context_len,
+                                       int partition_size, int window, int num_sinks);
 
 /* ---- decode attention without a caller workspace ----------------------
  * The paper has no counterpart to this call; it is a convenience of this
@@ -346,6 +372,110 @@ int pa_bm_append_slots(pa_bm *bm, const int32_t *seq_ids, int n, int64_t *slots,
  * tables [n][max_blocks_per_seq] (unused entries = -1), context_lens [n]. */
 int pa_bm_build_tables(const pa_bm *bm, const int32_t *seq_ids, int n, int32_t *tables,
                        int max_blocks_per_seq, int32_t *context_lens);
+
+/* Block ids of a batch without padding: sequence by sequence, each one's ids in
+ * logical order, into out[0..cap), and (when not NULL) every sequence's tokens
+ * into context_lens [n].  Returns the number of ids (PA_ERR_INVALID_ARG if cap
+ * is too small).  The block_ids and context_lens of pa_build_tables, which
+ * lays the padded tables out on the device: this list is the smaller upload. */
+int pa_bm_flat_blocks(const pa_bm *bm, const int32_t *seq_ids, int n, int32_t *out, int cap,
+                      int32_t *context_lens);
+
+/* ---- batch tables on the device ------------------------------------------
+ * The device counterpart of pa_bm_build_tables, with the step's slot map: from
+ * each sequence's length and one flat list of block ids it lays out what the
+ * cache write and the decode calls read.  No counterpart in the pages, which
+ * say nothing of how tables reach the device.
+ *
+ * With n_i = context_lens[i] tokens in the cache after this step, the last
+ * c_i = new_lens[i] of them new, b_i = ceil(n_i / block_size),
+ * first_i = b_0 + ... + b_(i-1) and start_i = c_0 + ... + c_(i-1):
+ *   block_tables[i][j] = block_ids[first_i + j] for j < b_i, else -1
+ *                                             ([num_seqs][max_blocks_per_seq])
+ *   query_start[i] = start_i, query_start[num_seqs] = start_num_seqs = total
+ *   row start_i + r (r < c_i) is position p = n_i - c_i + r of sequence i:
+ *     positions[row] = p
+ *     slot_mapping[row] = block * block_size + p % block_size, with
+ *                         block = block_ids[first_i + p / block_size]
+ *   rows total .. max_tokens-1: slot_mapping = -1 (padding, which the cache
+ *   writes skip), positions = 0.
+ * positions and query_start may be NULL; slot_mapping may be NULL when
+ * max_tokens is 0, and block_ids when num_ids is 0.  The outputs must not
+ * overlap the inputs.  One launch; the sums are taken by every CTA for itself,
+ * so there is no workspace and calls on different streams do not meet.
+ *
+ * Device data is checked as everywhere: a length outside [0,
+ * max_blocks_per_seq * block_size] or a new length outside [0, n_i] is clamped
+ * and sets PA_STATUS_BAD_CONTEXT_LEN; a block id outside [0, num_blocks) gives
+ * table entry -1 and slots -1 and sets PA_STATUS_BAD_BLOCK_ID; ids past
+ * num_ids likewise, and rows past max_tokens are dropped, with
+ * PA_STATUS_SHORT_LIST. */
+int pa_build_tables(int32_t *block_tables, int64_t *slot_mapping, int32_t *positions, int32_t *query_start,
+                    const int32_t *block_ids, const int32_t *context_lens, const int32_t *new_lens,
+                    int num_seqs, int max_blocks_per_seq, int max_tokens, int num_ids, int block_size,
+                    int num_blocks, int32_t *dev_status, void *stream);
+
+/* ---- 4-bit cache -----------------------------------------------------------
+ * K and V held in 4 bits a value, with a step and a minimum for every group of
+ * group_size (32 or 64) values of a head row.  Each cache is a byte array
+ *   [num_blocks][num_kv_heads][page_bytes],
+ *   page_bytes = block_size * (head_dim / 2 + 4 * head_dim / group_size),
+ * 16-byte aligned.  A page holds its block_size rows' codes (head_dim / 2
+ * bytes each), then their parameters: [block_size][head_dim / group_size]
+ * pairs (step s, minimum m) of bf16.  Code c of a group stands for s * c + m.
+ * Within a row's codes, values go in units of four (16 bits, the first value
+ * in the lowest bits); with W = head_dim / 64, unit 16 w + 8 h + g (w < W,
+ * h < 2, g < 8) is half h of 32-bit word g * W + w.  (The order gives each lane
+ * of the decode kernel its share of a row in one load.)
+ *
+ * Quantisation of a group, every operation rounded to fp32 unless stated, so
+ * that every writer gives the same bits:
+ *   m = min(x) rounded down to bf16;  far = max(x) - m;
+ *   s = 0 if far = 0, else max(far / 15 rounded up to bf16, 2^-126);
+ *   c = round_half_even((x - m) * (1 / s)), 0 where s = 0.
+ * Then |s c + m - x| <= s / 2 (up to fp32 rounding).  A group that holds a NaN,
+ * an infinity or a magnitude of 2^126 or more stands for NaN throughout (m =
+ * NaN, s = 0), as an unquantised cache would let it show.
+ *
+ * Whole blocks are bytes to pa_copy_blocks and pa_swap_blocks: pass dtype
+ * PA_BF16 and head_dim = page_bytes / block_size / 2 with the block size. */
+
+/* Bytes of one page; 0 if the sizes are not supported (head_dim 64 or 128,
+ * block_size 16 or 32, group_size 32 or 64). */
+size_t pa_q4_page_bytes(int head_dim, int block_size, int group_size);
+
+/* Quantise and write new rows: for each token t with slot s = slot_mapping[t]
+ * >= 0, head rows k[t][h] and v[t][h] ([num_tokens][num_kv_heads][head_dim],
+ * dtype) go to row s % block_size of pages (s / block_size, h).  Padding (slot
+ * < 0), bad slots and repeated slots as in pa_reshape_and_cache. */
+int pa_reshape_and_cache_q4(const void *k, const void *v, void *k_cache, void *v_cache,
+                            const int64_t *slot_mapping, int num_tokens, int num_kv_heads, int head_dim,
+                            int block_size, int group_size, int num_blocks, int dtype, int32_t *dev_status,
+                            void *stream);
+
+/* Read rows back as values s * c + m, rounded once to dtype: k[t][h], v[t][h]
+ * from the slots of slot_mapping (any order, repeats allowed).  Rows with a
+ * negative slot, or (flagged) one past the pool, are left as they were. */
+int pa_gather_q4(void *k, void *v, const void *k_cache, const void *v_cache, const int64_t *slot_mapping,
+                 int num_tokens, int num_kv_heads, int head_dim, int block_size, int group_size,
+                 int num_blocks, int dtype, int32_t *dev_status, void *stream);
+
+/* Decode attention over the 4-bit cache: pa_decode (window == 0) or
+ * pa_decode_window (window >= 1) with K_i[t], V_i[t] the values s * c + m that
+ * the cache holds.  args->dtype is the type of q and out; products and sums
+ * are in fp32 or more.  A block id out of range reads as zeros (flagged).
+ * args->partition_size is 0 (the library picks) or a multiple of 32 in
+ * [32, 4096]; args->simt must be 0 and k_new, v_new and slot_mapping NULL
+ * (PA_ERR_UNSUPPORTED): pa_reshape_and_cache_q4 writes the step's tokens. */
+int pa_decode_q4(void *out, const void *q, const void *k_cache, const void *v_cache,
+                 const int32_t *block_tables, const int32_t *context_lens, int num_q_heads, int num_kv_heads,
+                 int head_dim, int block_size, int group_size, float scale, int window, int num_sinks,
+                 const pa_decode_args *args);
+
+/* Bytes of workspace pa_decode_q4 needs (0 when no sequence can span more than
+ * one partition). */
+size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                   int max_context_len, int partition_size, int window, int num_sinks);
 
 /* ---- self-test of the bounded wait ----------------------------------------
  * Every wait of the decode kernels for staged data gives up after about two

@@ -11,6 +11,7 @@ over ``pa_bm_*``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -36,6 +37,7 @@ STATUS_BAD_CONTEXT_LEN = 2
 STATUS_BAD_SLOT = 4
 STATUS_BAD_PAIR = 8
 STATUS_WAIT_TIMEOUT = 16
+STATUS_SHORT_LIST = 32
 
 
 class PAError(RuntimeError):
@@ -119,6 +121,26 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.pa_bm_num_cached.argtypes = [vp]
     lib.pa_bm_build_tables.restype = i32
     lib.pa_bm_build_tables.argtypes = [vp, vp, i32, vp, i32, vp]
+    lib.pa_decode_window.restype = i32
+    lib.pa_decode_window.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, i32, i32,
+                                     ctypes.POINTER(_DecodeArgs)]
+    lib.pa_decode_window_workspace_size.restype = sz
+    lib.pa_decode_window_workspace_size.argtypes = [i32] * 7
+    lib.pa_decode_q4.restype = i32
+    lib.pa_decode_q4.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, i32,
+                                 ctypes.POINTER(_DecodeArgs)]
+    lib.pa_decode_q4_workspace_size.restype = sz
+    lib.pa_decode_q4_workspace_size.argtypes = [i32] * 8
+    lib.pa_bm_flat_blocks.restype = i32
+    lib.pa_bm_flat_blocks.argtypes = [vp, vp, i32, vp, i32, vp]
+    lib.pa_build_tables.restype = i32
+    lib.pa_build_tables.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.pa_q4_page_bytes.restype = sz
+    lib.pa_q4_page_bytes.argtypes = [i32, i32, i32]
+    lib.pa_reshape_and_cache_q4.restype = i32
+    lib.pa_reshape_and_cache_q4.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.pa_gather_q4.restype = i32
+    lib.pa_gather_q4.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp]
     lib.pa_last_error_string.restype = ctypes.c_char_p
     lib.pa_last_error_string.argtypes = []
     lib.pa_version.restype = i32
@@ -152,8 +174,19 @@ def _raise(rc: int):
 
 def _stream_ptr(stream, device) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _ptr(t: torch.Tensor | None):
+    return t.data_ptr() if t is not None else None
+
+
+def _on_device(dev: torch.device):
+    """Makes dev the current device for a call; nothing to do when it is."""
+    if torch.cuda.current_device() == dev.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
 
 
 def _check_cuda(t: torch.Tensor, name: str, dtypes, dev=None):
@@ -221,6 +254,64 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache
     same launch (fused cache write).  ``simt=True`` (bf16 only) computes the
     products with fp32 FMAs instead of tensor-core MMAs.
     """
+    call = _decode_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
+                        partition_size, workspace, status, phase, k_new, v_new, slot_mapping, simt,
+                        skip_counter_reset)
+    return call(stream)
+
+
+def pa_decode_window_workspace_size(num_seqs: int, num_q_heads: int, head_dim: int, max_context_len: int,
+                                    partition_size: int = 0, *, window: int, num_sinks: int = 0) -> int:
+    return int(_lib.pa_decode_window_workspace_size(num_seqs, num_q_heads, head_dim, max_context_len,
+                                                    partition_size, window, num_sinks))
+
+
+def pa_decode_window(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, *, window: int,
+                     num_sinks: int = 0, max_context_len: int, partition_size: int = 0,
+                     workspace: torch.Tensor | None = None, status: DeviceStatus | None = None, stream=None,
+                     phase: int = 0, k_new: torch.Tensor | None = None, v_new: torch.Tensor | None = None,
+                     slot_mapping: torch.Tensor | None = None, skip_counter_reset: bool = False) -> torch.Tensor:
+    """``pa_decode`` over the last ``window`` tokens of each sequence and its
+    first ``num_sinks``.  Blocks that hold none of them are not looked up, so
+    their table entries may hold anything.  The other arguments are those of
+    ``pa_decode``; the workspace takes ``pa_decode_window_workspace_size`` bytes.
+    """
+    if window < 1 or num_sinks < 0:
+        raise ValueError("window must be at least 1 and num_sinks at least 0")
+    call = _decode_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
+                        partition_size, workspace, status, phase, k_new, v_new, slot_mapping, False,
+                        skip_counter_reset, window, num_sinks)
+    return call(stream)
+
+
+class _PreparedCall:
+    """A checked decode call: pointers and sizes are taken from its tensors,
+    which it keeps, once; each call enqueues it on a stream."""
+
+    def __init__(self, fn, out, operands, sizes, args, device, keep):
+        self._fn, self._out, self._args, self._device, self._keep = fn, out, args, device, keep
+        self._operands = [ctypes.c_void_p(t.data_ptr()) for t in (out, *operands)]
+        self._sizes, self._ref = sizes, ctypes.byref(args)
+
+    def __call__(self, stream=None, phase=None) -> torch.Tensor:
+        a = self._args
+        a.stream = _stream_ptr(stream, self._device)
+        if phase is not None:
+            a.phase = phase
+        if torch.cuda.current_device() == self._device.index:
+            rc = self._fn(*self._operands, *self._sizes, self._ref)
+        else:
+            with torch.cuda.device(self._device):
+                rc = self._fn(*self._operands, *self._sizes, self._ref)
+        _raise(rc)
+        return self._out
+
+
+def _decode_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, partition_size,
+                 workspace, status, phase, k_new, v_new, slot_mapping, simt, skip_counter_reset, window=0,
+                 num_sinks=0) -> _PreparedCall:
+    """The checks and arguments of pa_decode (window 0) and pa_decode_window."""
     fdt = (torch.float32, torch.bfloat16)
     _check_cuda(q, "q", fdt)
     dev = q.device
@@ -236,12 +327,12 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache
     if (hd2 != hd or tuple(v_cache.shape) != tuple(k_cache.shape) or tuple(out.shape) != tuple(q.shape)
             or block_tables.shape[0] != S or tuple(context_lens.shape) != (S,)):
         raise ValueError("inconsistent shapes")
-    need = pa_decode_workspace_size(S, Hq, hd, max_context_len, partition_size)
-    if need and workspace is None:
-        workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
-        skip_counter_reset = True
-    if workspace is not None:
-        _check_cuda(workspace, "workspace", (torch.uint8,), dev)
+    if window:
+        need = pa_decode_window_workspace_size(S, Hq, hd, max_context_len, partition_size, window=window,
+                                               num_sinks=num_sinks)
+    else:
+        need = pa_decode_workspace_size(S, Hq, hd, max_context_len, partition_size)
+    workspace, skip_counter_reset = _workspace(workspace, need, skip_counter_reset, dev)
     fused = (k_new, v_new, slot_mapping)
     if any(t is not None for t in fused):
         if any(t is None for t in fused):
@@ -257,17 +348,26 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache
                        workspace.data_ptr() if workspace is not None else None,
                        workspace.numel() if workspace is not None else 0,
                        status.ptr() if status is not None else None,
-                       _stream_ptr(stream, dev), phase,
+                       None, phase,
                        k_new.data_ptr() if k_new is not None else None,
                        v_new.data_ptr() if v_new is not None else None,
                        slot_mapping.data_ptr() if slot_mapping is not None else None,
                        1 if simt else 0, 1 if skip_counter_reset else 0)
-    with torch.cuda.device(dev):
-        rc = _lib.pa_decode(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                            block_tables.data_ptr(), context_lens.data_ptr(), Hq, Hkv, hd, bs,
-                            float(scale), ctypes.byref(args))
-    _raise(rc)
-    return out
+    sizes = [Hq, Hkv, hd, bs, float(scale)]
+    keep = (out, q, k_cache, v_cache, block_tables, context_lens, workspace, status, k_new, v_new, slot_mapping)
+    operands = (q, k_cache, v_cache, block_tables, context_lens)
+    if window:
+        return _PreparedCall(_lib.pa_decode_window, out, operands, [*sizes, window, num_sinks], args, dev, keep)
+    return _PreparedCall(_lib.pa_decode, out, operands, sizes, args, dev, keep)
+
+
+def _workspace(workspace, need, skip_counter_reset, dev):
+    """The caller's workspace, checked, or a zeroed one when one is needed."""
+    if need and workspace is None:
+        return torch.zeros(need, dtype=torch.uint8, device=dev), True
+    if workspace is not None:
+        _check_cuda(workspace, "workspace", (torch.uint8,), dev)
+    return workspace, skip_counter_reset
 
 
 def pa_reshape_and_cache(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -342,6 +442,166 @@ def pa_swap_blocks(src_k: torch.Tensor, src_v: torch.Tensor, dst_k: torch.Tensor
                                  src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], nbs, dst_k.shape[0], Hkv, hd,
                                  bs, _dtype_code(src_k.dtype), status.ptr() if status is not None else None,
                                  _stream_ptr(stream, dev))
+    _raise(rc)
+
+
+def pa_build_tables(block_tables: torch.Tensor, slot_mapping: torch.Tensor, positions: torch.Tensor | None,
+                    query_start: torch.Tensor | None, block_ids: torch.Tensor, context_lens: torch.Tensor,
+                    new_lens: torch.Tensor, *, block_size: int, num_blocks: int,
+                    status: DeviceStatus | None = None, stream=None) -> None:
+    """Lay out a batch's tables on the GPU from its lengths and flat block list.
+
+    Inputs (int32, on the GPU): block_ids [N], every sequence's blocks in
+    order without padding; context_lens [S], the tokens each sequence holds
+    after this step; new_lens [S], how many of them (the last ones) are new.
+    Outputs: block_tables [S, max_blocks] int32 padded with -1; slot_mapping
+    [T] int64 and positions [T] int32 (or None) of the new tokens, sequence by
+    sequence, rows behind the last token -1 and 0; query_start [S + 1] int32
+    (or None), where each sequence's new tokens begin.
+    ``BlockManager.flat_blocks`` gives block_ids and context_lens.
+    """
+    _check_cuda(block_tables, "block_tables", (torch.int32,))
+    dev = block_tables.device
+    _check_cuda(slot_mapping, "slot_mapping", (torch.int64,), dev)
+    for name, t in (("block_ids", block_ids), ("context_lens", context_lens), ("new_lens", new_lens)):
+        _check_cuda(t, name, (torch.int32,), dev)
+    if block_tables.dim() != 2 or slot_mapping.dim() != 1 or block_ids.dim() != 1:
+        raise ValueError("block_tables must be [S, max_blocks], slot_mapping [T], block_ids [N]")
+    S, T = block_tables.shape[0], slot_mapping.shape[0]
+    if tuple(context_lens.shape) != (S,) or tuple(new_lens.shape) != (S,):
+        raise ValueError("context_lens and new_lens must be [S]")
+    if positions is not None:
+        _check_cuda(positions, "positions", (torch.int32,), dev)
+        if tuple(positions.shape) != (T,):
+            raise ValueError("positions must be [T] like slot_mapping")
+    if query_start is not None:
+        _check_cuda(query_start, "query_start", (torch.int32,), dev)
+        if tuple(query_start.shape) != (S + 1,):
+            raise ValueError("query_start must be [S + 1]")
+    with _on_device(dev):
+        rc = _lib.pa_build_tables(block_tables.data_ptr(), slot_mapping.data_ptr(), _ptr(positions),
+                                  _ptr(query_start), block_ids.data_ptr(), context_lens.data_ptr(),
+                                  new_lens.data_ptr(), S, block_tables.shape[1], T, block_ids.shape[0], block_size,
+                                  num_blocks, status.ptr() if status is not None else None,
+                                  _stream_ptr(stream, dev))
+    _raise(rc)
+
+
+def pa_q4_page_bytes(head_dim: int, block_size: int, group_size: int = 64) -> int:
+    """Bytes of one page (block, KV head) of a 4-bit cache; its caches are
+    uint8 tensors [num_blocks, Hkv, page_bytes]."""
+    n = int(_lib.pa_q4_page_bytes(head_dim, block_size, group_size))
+    if n == 0:
+        raise PAError(PA_ERR_UNSUPPORTED, "pa_q4_page_bytes: head_dim must be 64 or 128, block_size 16 or 32, "
+                                          "group_size 32 or 64")
+    return n
+
+
+def q4_block_rows(cache: torch.Tensor, block_size: int) -> torch.Tensor:
+    """A 4-bit cache's bytes as the bf16 [num_blocks, Hkv, block_size, n] tensor
+    of the same memory that ``pa_copy_blocks`` and ``pa_swap_blocks`` take
+    (they move whole blocks bit for bit)."""
+    nb, Hkv, page = cache.shape
+    if page % (2 * block_size):
+        raise ValueError(f"page_bytes {page} does not hold whole rows of {block_size} tokens")
+    return cache.view(torch.bfloat16).view(nb, Hkv, block_size, page // (2 * block_size))
+
+
+def _q4_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor, head_dim: int, group_size: int, dev):
+    """Checks a pair of 4-bit caches; returns (num_blocks, Hkv, block_size)."""
+    _check_cuda(k_cache, "k_cache", (torch.uint8,), dev)
+    _check_cuda(v_cache, "v_cache", (torch.uint8,), dev)
+    if k_cache.dim() != 3 or v_cache.shape != k_cache.shape:
+        raise ValueError("4-bit caches must be uint8 [num_blocks, Hkv, page_bytes], both of one shape")
+    nb, Hkv, page = k_cache.shape
+    for bs in (16, 32):
+        if page == _lib.pa_q4_page_bytes(head_dim, bs, group_size):
+            return nb, Hkv, bs
+    raise ValueError(f"page_bytes {page} is not pa_q4_page_bytes({head_dim}, 16 or 32, {group_size})")
+
+
+def pa_reshape_and_cache_q4(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                            slot_mapping: torch.Tensor, *, group_size: int = 64,
+                            status: DeviceStatus | None = None, stream=None) -> None:
+    """Quantise k, v [T, Hkv, hd] (bf16 or fp32) into the 4-bit caches
+    (uint8 [num_blocks, Hkv, page_bytes]) at slot_mapping [T] int64."""
+    _q4_rows_call(_lib.pa_reshape_and_cache_q4, k, v, k_cache, v_cache, slot_mapping, group_size, status, stream)
+
+
+def pa_gather_q4(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 slot_mapping: torch.Tensor, *, group_size: int = 64, status: DeviceStatus | None = None,
+                 stream=None) -> None:
+    """Read rows of the 4-bit caches back into k, v [T, Hkv, hd] (bf16 or
+    fp32); rows with a negative slot are left as they were."""
+    _q4_rows_call(_lib.pa_gather_q4, k, v, k_cache, v_cache, slot_mapping, group_size, status, stream)
+
+
+def pa_decode_q4_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                max_context_len: int, partition_size: int = 0, *, window: int = 0,
+                                num_sinks: int = 0) -> int:
+    return int(_lib.pa_decode_q4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                                                partition_size, window, num_sinks))
+
+
+def pa_decode_q4(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, *, max_context_len: int,
+                 group_size: int = 64, window: int = 0, num_sinks: int = 0, partition_size: int = 0,
+                 workspace: torch.Tensor | None = None, status: DeviceStatus | None = None, stream=None,
+                 phase: int = 0, skip_counter_reset: bool = False) -> torch.Tensor:
+    """Paged decode attention over 4-bit caches (uint8 [num_blocks, Hkv,
+    page_bytes], written by ``pa_reshape_and_cache_q4``); writes ``out``
+    [S, Hq, hd], of q's type, and returns it.
+
+    window 0 attends to every token; otherwise to the last ``window`` tokens
+    and the first ``num_sinks``, as ``pa_decode_window`` does.  The workspace,
+    where one is needed, takes ``pa_decode_q4_workspace_size`` bytes; the other
+    arguments are those of ``pa_decode``.
+    """
+    return _decode_q4_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, group_size,
+                           window, num_sinks, partition_size, workspace, status, phase, skip_counter_reset)(stream)
+
+
+def _decode_q4_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, group_size,
+                    window, num_sinks, partition_size, workspace, status, phase, skip_counter_reset) -> _PreparedCall:
+    """The checks and arguments of pa_decode_q4."""
+    _check_cuda(q, "q", (torch.float32, torch.bfloat16))
+    dev = q.device
+    _check_cuda(out, "out", (q.dtype,), dev)
+    _check_cuda(block_tables, "block_tables", (torch.int32,), dev)
+    _check_cuda(context_lens, "context_lens", (torch.int32,), dev)
+    if q.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q must be [S, Hq, hd], tables [S, max_blocks]")
+    S, Hq, hd = q.shape
+    nb, Hkv, bs = _q4_geometry(k_cache, v_cache, hd, group_size, dev)
+    if tuple(out.shape) != tuple(q.shape) or block_tables.shape[0] != S or tuple(context_lens.shape) != (S,):
+        raise ValueError("inconsistent shapes")
+    need = pa_decode_q4_workspace_size(S, Hq, Hkv, hd, max_context_len, partition_size, window=window,
+                                       num_sinks=num_sinks)
+    workspace, skip_counter_reset = _workspace(workspace, need, skip_counter_reset, dev)
+    args = _DecodeArgs(S, block_tables.shape[1], nb, _dtype_code(q.dtype), partition_size, max_context_len,
+                       _ptr(workspace), workspace.numel() if workspace is not None else 0,
+                       status.ptr() if status is not None else None, None, phase, None, None, None, 0,
+                       1 if skip_counter_reset else 0)
+    return _PreparedCall(_lib.pa_decode_q4, out, (q, k_cache, v_cache, block_tables, context_lens),
+                         [Hq, Hkv, hd, bs, group_size, float(scale), window, num_sinks], args, dev,
+                         (workspace, status, q, k_cache, v_cache, block_tables, context_lens))
+
+
+def _q4_rows_call(fn, k, v, k_cache, v_cache, slot_mapping, group_size, status, stream):
+    _check_cuda(k, "k", (torch.float32, torch.bfloat16))
+    dev = k.device
+    _check_cuda(v, "v", (k.dtype,), dev)
+    _check_cuda(slot_mapping, "slot_mapping", (torch.int64,), dev)
+    if k.dim() != 3 or v.shape != k.shape or tuple(slot_mapping.shape) != (k.shape[0],):
+        raise ValueError("k, v must be [T, Hkv, hd] and slot_mapping [T]")
+    T, Hkv, hd = k.shape
+    nb, heads, bs = _q4_geometry(k_cache, v_cache, hd, group_size, dev)
+    if heads != Hkv:
+        raise ValueError("inconsistent shapes")
+    with _on_device(dev):
+        rc = fn(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, Hkv,
+                hd, bs, group_size, nb, _dtype_code(k.dtype), status.ptr() if status is not None else None,
+                _stream_ptr(stream, dev))
     _raise(rc)
 
 
@@ -449,6 +709,20 @@ class BlockManager:
         if r < 0:
             _raise(r)
         return r
+
+    def flat_blocks(self, seq_ids):
+        """Block ids of a batch without padding, int32 [N], and context
+        lengths, int32 [n] (host): what ``pa_build_tables`` lays out."""
+        ids = torch.tensor(list(seq_ids), dtype=torch.int32)
+        n = ids.numel()
+        lens = torch.tensor([self.num_tokens(s) for s in ids.tolist()], dtype=torch.int32)
+        cap = int(((lens.long() + self.block_size - 1) // self.block_size).sum())
+        out = torch.empty(cap, dtype=torch.int32)
+        got = _lib.pa_bm_flat_blocks(self._h, ids.data_ptr() if n else None, n, out.data_ptr() if cap else None, cap,
+                                     lens.data_ptr() if n else None)
+        if got < 0:
+            _raise(got)
+        return out[:got], lens
 
     def build_tables(self, seq_ids, max_blocks_per_seq: int):
         """Padded int32 tables [n, max_blocks_per_seq] and context lengths [n] (host)."""

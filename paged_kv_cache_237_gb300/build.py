@@ -22,9 +22,10 @@ LIB_NAME = "libpa_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-CUDA_SOURCES = ["pa_decode.cu", "pa_decode_simt.cu", "pa_cache.cu"]
+CUDA_SOURCES = ["pa_decode.cu", "pa_decode_simt.cu", "pa_cache.cu", "pa_decode_q4.cu", "pa_cache_q4.cu",
+                "pa_tables.cu"]
 CXX_SOURCES = ["block_manager.cpp", "pa_api.cpp"]
-HEADERS = ["pa_internal.h", "pa_decode_common.cuh"]
+HEADERS = ["pa_internal.h", "pa_decode_common.cuh", "pa_q4.cuh"]
 
 
 def _nvcc() -> str:

@@ -372,6 +372,23 @@ extern "C" int pa_bm_build_tables(const pa_bm *bm, const int32_t *seq_ids, int n
     return PA_OK;
 }
 
+extern "C" int pa_bm_flat_blocks(const pa_bm *bm, const int32_t *seq_ids, int n, int32_t *out, int cap,
+                                 int32_t *context_lens) {
+    if (!bm || n < 0 || cap < 0 || (n > 0 && !seq_ids) || (cap > 0 && !out))
+        return pa_fail(PA_ERR_INVALID_ARG, "pa_bm_flat_blocks: bad arguments");
+    int64_t at = 0;
+    for (int k = 0; k < n; ++k) {
+        auto it = bm->seqs.find(seq_ids[k]);
+        if (it == bm->seqs.end()) return pa_fail(PA_ERR_REFCOUNT, "pa_bm_flat_blocks: unknown sequence");
+        const auto &blocks = it->second.blocks;
+        if (at + static_cast<int64_t>(blocks.size()) > cap)
+            return pa_fail(PA_ERR_INVALID_ARG, "pa_bm_flat_blocks: out too small");
+        for (int32_t b : blocks) out[at++] = b;
+        if (context_lens) context_lens[k] = static_cast<int32_t>(it->second.num_tokens);
+    }
+    return static_cast<int>(at);
+}
+
 extern "C" int pa_bm_move_seq(pa_bm *from, pa_bm *to, int seq_id, int64_t *pairs, int cap, int *num_pairs) {
     if (!from || !to || !num_pairs || cap < 0 || (cap > 0 && !pairs) || from == to)
         return pa_fail(PA_ERR_INVALID_ARG, "pa_bm_move_seq: bad arguments");

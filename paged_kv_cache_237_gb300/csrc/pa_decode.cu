@@ -60,7 +60,7 @@ constexpr int bf16_stages() { return HD == 128 ? 2 : 3; }
 template <int HD>
 constexpr int bf16_ctas_per_sm() { return HD == 128 ? 3 : 4; }
 
-template <int HD, int NSTAGE, bool ROWS16>
+template <int HD, int NSTAGE, bool ROWS16, bool WIN>
 __global__ void __launch_bounds__(kWarps * 32, bf16_ctas_per_sm<HD>())
     decode_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const DecodeParams p) {
@@ -116,17 +116,17 @@ __global__ void __launch_bounds__(kWarps * 32, bf16_ctas_per_sm<HD>())
     int nb = 0;
     for (long long item = blockIdx.x;;) {
         Item it;
-        if (!next_item(it, cur, item, p, 16, lane)) break;
+        if (!next_item<WIN>(it, cur, item, p, 16, lane)) break;
         const int my_n = it.nchunks > warp ? (it.nchunks - warp + kWarps - 1) / kWarps : 0;
 
         // Rows of this warp's chunks: lane j holds chunks j and j + 32.
         int rowA = oob_row, rowB = oob_row;
         if (lane < my_n) {
-            int r = chunk_row(p, it, warp, lane);
+            int r = chunk_row<kWarps, WIN>(p, it, warp, lane);
             rowA = r < 0 ? oob_row : r;
         }
         if (lane + 32 < my_n) {
-            int r = chunk_row(p, it, warp, lane + 32);
+            int r = chunk_row<kWarps, WIN>(p, it, warp, lane + 32);
             rowB = r < 0 ? oob_row : r;
         }
 
@@ -207,7 +207,19 @@ __global__ void __launch_bounds__(kWarps * 32, bf16_ctas_per_sm<HD>())
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            if (valid < kChunk) {
+            uint32_t mask = 0xffffu;   // windowed: the chunk's tokens attended to
+            if constexpr (WIN) {
+                mask = window_mask(p, it.n, token_pos<WIN>(p, it, tok0), valid);
+                if (mask != 0xffffu) {
+                    // As below, for masked tokens anywhere in the chunk.
+                    uint8_t *vg = wbuf + s * STAGE_BYTES + PAGE_BYTES;
+                    for (int i = lane; i < HALVES * kChunk * 8; i += 32)
+                        if (!((mask >> (i / 8 % kChunk)) & 1u))
+                            *reinterpret_cast<uint4 *>(vg + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            } else if (valid < kChunk) {
                 // Tokens past the context: zero their V rows so that p = 0
                 // multiplies exact zeros (the slots may hold anything, NaN too).
                 uint8_t *vg = wbuf + s * STAGE_BYTES + PAGE_BYTES;
@@ -242,7 +254,7 @@ __global__ void __launch_bounds__(kWarps * 32, bf16_ctas_per_sm<HD>())
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int tok = 8 * nt + 2 * t + (j & 1);
-                    sc[nt][j] = tok < valid ? sc[nt][j] * p.scale_log2 : -INFINITY;
+                    sc[nt][j] = (WIN ? (mask >> tok) & 1u : tok < valid) ? sc[nt][j] * p.scale_log2 : -INFINITY;
                 }
 
             // Online softmax, base 2.  Row g uses sc[.][0..1], row g + 8 sc[.][2..3].
@@ -386,7 +398,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) decode_reduce_kernel(const 
     // writes them in sequence order, so the last sequences' are still in L2.
     const int seq = p.reduce_newest_first ? p.num_seqs - 1 - static_cast<int>(blockIdx.y)
                                           : static_cast<int>(blockIdx.y);
-    const int n = seq_len(p, seq);
+    const int n = p.window ? seq_view<true>(p, seq).seen : seq_len(p, seq);
     if (n <= p.partition_size) return;
     const int np = (n + p.partition_size - 1) / p.partition_size;
     const long long base = (long long)seq * p.max_parts * p.num_q_heads + qh;
@@ -494,14 +506,14 @@ using pa::DecodeParams;
 
 using namespace pa::host;
 
-template <int HD, bool ROWS16>
+template <int HD, bool ROWS16, bool WIN>
 int launch_bf16(const DecodeParams &p, const void *k_cache, const void *v_cache, long long items,
                 int dev, cudaStream_t st) {
     constexpr int NS = pa::bf16_stages<HD>();
     constexpr int STAGE = 2 * (HD / 64) * pa::kChunk * 128;
     constexpr int SMEM = pa::kWarps * NS * STAGE + pa::kWarps * NS * 8 + 1024;
     static KernelSlot slot;
-    auto kernel = pa::decode_bf16_kernel<HD, NS, ROWS16>;
+    auto kernel = pa::decode_bf16_kernel<HD, NS, ROWS16, WIN>;
     const int occ = ensure_kernel(kernel, slot, SMEM, dev);
     if (occ == 0) return pa_fail(PA_ERR_CUDA, "pa_decode: cannot configure the bf16 kernel");
     CUtensorMap mk, mv;
@@ -541,18 +553,24 @@ cudaError_t launch_reduce(const DecodeParams &p, cudaStream_t st) {
                  : cudaLaunchKernelEx(&cfg, pa::decode_reduce_kernel<OutT, HD, 8>, p);
 }
 
-inline bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-// Workspace layout: [work counter, 8 bytes, padded to 256] [partial (max, sum)]
-// [partial accumulators].  The counter sits at offset 0 whatever the sizes, so
-// a workspace reused for other sizes keeps a valid (zero) counter.
-constexpr size_t kWorkspaceHeader = 256;
+template <int HD>
+int launch_bf16_any(const DecodeParams &p, const void *k_cache, const void *v_cache, long long items, int dev,
+                    cudaStream_t st) {
+    if (p.group > 8)
+        return p.window ? launch_bf16<HD, true, true>(p, k_cache, v_cache, items, dev, st)
+                        : launch_bf16<HD, true, false>(p, k_cache, v_cache, items, dev, st);
+    return p.window ? launch_bf16<HD, false, true>(p, k_cache, v_cache, items, dev, st)
+                    : launch_bf16<HD, false, false>(p, k_cache, v_cache, items, dev, st);
+}
 
 int effective_partition(int partition_size) { return partition_size == 0 ? 512 : partition_size; }
 
 }  // namespace
+
+cudaError_t pa::launch_merge(const DecodeParams &p, bool f32, int head_dim, cudaStream_t st) {
+    if (f32) return head_dim == 128 ? launch_reduce<float, 128>(p, st) : launch_reduce<float, 64>(p, st);
+    return head_dim == 128 ? launch_reduce<__nv_bfloat16, 128>(p, st) : launch_reduce<__nv_bfloat16, 64>(p, st);
+}
 
 extern "C" size_t pa_decode_workspace_size(int num_seqs, int num_q_heads, int head_dim,
                                            int max_context_len, int partition_size) {
@@ -606,11 +624,12 @@ int context_cap(const pa_decode_args *a, int block_size) {
 
 }  // namespace
 
-extern "C" int pa_decode(void *out, const void *q, const void *k_cache, const void *v_cache,
-                         const int32_t *block_tables, const int32_t *context_lens, int num_q_heads,
-                         int num_kv_heads, int head_dim, int block_size, float scale,
-                         const pa_decode_args *a) {
-    PaTraceRange trace("pa_decode");
+namespace {
+
+// Both entry points below: window == 0 attends to every token.
+int decode_any(void *out, const void *q, const void *k_cache, const void *v_cache,
+               const int32_t *block_tables, const int32_t *context_lens, int num_q_heads, int num_kv_heads,
+               int head_dim, int block_size, float scale, int window, int num_sinks, const pa_decode_args *a) {
     if (!a) return pa_fail(PA_ERR_INVALID_ARG, "pa_decode: args is NULL");
     if (a->num_seqs < 0) return pa_fail(PA_ERR_INVALID_ARG, "pa_decode: num_seqs < 0");
     if (a->num_seqs == 0) return PA_OK;
@@ -620,10 +639,14 @@ extern "C" int pa_decode(void *out, const void *q, const void *k_cache, const vo
     const int P = effective_partition(a->partition_size);
     const long long total_rows = static_cast<long long>(a->num_blocks) * num_kv_heads * block_size;
     const int ctx_cap = context_cap(a, block_size);
-    const int max_parts = ctx_cap <= P ? 1 : static_cast<int>((static_cast<long long>(ctx_cap) + P - 1) / P);
+    // A window longer than any sequence, or sinks past its end, change nothing.
+    if (window > ctx_cap) window = ctx_cap > 0 ? ctx_cap : 1;
+    if (num_sinks > ctx_cap) num_sinks = ctx_cap;
+    const int walk_cap = seen_cap(ctx_cap, window, num_sinks, pa::kChunk);
+    const int max_parts = walk_cap <= P ? 1 : static_cast<int>((static_cast<long long>(walk_cap) + P - 1) / P);
     DecodeParams p{};
     if (max_parts > 1) {
-        const size_t need = pa_decode_workspace_size(a->num_seqs, num_q_heads, head_dim, ctx_cap, P);
+        const size_t need = pa_decode_workspace_size(a->num_seqs, num_q_heads, head_dim, walk_cap, P);
         if (!a->workspace || a->workspace_bytes < need || !aligned16(a->workspace))
             return pa_fail(PA_ERR_WORKSPACE, "pa_decode: workspace missing, unaligned or smaller than pa_decode_workspace_size()");
         const size_t rows = static_cast<size_t>(a->num_seqs) * max_parts * num_q_heads;
@@ -654,6 +677,10 @@ extern "C" int pa_decode(void *out, const void *q, const void *k_cache, const vo
     p.ctx_cap = ctx_cap;
     p.total_rows = static_cast<int>(total_rows);
     p.scale_log2 = scale * 1.4426950408889634f;
+    p.window = window;
+    p.num_sinks = num_sinks;
+    p.view_gran = pa::kChunk;
+    p.sink_end = pa::host::round_up_int(num_sinks, pa::kChunk);
     const bool use_mma = a->dtype == PA_BF16 && !a->simt;
     const int tile = use_mma ? 16 : 8;
     p.tile_rows = p.group < tile ? p.group : tile;
@@ -681,29 +708,51 @@ extern "C" int pa_decode(void *out, const void *q, const void *k_cache, const vo
             cudaMemsetAsync(p.work_ctr, 0, sizeof(unsigned long long), st) != cudaSuccess)
             return pa_fail(PA_ERR_CUDA, "pa_decode: cannot reset the work counter");
         if (use_mma) {
-            const bool rows16 = p.group > 8;
-            if (head_dim == 128)
-                rc = rows16 ? launch_bf16<128, true>(p, k_cache, v_cache, items, dev, st)
-                            : launch_bf16<128, false>(p, k_cache, v_cache, items, dev, st);
-            else
-                rc = rows16 ? launch_bf16<64, true>(p, k_cache, v_cache, items, dev, st)
-                            : launch_bf16<64, false>(p, k_cache, v_cache, items, dev, st);
+            rc = head_dim == 128 ? launch_bf16_any<128>(p, k_cache, v_cache, items, dev, st)
+                                 : launch_bf16_any<64>(p, k_cache, v_cache, items, dev, st);
         } else {
             rc = pa::launch_simt_pass(p, k_cache, v_cache, a->dtype == PA_F32, head_dim, items, dev, st);
         }
     }
     if (rc != PA_OK) return rc;
     if (max_parts > 1 && a->phase != PA_PHASE_PARTITIONS) {
-        cudaError_t le;
-        if (a->dtype == PA_BF16)
-            le = head_dim == 128 ? launch_reduce<__nv_bfloat16, 128>(p, st) : launch_reduce<__nv_bfloat16, 64>(p, st);
-        else
-            le = head_dim == 128 ? launch_reduce<float, 128>(p, st) : launch_reduce<float, 64>(p, st);
+        const cudaError_t le = pa::launch_merge(p, a->dtype == PA_F32, head_dim, st);
         if (le != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(le));
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
     return PA_OK;
+}
+
+}  // namespace
+
+extern "C" int pa_decode(void *out, const void *q, const void *k_cache, const void *v_cache,
+                         const int32_t *block_tables, const int32_t *context_lens, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, float scale,
+                         const pa_decode_args *a) {
+    PaTraceRange trace("pa_decode");
+    return decode_any(out, q, k_cache, v_cache, block_tables, context_lens, num_q_heads, num_kv_heads, head_dim,
+                      block_size, scale, 0, 0, a);
+}
+
+extern "C" size_t pa_decode_window_workspace_size(int num_seqs, int num_q_heads, int head_dim, int max_context_len,
+                                                  int partition_size, int window, int num_sinks) {
+    if (window <= 0 || num_sinks < 0) return 0;
+    return pa_decode_workspace_size(num_seqs, num_q_heads, head_dim, seen_cap(max_context_len, window, num_sinks, pa::kChunk),
+                                    partition_size);
+}
+
+extern "C" int pa_decode_window(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *block_tables, const int32_t *context_lens, int num_q_heads,
+                                int num_kv_heads, int head_dim, int block_size, float scale, int window,
+                                int num_sinks, const pa_decode_args *a) {
+    PaTraceRange trace("pa_decode_window");
+    if (window < 1 || num_sinks < 0)
+        return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_window: window must be at least 1 and num_sinks at least 0");
+    if (a && a->simt && a->dtype == PA_BF16)
+        return pa_fail(PA_ERR_UNSUPPORTED, "pa_decode_window: simt is not available with a window");
+    return decode_any(out, q, k_cache, v_cache, block_tables, context_lens, num_q_heads, num_kv_heads, head_dim,
+                      block_size, scale, window, num_sinks, a);
 }
 
 // ====================================================== no-alloc variant ===

@@ -30,6 +30,32 @@ __device__ __forceinline__ int seq_len(const DecodeParams &p, int s) {
 
 __device__ __forceinline__ int parts_of(int n, int P) { return n <= P ? 1 : (n + P - 1) / P; }
 
+// What a pass walks of a sequence: `seen` tokens on an axis of their own,
+// whose token v is position v, or v + skip from sink_end on.  Without a window
+// that is every token.  With one, the whole spans of view_gran tokens that lie
+// behind the window and past the sinks drop out; the few masked tokens of the
+// spans at its edges stay, and the passes mask them.
+struct SeqView {
+    int n, seen, skip;
+};
+
+template <bool WIN>
+__device__ __forceinline__ SeqView seq_view(const DecodeParams &p, int s) {
+    const int n = seq_len(p, s);
+    if (!WIN) return {n, n, 0};
+    const int behind = max(0, n - p.window);
+    const int skip = max(0, behind / p.view_gran * p.view_gran - p.sink_end);
+    return {n, n - skip, skip};
+}
+
+// Which of the 16 tokens from position pos on a windowed sequence of n tokens
+// attends to, among the first `valid`.
+__device__ __forceinline__ uint32_t window_mask(const DecodeParams &p, int n, int pos, int valid) {
+    const int behind = min(max(max(n - p.window, 0) - pos, 0), 16), sinks = min(max(p.num_sinks - pos, 0), 16);
+    const uint32_t below = (1u << sinks) - 1u, inside = ~((1u << behind) - 1u);
+    return (below | inside) & ((1u << min(max(valid, 0), 16)) - 1u);
+}
+
 // Position of the walk over (sequence, partition) pairs: `base` is the global
 // index of sequence `seq`'s first partition.
 struct SeqCursor {
@@ -39,10 +65,11 @@ struct SeqCursor {
 
 // Move the cursor forward to the sequence that owns global partition gp
 // (32 sequences per step, warp-parallel).  False when gp is past the end.
-static __device__ bool seek(SeqCursor &c, long long gp, const DecodeParams &p, int lane) {
+template <bool WIN>
+__device__ bool seek(SeqCursor &c, long long gp, const DecodeParams &p, int lane) {
     while (c.seq < p.num_seqs) {
         const int s = c.seq + lane;
-        const int np = s < p.num_seqs ? parts_of(seq_len(p, s), p.partition_size) : 0;
+        const int np = s < p.num_seqs ? parts_of(seq_view<WIN>(p, s).seen, p.partition_size) : 0;
         int incl = np;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -120,15 +147,17 @@ __device__ void merge_and_store(const uint8_t *smem, int warp_bytes, const Decod
 // Describes the item a CTA is working on.
 struct Item {
     int seq, part, kvh, ht, qh0, rows, n;
+    int seen, skip;       // see SeqView; tok_begin and tok_end count on its axis
     int tok_begin, tok_end, nchunks;
     bool single;
 };
 
+template <bool WIN = false>
 __device__ __forceinline__ bool next_item(Item &it, SeqCursor &cur, long long item,
                                           const DecodeParams &p, int tile_rows, int lane) {
     const int T = p.num_kv_heads * p.head_tiles;
     const long long gp = item / T;
-    if (!seek(cur, gp, p, lane)) return false;
+    if (!seek<WIN>(cur, gp, p, lane)) return false;
     const int r = static_cast<int>(item % T);
     const int ht = r % p.head_tiles;
     it.seq = cur.seq;
@@ -140,24 +169,32 @@ __device__ __forceinline__ bool next_item(Item &it, SeqCursor &cur, long long it
     const int raw = p.context_lens[it.seq];
     if (threadIdx.x == 0 && r == 0 && it.part == 0 && (raw < 0 || raw > p.ctx_cap))
         flag_status(p.status, PA_STATUS_BAD_CONTEXT_LEN);
-    const int n = seq_len(p, it.seq);
-    it.n = n;
+    const SeqView view = seq_view<WIN>(p, it.seq);
+    it.n = view.n;
+    it.seen = view.seen;
+    it.skip = view.skip;
     it.tok_begin = it.part * p.partition_size;
-    it.tok_end = min(n, it.tok_begin + p.partition_size);
+    it.tok_end = min(view.seen, it.tok_begin + p.partition_size);
     const int ntok = max(0, it.tok_end - it.tok_begin);
     it.nchunks = (ntok + kChunk - 1) / kChunk;
-    it.single = n <= p.partition_size;
+    it.single = view.seen <= p.partition_size;
     return true;
+}
+
+// Position in the sequence of token v of the item's axis.
+template <bool WIN>
+__device__ __forceinline__ int token_pos(const DecodeParams &p, const Item &it, int v) {
+    return WIN && v >= p.sink_end ? v + it.skip : v;
 }
 
 // Physical location of this warp's k-th chunk of the item, as a row of the
 // [num_blocks * Hkv * block_size, head_dim] view of a cache; an invalid block
 // id gives -1 and sets a flag (the passes then load rows past the view, which
 // TMA fills with zeros).
-template <int NW = kWarps>
+template <int NW = kWarps, bool WIN = false>
 __device__ __forceinline__ int chunk_row(const DecodeParams &p, const Item &it, int warp, int k) {
     const int c = warp + NW * k;
-    const int tok = it.tok_begin + c * kChunk;
+    const int tok = token_pos<WIN>(p, it, it.tok_begin + c * kChunk);
     const int phys = p.block_tables[(long long)it.seq * p.max_blocks_per_seq + tok / p.block_size];
     if (phys < 0 || phys >= p.num_blocks) {
         flag_status(p.status, PA_STATUS_BAD_BLOCK_ID);
@@ -179,7 +216,7 @@ struct NewToken {
 
 __device__ __forceinline__ NewToken new_token(const DecodeParams &p, const Item &it) {
     NewToken t{-1, 0, -1};
-    if (!p.k_new || it.n <= 0 || it.tok_end != it.n) return t;
+    if (!p.k_new || it.n <= 0 || it.tok_end != it.seen) return t;
     const int64_t slot = p.slot_mapping[it.seq];
     if (slot < 0) return t;
     const int pos = it.n - 1;
@@ -188,8 +225,8 @@ __device__ __forceinline__ NewToken new_token(const DecodeParams &p, const Item 
         if (threadIdx.x == 0 && it.kvh == 0 && it.ht == 0) flag_status(p.status, PA_STATUS_BAD_SLOT);
         return t;
     }
-    t.chunk = (pos - it.tok_begin) / kChunk;
-    t.row = (pos - it.tok_begin) % kChunk;
+    t.chunk = (it.seen - 1 - it.tok_begin) / kChunk;   // position n - 1 is the axis' last token
+    t.row = (it.seen - 1 - it.tok_begin) % kChunk;
     t.cache_row = ((long long)phys * p.num_kv_heads + it.kvh) * p.block_size + pos % p.block_size;
     return t;
 }
@@ -211,6 +248,9 @@ __device__ __forceinline__ void finish_handouts(unsigned long long *ctr) {
 // defined in pa_decode_simt.cu.  Enqueues one launch on `st`.
 int launch_simt_pass(const DecodeParams &p, const void *k_cache, const void *v_cache, bool f32, int head_dim,
                      long long items, int dev, cudaStream_t st);
+
+// The split-K merge of a pass's partials (pa_decode.cu).
+cudaError_t launch_merge(const DecodeParams &p, bool f32, int head_dim, cudaStream_t st);
 
 // ------------------------------------------------------- host helpers ---
 namespace host {
@@ -301,6 +341,29 @@ inline bool make_map(CUtensorMap *map, const void *base, long long rows, int hd,
                      box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
+}
+
+inline bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
+
+inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// Workspace layout: [work counter, 8 bytes, padded to 256] [partial (max, sum)]
+// [partial accumulators].  The counter sits at offset 0 whatever the sizes, so
+// a workspace reused for other sizes keeps a valid (zero) counter.
+constexpr size_t kWorkspaceHeader = 256;
+
+// n rounded up to a multiple of gran, or the largest one an int holds.
+inline int round_up_int(int n, int gran) {
+    const long long r = (static_cast<long long>(n) + gran - 1) / gran * gran;
+    return static_cast<int>(r < 0x7fffffffll ? r : 0x7fffffffll / gran * gran);
+}
+
+// Tokens a pass walks of a sequence of up to n tokens (SeqView's axis, in
+// spans of gran tokens), at most; window 0 is no window.
+inline int seen_cap(int n, int window, int num_sinks, int gran) {
+    if (window <= 0) return n;
+    const long long seen = (static_cast<long long>(num_sinks) + gran - 1) / gran * gran + window + gran - 1;
+    return static_cast<int>(seen < n ? seen : n);
 }
 
 // Launch a partition pass as a programmatic dependent of whatever kernel

@@ -120,7 +120,7 @@ struct SimtLayout {
     static constexpr int RSLOTS = (MAX_CHUNKS + 31) / 32;
 };
 
-template <typename T, int HD, int HT, int NW, int NSTAGE, int CPS>
+template <typename T, int HD, int HT, int NW, int NSTAGE, int CPS, bool WIN>
 __global__ void __launch_bounds__(NW * 32, CPS)
     decode_simt_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const DecodeParams p) {
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(NW * 32, CPS)
     int nb = 0;
     for (long long item = blockIdx.x;;) {
         Item it;
-        if (!next_item(it, cur, item, p, kSimtTile, lane)) break;
+        if (!next_item<WIN>(it, cur, item, p, kSimtTile, lane)) break;
         const int my_n = it.nchunks > warp ? (it.nchunks - warp + NW - 1) / NW : 0;
 
         // Rows of this warp's chunks: slot j of lane i holds chunk i + 32 j.
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(NW * 32, CPS)
         for (int j = 0; j < Lay::RSLOTS; ++j) {
             rows[j] = oob_row;
             if (lane + 32 * j < my_n) {
-                const int r = chunk_row<NW>(p, it, warp, lane + 32 * j);
+                const int r = chunk_row<NW, WIN>(p, it, warp, lane + 32 * j);
                 rows[j] = r < 0 ? oob_row : r;
             }
         }
@@ -252,6 +252,8 @@ __global__ void __launch_bounds__(NW * 32, CPS)
             const uint8_t *Vs = stage + PAGE_BYTES;
             const int c = warp + NW * k;
             const int valid = min(kChunk, it.tok_end - (it.tok_begin + c * kChunk));
+            uint32_t mask = 0xffffu;   // windowed: the chunk's tokens attended to
+            if constexpr (WIN) mask = window_mask(p, it.n, token_pos<WIN>(p, it, it.tok_begin + c * kChunk), valid);
             if (c == ntok.chunk) {
                 // Fused cache write: the new token's row goes into the staged
                 // tile (whatever the copy read) and, once per (sequence, KV
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(NW * 32, CPS)
             for (int h = 0; h < HT; ++h) {
                 const float part = sc2[h].x + sc2[h].y;
                 float x = part + __shfl_xor_sync(kFull, part, 16);
-                x = tok < valid ? x : -INFINITY;   // slots past the context may hold anything
+                x = (WIN ? (mask >> tok) & 1u : tok < valid) ? x : -INFINITY;   // masked slots may hold anything
                 float mx = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
@@ -366,11 +368,12 @@ __global__ void __launch_bounds__(NW * 32, CPS)
 #pragma unroll
                     for (int v = 0; v < VEC / 2; ++v) acc[h][v] = __ffma2_rn(pt[h], vv[v], acc[h][v]);
             };
-            if (valid == kChunk) {
+            if (WIN ? mask == 0xffffu : valid == kChunk) {
 #pragma unroll
                 for (int i = 0; i < kChunk / TS; ++i) pv_token(ts + i * TS);
             } else {
-                for (int t = ts; t < valid; t += TS) pv_token(t);
+                for (int t = ts; t < valid; t += TS)
+                    if (!WIN || ((mask >> t) & 1u)) pv_token(t);
             }
             __syncwarp();   // p_s and this stage are free again
             if (k + NSTAGE < my_n) issue(k + NSTAGE);
@@ -432,13 +435,13 @@ __global__ void __launch_bounds__(NW * 32, CPS)
     }
 }
 
-template <typename T, int HD, int HT>
+template <typename T, int HD, int HT, bool WIN>
 int launch_one(const DecodeParams &p, const void *k_cache, const void *v_cache, long long items, int dev,
                cudaStream_t st) {
     using S = SimtShape<T, HD>;
     using Lay = SimtLayout<T, HD, HT, S::NW, S::NSTAGE>;
     static host::KernelSlot slot;
-    auto kernel = decode_simt_kernel<T, HD, HT, S::NW, S::NSTAGE, S::CPS>;
+    auto kernel = decode_simt_kernel<T, HD, HT, S::NW, S::NSTAGE, S::CPS, WIN>;
     const int occ = host::ensure_kernel(kernel, slot, Lay::SMEM, dev, S::NW * 32);
     if (occ == 0) return pa_fail(PA_ERR_CUDA, "pa_decode: cannot configure the fp32-FMA kernel");
     CUtensorMap mk, mv;
@@ -452,13 +455,13 @@ int launch_one(const DecodeParams &p, const void *k_cache, const void *v_cache, 
     return PA_OK;
 }
 
-template <typename T, int HD>
+template <typename T, int HD, bool WIN>
 int launch_tile(const DecodeParams &p, const void *k_cache, const void *v_cache, long long items, int dev,
                 cudaStream_t st) {
-    if (p.tile_rows <= 1) return launch_one<T, HD, 1>(p, k_cache, v_cache, items, dev, st);
-    if (p.tile_rows <= 2) return launch_one<T, HD, 2>(p, k_cache, v_cache, items, dev, st);
-    if (p.tile_rows <= 4) return launch_one<T, HD, 4>(p, k_cache, v_cache, items, dev, st);
-    return launch_one<T, HD, 8>(p, k_cache, v_cache, items, dev, st);
+    if (p.tile_rows <= 1) return launch_one<T, HD, 1, WIN>(p, k_cache, v_cache, items, dev, st);
+    if (p.tile_rows <= 2) return launch_one<T, HD, 2, WIN>(p, k_cache, v_cache, items, dev, st);
+    if (p.tile_rows <= 4) return launch_one<T, HD, 4, WIN>(p, k_cache, v_cache, items, dev, st);
+    return launch_one<T, HD, 8, WIN>(p, k_cache, v_cache, items, dev, st);
 }
 
 }  // namespace
@@ -467,11 +470,16 @@ int launch_simt_pass(const DecodeParams &p, const void *k_cache, const void *v_c
                      long long items, int dev, cudaStream_t st) {
     if (p.tile_rows < 1 || p.tile_rows > kSimtTile)
         return pa_fail(PA_ERR_INVALID_ARG, "pa_decode: head tile out of range for the fp32-FMA kernel");
+    if (p.window) {   // bf16 with a window always runs on the tensor cores
+        if (!f32) return pa_fail(PA_ERR_UNSUPPORTED, "pa_decode: the fp32-FMA pass takes no window with bf16");
+        return head_dim == 128 ? launch_tile<float, 128, true>(p, k_cache, v_cache, items, dev, st)
+                               : launch_tile<float, 64, true>(p, k_cache, v_cache, items, dev, st);
+    }
     if (f32)
-        return head_dim == 128 ? launch_tile<float, 128>(p, k_cache, v_cache, items, dev, st)
-                               : launch_tile<float, 64>(p, k_cache, v_cache, items, dev, st);
-    return head_dim == 128 ? launch_tile<__nv_bfloat16, 128>(p, k_cache, v_cache, items, dev, st)
-                           : launch_tile<__nv_bfloat16, 64>(p, k_cache, v_cache, items, dev, st);
+        return head_dim == 128 ? launch_tile<float, 128, false>(p, k_cache, v_cache, items, dev, st)
+                               : launch_tile<float, 64, false>(p, k_cache, v_cache, items, dev, st);
+    return head_dim == 128 ? launch_tile<__nv_bfloat16, 128, false>(p, k_cache, v_cache, items, dev, st)
+                           : launch_tile<__nv_bfloat16, 64, false>(p, k_cache, v_cache, items, dev, st);
 }
 
 }  // namespace pa

@@ -53,6 +53,10 @@ struct DecodeParams {
     int total_rows;        // num_blocks * num_kv_heads * block_size (TMA row extent)
     int reduce_newest_first;   // merge pass walks sequences last to first
     float scale_log2;      // scale * log2(e)
+    // Sliding window (0: none): a sequence of n tokens attends to positions
+    // >= n - window and < num_sinks.  Whole view_gran-token spans between the
+    // two are left out of the work; sink_end is num_sinks rounded up to them.
+    int window, num_sinks, sink_end, view_gran;
 };
 
 // ------------------------------------------------------------------ PTX ---

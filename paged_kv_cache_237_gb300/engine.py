@@ -23,12 +23,21 @@ class DecodeStep:
     The workspace is zeroed once here, so the calls skip the per-call reset of
     its work counter (every completed call leaves the counter zero).  Steps
     that run one after another on one stream may share a workspace and a
-    status word: pass them in."""
+    status word: pass them in.
+
+    With ``window`` (and ``num_sinks``) the step attends to each sequence's
+    last ``window`` tokens and its first ``num_sinks`` (``pa_decode_window``)."""
 
     def __init__(self, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
                  max_context_len: int, partition_size: int = 0, simt: bool = False,
-                 workspace: torch.Tensor | None = None, status: binding.DeviceStatus | None = None):
+                 workspace: torch.Tensor | None = None, status: binding.DeviceStatus | None = None,
+                 window: int = 0, num_sinks: int = 0):
+        if window < 0 or num_sinks < 0 or (num_sinks and not window):
+            raise ValueError("window and num_sinks must not be negative, and num_sinks needs a window")
+        if window and simt:
+            raise ValueError("simt is not available with a window")
+        self.window, self.num_sinks = window, num_sinks
         self.q, self.k_cache, self.v_cache = q, k_cache, v_cache
         self.block_tables, self.context_lens = block_tables, context_lens
         self.scale = scale
@@ -37,22 +46,37 @@ class DecodeStep:
         self.simt = simt
         self.out = torch.empty_like(q)
         S, Hq, hd = q.shape
-        ws = binding.pa_decode_workspace_size(S, Hq, hd, max_context_len, partition_size)
-        if workspace is not None and workspace.numel() < ws:
-            raise ValueError(f"workspace has {workspace.numel()} bytes, {ws} needed")
-        if workspace is None and ws:
-            workspace = torch.zeros(ws, dtype=torch.uint8, device=q.device)
-        self.workspace = workspace if ws else None
+        if window:
+            ws = binding.pa_decode_window_workspace_size(S, Hq, hd, max_context_len, partition_size, window=window,
+                                                         num_sinks=num_sinks)
+        else:
+            ws = binding.pa_decode_workspace_size(S, Hq, hd, max_context_len, partition_size)
+        self.workspace = _own_workspace(workspace, ws, q.device)
         self.status = status if status is not None else binding.DeviceStatus(q.device)
+        self._plain = None      # the windowed call without a fused write, checked once
 
     def decode(self, stream=None, phase: int = binding.PA_PHASE_ALL, k_new=None, v_new=None,
                slot_mapping=None) -> torch.Tensor:
+        if self.window:
+            return self._decode_window(stream, phase, k_new, v_new, slot_mapping)
         return binding.pa_decode(self.out, self.q, self.k_cache, self.v_cache, self.block_tables,
                                  self.context_lens, self.scale, max_context_len=self.max_context_len,
                                  partition_size=self.partition_size, workspace=self.workspace,
                                  status=self.status, stream=stream, phase=phase, k_new=k_new,
                                  v_new=v_new, slot_mapping=slot_mapping, simt=self.simt,
                                  skip_counter_reset=True)
+
+    def _decode_window(self, stream, phase, k_new, v_new, slot_mapping) -> torch.Tensor:
+        fused = k_new is not None or v_new is not None or slot_mapping is not None
+        call = None if fused else self._plain
+        if call is None:
+            call = binding._decode_call(self.out, self.q, self.k_cache, self.v_cache, self.block_tables,
+                                        self.context_lens, self.scale, self.max_context_len, self.partition_size,
+                                        self.workspace, self.status, phase, k_new, v_new, slot_mapping, False, True,
+                                        self.window, self.num_sinks)
+            if not fused:
+                self._plain = call
+        return call(stream, phase)
 
     def run_fused(self, k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
                   cow_pairs: torch.Tensor | None = None, stream=None,
@@ -70,6 +94,61 @@ class DecodeStep:
         if slot_mapping.numel():
             binding.pa_reshape_and_cache(k_new, v_new, self.k_cache, self.v_cache, slot_mapping,
                                          status=self.status, stream=stream)
+
+    def run(self, k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
+            cow_pairs: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        self.write_tokens(k_new, v_new, slot_mapping, cow_pairs, stream)
+        return self.decode(stream)
+
+
+def _own_workspace(workspace: torch.Tensor | None, need: int, device) -> torch.Tensor | None:
+    """The workspace a step keeps: the one given (checked), a zeroed one, or None when it needs none."""
+    if workspace is not None and workspace.numel() < need:
+        raise ValueError(f"workspace has {workspace.numel()} bytes, {need} needed")
+    if workspace is None and need:
+        workspace = torch.zeros(need, dtype=torch.uint8, device=device)
+    return workspace if need else None
+
+
+class Q4DecodeStep:
+    """``DecodeStep`` over a 4-bit cache: holds the output, workspace and
+    status word of a repeated step, and its call, checked once.  The tensors
+    given are the step's for its life (update them in place).
+
+    k_cache, v_cache are uint8 [num_blocks, Hkv, page_bytes]; q may be bf16 or
+    fp32.  ``window`` 0 attends to every token."""
+
+    def __init__(self, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, max_context_len: int,
+                 partition_size: int = 0, group_size: int = 64, window: int = 0, num_sinks: int = 0,
+                 workspace: torch.Tensor | None = None, status: binding.DeviceStatus | None = None):
+        self.q, self.k_cache, self.v_cache = q, k_cache, v_cache
+        self.block_tables, self.context_lens = block_tables, context_lens
+        self.group_size = group_size
+        self.out = torch.empty_like(q)
+        self.status = status if status is not None else binding.DeviceStatus(q.device)
+        S, Hq, hd = q.shape
+        _, Hkv, self.block_size = binding._q4_geometry(k_cache, v_cache, hd, group_size, q.device)
+        ws = binding.pa_decode_q4_workspace_size(S, Hq, Hkv, hd, max_context_len, partition_size, window=window,
+                                                 num_sinks=num_sinks)
+        self.workspace = _own_workspace(workspace, ws, q.device)
+        self._call = binding._decode_q4_call(self.out, q, k_cache, v_cache, block_tables, context_lens, scale,
+                                             max_context_len, group_size, window, num_sinks, partition_size,
+                                             self.workspace, self.status, binding.PA_PHASE_ALL, True)
+
+    def decode(self, stream=None, phase: int = binding.PA_PHASE_ALL) -> torch.Tensor:
+        return self._call(stream, phase)
+
+    def write_tokens(self, k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
+                     cow_pairs: torch.Tensor | None = None, stream=None) -> None:
+        """The step's cache updates: copy-on-write copies, then the new rows, quantised."""
+        if cow_pairs is not None and cow_pairs.numel():
+            binding.pa_copy_blocks(binding.q4_block_rows(self.k_cache, self.block_size),
+                                   binding.q4_block_rows(self.v_cache, self.block_size), cow_pairs,
+                                   status=self.status, stream=stream)
+        if slot_mapping.numel():
+            binding.pa_reshape_and_cache_q4(k_new, v_new, self.k_cache, self.v_cache, slot_mapping,
+                                            group_size=self.group_size, status=self.status, stream=stream)
 
     def run(self, k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
             cow_pairs: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -121,4 +200,4 @@ def prefix_share_state(device="cuda", seed: int | None = None) -> dict:
     )
 
 
-__all__ = ["DecodeStep", "prefix_share_state", "WORKLOADS"]
+__all__ = ["DecodeStep", "Q4DecodeStep", "prefix_share_state", "WORKLOADS"]
