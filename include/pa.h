@@ -465,7 +465,7 @@ int pa_gather_q4(void *k, void *v, const void *k_cache, const void *v_cache, con
  * the cache holds.  args->dtype is the type of q and out; products and sums
  * are in fp32 or more.  A block id out of range reads as zeros (flagged).
  * args->partition_size is 0 (the library picks) or a multiple of 32 in
- * [32, 4096]; args->simt must be 0 and k_new, v_new and slot_mapping NULL
+ * [32, 1024]; args->simt must be 0 and k_new, v_new and slot_mapping NULL
  * (PA_ERR_UNSUPPORTED): pa_reshape_and_cache_q4 writes the step's tokens. */
 int pa_decode_q4(void *out, const void *q, const void *k_cache, const void *v_cache,
                  const int32_t *block_tables, const int32_t *context_lens, int num_q_heads, int num_kv_heads,

@@ -4,8 +4,12 @@
 // For a query row q and a token t with codes c, steps s_g and minima m_g:
 //   q . K_t = sum_g s_g (sum_{d in g} q_d c_d) + m_g (sum_{d in g} q_d)
 //   o_d     = sum_t p_t (s_g c_td + m_g)
-// Work items, hand-out, the merge of the warps' states and the split-K merge
-// are those of the other passes (pa_decode_common.cuh).
+// Work.  A row is one (sequence, KV head, head tile); laid end to end, the
+// batch's rows are one axis of units of 32 tokens, and every warp takes an equal
+// stretch of it, so that all finish together whatever the lengths.  A warp
+// stores the rows that lie in its stretch whole, and one partial for a row that
+// its stretch's beginning or end cuts; a second launch joins those.  No barrier
+// and no counter: warps do not meet.
 //
 // The products run on fp16 tensor-core MMAs with tokens as rows of both: S = K
 // Q^T has K's codes as its A operand, O^T = V^T W has V's.  With tokens as
@@ -28,6 +32,19 @@
 
 #include "pa_decode_common.cuh"
 #include "pa_q4.cuh"
+
+#ifndef PA_Q4_CPS
+#define PA_Q4_CPS 3
+#endif
+#ifndef PA_Q4_MINP
+#define PA_Q4_MINP 128
+#endif
+#ifndef PA_Q4_WARPS
+#define PA_Q4_WARPS 4
+#endif
+#ifndef PA_Q4_NST
+#define PA_Q4_NST 2
+#endif
 
 namespace pa {
 namespace {
@@ -52,6 +69,34 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t u) {
     return __half22float2(h);
 }
 
+// 2^x to about 2^-22, results below the normals flushed to zero: a weight that
+// small adds nothing to a sum that holds one of 2^-8 or more.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A token's steps and minima; NORMAL codes carry 16 steps more than the value.
+template <int NG, bool NORMAL>
+__device__ __forceinline__ void load_pairs(const uint8_t *at, float (&s)[NG], float (&m)[NG]) {
+    uint32_t pair[NG];
+    if constexpr (NG == 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(at);
+        pair[0] = x.x, pair[1] = x.y, pair[2] = x.z, pair[3] = x.w;
+    } else if constexpr (NG == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(at);
+        pair[0] = x.x, pair[1] = x.y;
+    } else {
+        pair[0] = *reinterpret_cast<const uint32_t *>(at);
+    }
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+        s[i] = q4_step(pair[i]);
+        m[i] = NORMAL ? fmaf(-16.f, s[i], q4_min(pair[i])) : q4_min(pair[i]);
+    }
+}
+
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // The two nibble pairs (a nibble of each half-word) at a time that make the
@@ -73,6 +118,21 @@ __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&r)[4]) {
     }
 }
 
+// The same for V, whose products can be untangled in the output: not NORMAL,
+// values 1 and 3 come as whole bytes, lower code * 2^-24 + code * 2^-20, which
+// saves an and each.
+template <bool NORMAL>
+__device__ __forceinline__ void codes_or_bytes_f16(uint32_t x, uint32_t (&r)[4]) {
+    if constexpr (NORMAL) {
+        codes_f16<true>(x, r);
+    } else {
+        r[1] = x & 0x00ff00ffu;
+        r[0] = x & 0x000f000fu;
+        r[3] = __byte_perm(x, 0u, 0x4341);
+        r[2] = r[3] & 0x000f000fu;
+    }
+}
+
 // The smallest power of two above x >= 0, within [2^-100, 2^120].
 __device__ __forceinline__ float pow2_above(float x) {
     const float c = fminf(fmaxf(x, 0x1p-101f), 0x1p119f);
@@ -83,17 +143,51 @@ __device__ __forceinline__ float pow2_above(float x) {
 // built for.
 template <int HD, int NT>
 struct Q4Shape {
-    static constexpr int NSTAGE = HD == 128 ? 2 : 3;
-    static constexpr int CPS = NT == 2 ? 2 : 3;
+    static constexpr int NSTAGE = HD == 128 ? PA_Q4_NST : PA_Q4_NST + 1;
+    static constexpr int CPS = NT == 2 ? 8 / PA_Q4_WARPS : PA_Q4_CPS;
 };
 
+constexpr int kQ4Warps = PA_Q4_WARPS;   // per CTA; they are independent
 constexpr int kUnit = 32;   // tokens per stage: one block of 32 or two of 16
+
+// Where a warp stands on the axis, kept in shared memory.
+struct Walk {
+    uint32_t pos, begin, end;    // next place, and the warp's stretch
+    uint32_t base, places;       // first place of sequence seq, places of each of its rows
+    int seq, n, seen, skip, begins;
+};
+
+// Up to 32 units of one row, kept in shared memory.
+struct Block {
+    int seq, qh0, rows, n, skip, tok_begin, tok_end;
+    int first, last;             // of the row's units in this stretch
+    int begins, whole;           // the stretch holds the row's beginning; the whole row
+};
+
+// The split-K state of a call, in its workspace.
+struct Q4Split {
+    uint32_t *share;             // places per warp
+    uint32_t *bases;             // [S] first place of each sequence
+    float *ml, *acc;             // [warps][2][rows][2] and [..][HD]: a row that the stretch
+                                 // does not begin (0) or does not end (1)
+};
+
+__device__ __forceinline__ uint32_t row_units(int seen) { return seen > kUnit ? (seen + kUnit - 1) / kUnit : 1; }
+
+// A row takes kRowCost more places on the axis than it has units, before them:
+// what beginning and ending a row costs a warp, in units.
+#ifndef PA_Q4_ROWCOST
+#define PA_Q4_ROWCOST 3
+#endif
+constexpr uint32_t kRowCost = PA_Q4_ROWCOST;
+__device__ __forceinline__ uint32_t row_places(int seen) { return row_units(seen) + kRowCost; }
 
 // T: type of q and out.  fp32 splits q and the weights into two fp16 parts.
 // NT: tiles of 8 query heads per work item.
 template <typename T, int HD, int G, int NT>
-__global__ void __launch_bounds__(kWarps * 32, Q4Shape<HD, NT>::CPS)
-    decode_q4_kernel(const uint8_t *__restrict__ k_cache, const uint8_t *__restrict__ v_cache, const DecodeParams p) {
+__global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
+    decode_q4_kernel(const uint8_t *__restrict__ k_cache, const uint8_t *__restrict__ v_cache, const DecodeParams p,
+                     const Q4Split split, uint32_t warps, uint32_t min_share) {
     using F = Q4Format<HD, G>;
     constexpr bool SPLIT = sizeof(T) == 4;
     constexpr int PARTS = SPLIT ? 2 : 1;
@@ -103,17 +197,15 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<HD, NT>::CPS)
     constexpr int STAGE_BYTES = 2 * HALF_BYTES;
     constexpr int WARP_BYTES = NSTAGE * STAGE_BYTES;
     constexpr int ROWS = 8 * NT;
-    constexpr int LD = HD + kEpiPad;
     constexpr int OW = HD / 32;    // code words a lane feeds to one token row's products
     constexpr int MT = HD / 16;    // m-tiles of the output
-    static_assert(WARP_BYTES >= (ROWS * LD + 2 * ROWS) * 4, "epilogue tile must fit in a warp's stages");
 
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     uint8_t *wbuf = smem + warp * WARP_BYTES;
     const uint32_t wbuf_s = smem_addr(wbuf);
-    const uint32_t bar_s = smem_addr(smem + kWarps * WARP_BYTES) + warp * NSTAGE * 8;
+    const uint32_t bar_s = smem_addr(smem + kQ4Warps * WARP_BYTES) + warp * NSTAGE * 8;
     if (lane == 0) {
         for (int s = 0; s < NSTAGE; ++s) mbar_init(bar_s + 8 * s, 1);
         fence_mbar_init();
@@ -121,7 +213,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<HD, NT>::CPS)
     __syncwarp();
 
     // Where the 16-token halves of a stage begin: two pages, or one of 32 rows.
-    const int bs = p.block_size;
+    const int bs = p.block_size, bs_shift = bs == 32 ? 5 : 4;
     const int page_bytes = bs * F::ROW_BYTES;
     const int code_half = bs == 16 ? page_bytes : 16 * F::CODE_BYTES;
     const int par_0 = bs * F::CODE_BYTES, par_half = bs == 16 ? page_bytes : 16 * F::PARAM_BYTES;
@@ -133,68 +225,173 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<HD, NT>::CPS)
 
     uint32_t n_issued = 0, n_done = 0;
     bool failed = false;
-    SeqCursor cur{0, 0};
     const uint64_t kv_policy = l2_evict_first_policy();
-    griddep_wait();   // everything above touched only this CTA's registers and shared memory
+    griddep_wait();   // everything above touched only this warp's registers and shared memory
 
-    __shared__ long long s_next[2];
-    const bool dynamic = p.work_ctr != nullptr;
-    long long ahead = 0;
-    if (dynamic && threadIdx.x == 0) ahead = gridDim.x + next_handout(p.work_ctr);
-    int nb = 0;
-    for (long long item = blockIdx.x;;) {
-        Item it;
-        if (!next_item<true>(it, cur, item, p, ROWS, lane)) break;
-        const int units = (it.tok_end - it.tok_begin + kUnit - 1) / kUnit;
-        const int my_n = units > warp ? (units - warp + kWarps - 1) / kWarps : 0;   // at most 32
-
-        // Pages of this warp's units: lane k holds unit k's first and (block
-        // size 16) second, as block * heads + head; -1 is a block id out of
-        // range, -2 a page past the item's tokens.
-        long long page_a = -2, page_b = -2;
-        auto page_of = [&](int v) -> long long {
-            if (v >= it.tok_end) return -2;
-            const int phys = p.block_tables[(long long)it.seq * p.max_blocks_per_seq + token_pos<true>(p, it, v) / bs];
+    // The warp's stretch.  Without a split (every row is short) it counts rows.
+    const bool cut = split.share != nullptr;
+    const uint32_t heads = p.num_kv_heads * p.head_tiles;
+    __shared__ Walk s_walk[kQ4Warps];
+    __shared__ Block s_blocks[kQ4Warps][2];
+    Walk &walk = s_walk[warp];
+    {
+        const uint32_t me = blockIdx.x * kQ4Warps + warp;   // those past `warps` get nothing
+        uint32_t total = p.num_seqs;
+        if (cut) {
+            total = 0;
+            for (int s = lane; s < p.num_seqs; s += 32) total += row_places(seq_view<true>(p, s).seen);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) total += __shfl_xor_sync(kFull, total, o);
+        }
+        total *= heads;
+        const uint32_t share = max((total + warps - 1) / warps, cut ? min_share : 1u);
+        const uint32_t begin = min(total, me * share), end = min(total, begin + share);
+        if (cut && me == 0 && lane == 0) *split.share = share;
+        // The sequence that holds place `begin`, 32 lengths at a time.
+        int seq = cut ? 0 : static_cast<int>(begin / heads);
+        uint32_t base = cut ? 0 : seq * heads;
+        while (cut && seq < p.num_seqs) {
+            const int s = seq + lane;
+            const uint32_t u = s < p.num_seqs ? row_places(seq_view<true>(p, s).seen) * heads : 0u;
+            uint32_t incl = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(kFull, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const unsigned hit = __ballot_sync(kFull, begin < base + incl);
+            if (hit) {
+                const int at = __ffs(hit) - 1;
+                base += __shfl_sync(kFull, incl - u, at);
+                seq += at;
+                break;
+            }
+            base += __shfl_sync(kFull, incl, 31);
+            seq += 32;
+        }
+        if (lane == 0) {
+            const SeqView view = begin < end ? seq_view<true>(p, seq) : SeqView{0, 0, 0};
+            walk = Walk{begin, begin, end, base, cut ? row_places(view.seen) : 1u, seq, view.n, view.seen, view.skip, 0};
+        }
+        __syncwarp();
+    }
+    // Takes up the next block of the stretch: its description into shared
+    // memory, its pages into page_a and page_b (lane k holds unit k's first and,
+    // with block size 16, second, as block * heads + head; -1 is a block id out
+    // of range, -2 a page past the block's tokens).  Returns its units, at most
+    // 32; -1 past the last.
+    auto read_block = [&](Block &to, int &page_a, int &page_b) {
+        page_a = page_b = -2;
+        uint32_t pos = walk.pos;
+        const uint32_t stretch_end = walk.end;
+        if (pos >= stretch_end) return -1;
+        int seq = walk.seq;
+        uint32_t base = walk.base, rp = walk.places;
+        SeqView view{walk.n, walk.seen, walk.skip};
+        while (pos >= base + rp * heads) {
+            base += rp * heads;
+            view = seq_view<true>(p, ++seq);
+            if (cut) rp = row_places(view.seen);
+        }
+        const uint32_t in_seq = pos - base, h = in_seq / rp, at = in_seq - h * rp;
+        uint32_t u = 0, left = 1;      // the row's next unit, and how many follow in this stretch
+        if (cut) {
+            const uint32_t skipped = at < kRowCost ? kRowCost - at : 0u;
+            u = at + skipped - kRowCost;
+            pos += skipped;
+            if (pos >= stretch_end) return -1;   // the row's units are all the next stretch's
+            left = min(rp - at - skipped, stretch_end - pos);
+        }
+        const int units = cut ? static_cast<int>(min(left, 32u)) : static_cast<int>(row_units(view.seen));
+        const bool first = u == 0 || pos == walk.begin, last = !cut || units == static_cast<int>(left);
+        const bool begins = first ? u == 0 : walk.begins != 0;
+        const int kvh = h / p.head_tiles, ht = h - kvh * p.head_tiles;
+        const int begin = static_cast<int>(u) * kUnit, end = min(view.seen, begin + units * kUnit);
+        __syncwarp();   // the slot's last readers, and the walk's, are done
+        if (lane == 0) {
+            to = Block{seq, kvh * p.group + ht * ROWS, min(ROWS, p.group - ht * ROWS), view.n, view.skip, begin, end,
+                       first, last, begins, begins && (!cut || u + units + kRowCost == rp)};
+            walk.pos = pos + (cut ? units : 1);
+            walk.base = base;
+            walk.places = rp;
+            walk.seq = seq;
+            walk.n = view.n;
+            walk.seen = view.seen;
+            walk.skip = view.skip;
+            walk.begins = begins;
+            if (h == 0 && u == 0) {
+                if (cut) split.bases[seq] = base;
+                const int raw = p.context_lens[seq];
+                if (raw < 0 || raw > p.ctx_cap) flag_status(p.status, PA_STATUS_BAD_CONTEXT_LEN);
+            }
+        }
+        __syncwarp();
+        auto page_of = [&](int v) {
+            if (v >= end) return -2;
+            const int pos = v >= p.sink_end ? v + view.skip : v;
+            const int phys = p.block_tables[(long long)seq * p.max_blocks_per_seq + (pos >> bs_shift)];
             if (phys < 0 || phys >= p.num_blocks) {
                 flag_status(p.status, PA_STATUS_BAD_BLOCK_ID);
                 return -1;
             }
-            return (long long)phys * p.num_kv_heads + it.kvh;
+            return phys * p.num_kv_heads + kvh;
         };
-        if (lane < my_n) {
-            const int v = it.tok_begin + (warp + kWarps * lane) * kUnit;
-            page_a = page_of(v);
-            if (bs == 16) page_b = page_of(v + 16);
-        }
-        auto issue = [&](int k) {
-            const long long a = __shfl_sync(kFull, page_a, k), b = __shfl_sync(kFull, page_b, k);
-            if (failed) return;
-            if (lane == 0) {
-                const int s = n_issued % NSTAGE;
-                const uint32_t dst = wbuf_s + s * STAGE_BYTES, bar = bar_s + 8 * s;
-                fence_proxy_async_smem();
-                mbar_arrive_expect_tx(bar, ((a >= 0) + (b >= 0)) * 2 * page_bytes);
-                if (a >= 0) {
-                    bulk_load_hint(dst, k_cache + a * page_bytes, page_bytes, bar, kv_policy);
-                    bulk_load_hint(dst + HALF_BYTES, v_cache + a * page_bytes, page_bytes, bar, kv_policy);
-                }
-                if (b >= 0) {
-                    bulk_load_hint(dst + page_bytes, k_cache + b * page_bytes, page_bytes, bar, kv_policy);
-                    bulk_load_hint(dst + HALF_BYTES + page_bytes, v_cache + b * page_bytes, page_bytes, bar, kv_policy);
-                }
+        const int v = begin + lane * kUnit;
+        page_a = page_of(v);
+        if (bs == 16) page_b = page_of(v + 16);
+        return units;
+    };
+    auto issue = [&](int page_a, int page_b, int k) {
+        const int a = __shfl_sync(kFull, page_a, k), b = __shfl_sync(kFull, page_b, k);
+        if (lane == 0) {
+            const int s = n_issued % NSTAGE;
+            const uint32_t dst = wbuf_s + s * STAGE_BYTES, bar = bar_s + 8 * s;
+            fence_proxy_async_smem();
+            mbar_arrive_expect_tx(bar, ((a >= 0) + (b >= 0)) * 2 * page_bytes);
+            if (a >= 0) {
+                const long long at = (long long)a * page_bytes;
+                bulk_load_hint(dst, k_cache + at, page_bytes, bar, kv_policy);
+                bulk_load_hint(dst + HALF_BYTES, v_cache + at, page_bytes, bar, kv_policy);
             }
-            ++n_issued;
-        };
-        const int pro = my_n < NSTAGE ? my_n : NSTAGE;
-        for (int k = 0; k < pro; ++k) issue(k);
+            if (b >= 0) {
+                const long long at = (long long)b * page_bytes;
+                bulk_load_hint(dst + page_bytes, k_cache + at, page_bytes, bar, kv_policy);
+                bulk_load_hint(dst + HALF_BYTES + page_bytes, v_cache + at, page_bytes, bar, kv_policy);
+            }
+        }
+        ++n_issued;
+    };
+
+    // A row's state, carried from block to block.
+    uint32_t qf[PARTS][NT][OW][4];
+    float qs[NT][2];            // per column (head): undoes q's scaling, times scale * log2(e)
+    // Sums of q over a group, times scale * log2(e): by column and group, or
+    // (bf16) group t's of head g as the coefficient of m in a B operand whose
+    // A operand is a row's (s, m) pairs as they are, in two bf16 parts.
+    float qsum[SPLIT ? NT : 1][2][NG];
+    uint32_t qm[NT][2];
+    float o[MT][NT][4];         // [row g or g + 8][column]: sums of w * code, see below
+    float om[NT][2][NG];        // this lane's tokens' sum of p * m
+    float ref[NT][2], l[NT][2];
+    float S[NG], inv[NG];       // w = p * s * inv, inv = 4 / S
+
+    int slot = 0, page_a, page_b, next_a, next_b;
+    int units = read_block(s_blocks[warp][0], page_a, page_b);
+    int asked = 0, asked_next = 0;        // units of the two blocks that have been issued
+    while (units >= 0 && !failed) {
+        const Block &it = s_blocks[warp][slot];
+        for (; asked < units && n_issued - n_done < NSTAGE; ++asked) issue(page_a, page_b, asked);
+        const int next_units = read_block(s_blocks[warp][slot ^ 1], next_a, next_b);
+        const bool some_bad = __any_sync(kFull, page_a == -1 || page_b == -1);
+        // Tokens from all_from to all_to are not masked.
+        const int all_from = max(0, it.n - p.window) - it.skip, all_to = it.tok_end, tok_begin = it.tok_begin;
+        const bool first = it.first;
+        if (first) {
 
         // q as B operands: lane (g, t) holds head g of each tile, the units of
         // its code words, divided by a power of two that brings the row's
         // largest magnitude into [2^14, 2^15) (exact for bf16: 8 bits of an
         // fp16's 11), and by 16 where a code comes out 16 times too large.
-        uint32_t qf[PARTS][NT][OW][4];
-        float qs[NT][2];            // per column (head): undoes the scaling, times scale * log2(e)
-        float qsum[NT][2][NG];      // sum of q over a group, times scale * log2(e)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int head = 8 * nt + g;
@@ -241,22 +438,29 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<HD, NT>::CPS)
             }
             // To the columns of the accumulators: heads 2 t and 2 t + 1.
             const float back = p.scale_log2 * (SPLIT ? 1.f : 0x1p24f) * pow2i(e);
+            float own = 0.f;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                sum[i] *= p.scale_log2;
+                if (t == i) own = sum[i];
+            }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 qs[nt][c] = __shfl_sync(kFull, back, 4 * (2 * t + c));
+                if constexpr (SPLIT)
 #pragma unroll
-                for (int i = 0; i < NG; ++i) qsum[nt][c][i] = __shfl_sync(kFull, sum[i] * p.scale_log2, 4 * (2 * t + c));
+                    for (int i = 0; i < NG; ++i) qsum[nt][c][i] = __shfl_sync(kFull, sum[i], 4 * (2 * t + c));
             }
+            // two bf16 parts (16 bits), each over a zero that meets the step
+            qm[nt][0] = __float_as_uint(own) & 0xffff0000u;
+            qm[nt][1] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(own - __uint_as_float(qm[nt][0]))))
+                        << 16;
         }
 
-        float o[MT][NT][4];          // [row g or g + 8][column]: sums of w * code, see below
-        float om[NT][2][NG];         // this lane's tokens' sum of p * m
-        float ref[NT][2], l[NT][2];
-        float S[NG], inv[NG];        // w = p * s * inv, inv = 2^7 / S
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-            S[i] = 0x1p-100f;
-            inv[i] = 0x1p107f;
+            S[i] = 1.f;
+            inv[i] = 4.f;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -264,213 +468,253 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<HD, NT>::CPS)
             for (int mt = 0; mt < MT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                ref[nt][c] = -0x1p126f;
+                ref[nt][c] = 0.f;
                 l[nt][c] = 0.f;
 #pragma unroll
                 for (int i = 0; i < NG; ++i) om[nt][c][i] = 0.f;
             }
         }
 
-        for (int k = 0; k < my_n; ++k) {
+        }   // first
+
+        for (int k = 0; k < units; ++k) {
             const int s = n_done % NSTAGE;
-            bool ok = !failed && mbar_wait_bounded(bar_s + 8 * s, (n_done / NSTAGE) & 1u);
+            bool ok = mbar_wait_bounded(bar_s + 8 * s, (n_done / NSTAGE) & 1u);
             if (__any_sync(kFull, !ok)) {
-                if (!failed && lane == 0) flag_status(p.status, PA_STATUS_WAIT_TIMEOUT);
+                if (lane == 0) flag_status(p.status, PA_STATUS_WAIT_TIMEOUT);
                 failed = true;
                 break;
             }
             ++n_done;
             uint8_t *stage = wbuf + s * STAGE_BYTES;
-            const int v0 = it.tok_begin + (warp + kWarps * k) * kUnit;
-            {
-                // A block id out of range reads as zeros.
-                const bool bad_a = __shfl_sync(kFull, page_a, k) == -1, bad_b = __shfl_sync(kFull, page_b, k) == -1;
-                if (bad_a || bad_b) {
-                    for (int i = lane * 4; i < page_bytes; i += 128)
-                        for (int h = 0; h < 2; ++h) {
-                            if (bad_a) *reinterpret_cast<uint32_t *>(stage + h * HALF_BYTES + i) = 0u;
-                            if (bad_b) *reinterpret_cast<uint32_t *>(stage + h * HALF_BYTES + page_bytes + i) = 0u;
+            const int v0 = tok_begin + k * kUnit;
+            float bias[2][2] = {{0.f, 0.f}, {0.f, 0.f}};   // of this lane's tokens' scores: -inf where masked
+            if (some_bad || v0 < all_from || v0 + kUnit > all_to) {
+                // A block id out of range reads as zeros, and a masked token's
+                // parameters become zeros (its codes are finite whatever they are).
+                const bool bad[2] = {__shfl_sync(kFull, page_a, k) == -1, __shfl_sync(kFull, page_b, k) == -1};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (bad[half])
+                        for (int i = lane * 4; i < page_bytes; i += 128) {
+                            *reinterpret_cast<uint32_t *>(stage + half * page_bytes + i) = 0u;
+                            *reinterpret_cast<uint32_t *>(stage + HALF_BYTES + half * page_bytes + i) = 0u;
                         }
-                    fence_proxy_async_smem();
-                    __syncwarp();
+                    const int v = v0 + 16 * half;
+                    const uint32_t mask = window_mask(p, it.n, v >= p.sink_end ? v + it.skip : v, it.tok_end - v);
+                    for (int i = lane; i < 16 * NG; i += 32)
+                        if (!((mask >> (i / NG)) & 1u)) {
+                            uint8_t *at = stage + par_0 + half * par_half + 4 * i;
+                            *reinterpret_cast<uint32_t *>(at) = 0u;
+                            *reinterpret_cast<uint32_t *>(at + HALF_BYTES) = 0u;
+                        }
+                    bias[half][0] = (mask >> row_g) & 1u ? 0.f : -INFINITY;
+                    bias[half][1] = (mask >> (row_g + 8)) & 1u ? 0.f : -INFINITY;
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
             }
+
+            // ---- S = K Q^T: rows are tokens, columns heads; one accumulator per group.
+            float sc[2][NT][4];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int v = v0 + 16 * half;
-                if (v >= it.tok_end) break;
-                const uint32_t mask = window_mask(p, it.n, token_pos<true>(p, it, v), it.tok_end - v);
-                if (!mask) continue;
                 const uint8_t *Kc = stage + half * code_half, *Kp = stage + par_0 + half * par_half;
-                const uint8_t *Vc = Kc + HALF_BYTES, *Vp = Kp + HALF_BYTES;
-                const bool seen0 = (mask >> row_g) & 1u, seen1 = (mask >> (row_g + 8)) & 1u;
-
-                // ---- S = K Q^T: rows are tokens, columns heads; one accumulator per group.
                 float acc[NT][NG][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < NG; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
-                {
-                    uint32_t w0[OW], w1[OW];   // the lane's words of rows g and g + 8
-                    const uint8_t *r0 = Kc + row_g * F::CODE_BYTES + t * 4 * OW, *r1 = r0 + 8 * F::CODE_BYTES;
-                    if constexpr (OW == 4) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(r0), y = *reinterpret_cast<const uint4 *>(r1);
-                        w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
-                        w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
-                    } else {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(r0), y = *reinterpret_cast<const uint2 *>(r1);
-                        w0[0] = x.x, w0[1] = x.y;
-                        w1[0] = y.x, w1[1] = y.y;
-                    }
-#pragma unroll
-                    for (int j = 0; j < OW; ++j) {
-                        uint32_t x, y;
-                        if constexpr (G == 64) {
-                            const int i = W * (j & 1) + j / 2;   // word (2 t + (j & 1), j / 2)
-                            x = w0[i];
-                            y = w1[i];
-                        } else {
-                            // halves of words (2 t, j / 2) and (2 t + 1, j / 2): one group each
-                            x = __byte_perm(w0[j / 2], w0[W + j / 2], j & 1 ? 0x7632 : 0x5410);
-                            y = __byte_perm(w1[j / 2], w1[W + j / 2], j & 1 ? 0x7632 : 0x5410);
-                        }
-                        uint32_t xr[4], yr[4];
-                        codes_f16<SPLIT>(x, xr);
-                        codes_f16<SPLIT>(y, yr);
-                        const uint32_t a0[4] = {xr[0], yr[0], xr[1], yr[1]}, a1[4] = {xr[2], yr[2], xr[3], yr[3]};
-                        const int i = G == 64 ? j / 2 : j;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int q = 0; q < PARTS; ++q) {
-                                mma_f16_16816(acc[nt][i], a0, qf[q][nt][j][0], qf[q][nt][j][1]);
-                                mma_f16_16816(acc[nt][i], a1, qf[q][nt][j][2], qf[q][nt][j][3]);
-                            }
-                    }
+                uint32_t w0[OW], w1[OW];   // the lane's words of rows g and g + 8
+                const uint8_t *r0 = Kc + row_g * F::CODE_BYTES + t * 4 * OW, *r1 = r0 + 8 * F::CODE_BYTES;
+                if constexpr (OW == 4) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(r0), y = *reinterpret_cast<const uint4 *>(r1);
+                    w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
+                    w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(r0), y = *reinterpret_cast<const uint2 *>(r1);
+                    w0[0] = x.x, w0[1] = x.y;
+                    w1[0] = y.x, w1[1] = y.y;
                 }
-
-                float sc[NT][4];
-                {
-                    uint32_t kp[2][NG];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint32_t *pp = reinterpret_cast<const uint32_t *>(Kp + (row_g + 8 * r) * F::PARAM_BYTES);
-#pragma unroll
-                        for (int i = 0; i < NG; ++i) kp[r][i] = pp[i];
+                for (int j = 0; j < OW; ++j) {
+                    uint32_t x, y;
+                    if constexpr (G == 64) {
+                        const int i = W * (j & 1) + j / 2;   // word (2 t + (j & 1), j / 2)
+                        x = w0[i];
+                        y = w1[i];
+                    } else {
+                        // halves of words (2 t, j / 2) and (2 t + 1, j / 2): one group each
+                        x = __byte_perm(w0[j / 2], w0[W + j / 2], j & 1 ? 0x7632 : 0x5410);
+                        y = __byte_perm(w1[j / 2], w1[W + j / 2], j & 1 ? 0x7632 : 0x5410);
                     }
+                    uint32_t xr[4], yr[4];
+                    codes_f16<SPLIT>(x, xr);
+                    codes_f16<SPLIT>(y, yr);
+                    const uint32_t a0[4] = {xr[0], yr[0], xr[1], yr[1]}, a1[4] = {xr[2], yr[2], xr[3], yr[3]};
+                    const int i = G == 64 ? j / 2 : j;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int r = c >> 1, col = c & 1;
-                            float x = 0.f, y = 0.f;
-#pragma unroll
-                            for (int i = 0; i < NG; ++i) {
-                                x = fmaf(q4_step(kp[r][i]), acc[nt][i][c], x);
-                                y = fmaf(SPLIT ? fmaf(-16.f, q4_step(kp[r][i]), q4_min(kp[r][i])) : q4_min(kp[r][i]),
-                                         qsum[nt][col][i], y);
-                            }
-                            sc[nt][c] = (r ? seen1 : seen0) ? fmaf(x, qs[nt][col], y) : -INFINITY;
+                        for (int q = 0; q < PARTS; ++q) {
+                            mma_f16_16816(acc[nt][i], a0, qf[q][nt][j][0], qf[q][nt][j][1]);
+                            mma_f16_16816(acc[nt][i], a1, qf[q][nt][j][2], qf[q][nt][j][3]);
                         }
                 }
-
-                // ---- weights.  w = p s / S in fp16 carries the value's step, so
-                // that the codes enter the second product as they are.
-                float sv[2][NG], mv[2][NG];
+                // sc: the scores less their references
+                float y[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) y[nt][c] = bias[half][c >> 1] - ref[nt][c & 1];
+                if constexpr (!SPLIT) {
+                    const uint8_t *at = Kp + row_g * F::PARAM_BYTES + 4 * (t & (NG - 1));
+                    const uint32_t a0 = *reinterpret_cast<const uint32_t *>(at);
+                    const uint32_t a1 = *reinterpret_cast<const uint32_t *>(at + 8 * F::PARAM_BYTES);
+                    const uint32_t a[4] = {a0, a1, a0, a1};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(y[nt], a, qm[nt][0], qm[nt][1]);
+                }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint32_t *pp = reinterpret_cast<const uint32_t *>(Vp + (row_g + 8 * r) * F::PARAM_BYTES);
+                    float ks[NG], km[NG];
+                    load_pairs<NG, SPLIT>(Kp + (row_g + 8 * r) * F::PARAM_BYTES, ks, km);
 #pragma unroll
-                    for (int i = 0; i < NG; ++i) {
-                        const uint32_t pair = (r ? seen1 : seen0) ? pp[i] : 0u;
-                        sv[r][i] = q4_step(pair);
-                        mv[r][i] = SPLIT ? fmaf(-16.f, sv[r][i], q4_min(pair)) : q4_min(pair);
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int col = 0; col < 2; ++col) {
+                            const int c = 2 * r + col;
+                            float x = ks[0] * acc[nt][0][c];
+                            if constexpr (SPLIT) y[nt][c] = fmaf(km[0], qsum[nt][col][0], y[nt][c]);
+#pragma unroll
+                            for (int i = 1; i < NG; ++i) {
+                                x = fmaf(ks[i], acc[nt][i][c], x);
+                                if constexpr (SPLIT) y[nt][c] = fmaf(km[i], qsum[nt][col][i], y[nt][c]);
+                            }
+                            sc[half][nt][c] = fmaf(x, qs[nt][col], y[nt][c]);
+                        }
                 }
-                float pr[NT][4], w[NT][NG][4], most = 0.f;
-                bool far = false;
+            }
+
+            // ---- weights.  w = p s inv in fp16 (inv = 4 / S, S a power of two)
+            // carries the value's step, so that the codes enter the second product
+            // as they are.  What would pass fp16's range is seen by sums, which the
+            // FMA pipe has room for: while this lane's p sum to at most 2^5 a head and
+            // its s inv to at most 2^10, no w passes 2^15.
+            float pr[2][NT][4];
+            float sum[NT][2], most = 0.f, wide = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) sum[nt][0] = sum[nt][1] = 0.f;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint8_t *Vp = stage + HALF_BYTES + par_0 + half * par_half;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float sv[NG], mv[NG];
+                    load_pairs<NG, SPLIT>(Vp + (row_g + 8 * r) * F::PARAM_BYTES, sv, mv);
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) wide = fmaf(sv[i], inv[i], wide);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const float x = sc[nt][c] - ref[nt][c & 1];
-                        far |= x > 8.f;
-                        pr[nt][c] = exp2f(x);
+                        pr[half][nt][c] = ex2(sc[half][nt][c]);
+                        sum[nt][c & 1] += pr[half][nt][c];
+                    }
+            }
 #pragma unroll
-                        for (int i = 0; i < NG; ++i) {
-                            w[nt][i][c] = pr[nt][c] * (sv[c >> 1][i] * inv[i]);
-                            most = fmaxf(most, w[nt][i][c]);
+            for (int nt = 0; nt < NT; ++nt) most = fmaxf(most, fmaxf(sum[nt][0], sum[nt][1]));   // passes NaN over
+            const bool fresh = first && k == 0;
+            if (fresh || __any_sync(kFull, most > 32.f || wide > 1024.f)) {
+                // Raise the references to the running maxima (a row's first unit
+                // sets them), choose S anew above every p s and a sixteenth of every
+                // s, and take p again.  Rare after the first unit.
+                float alpha[NT][2], rise[NT][2], keep = 0.f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float mx = fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][c + 2]), fmaxf(sc[1][nt][c], sc[1][nt][c + 2]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
+                        // by how much; a column of NaN alone stays where it is
+                        rise[nt][c] = !fresh ? fmaxf(mx, 0.f) : mx == -INFINITY ? 0.f : mx;
+                        alpha[nt][c] = !fresh ? ex2(-rise[nt][c]) : 0.f;
+                        ref[nt][c] += rise[nt][c];
+                        l[nt][c] *= alpha[nt][c];
+                        keep = fmaxf(keep, alpha[nt][c]);
+#pragma unroll
+                        for (int i = 0; i < NG; ++i) om[nt][c][i] *= alpha[nt][c];
+                    }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    sum[nt][0] = sum[nt][1] = 0.f;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            pr[half][nt][c] = ex2(sc[half][nt][c] - rise[nt][c & 1]);
+                            sum[nt][c & 1] += pr[half][nt][c];
                         }
-                    }
-                if (__any_sync(kFull, far || most > 32768.f)) {
-                    // A score 8 above its reference, or a weight past fp16's
-                    // range: raise the references to the running maxima and
-                    // choose S anew.  Rare after a sequence's first tokens.
-                    float alpha[NT][2], keep = 0.f;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float mx = fmaxf(sc[nt][c], sc[nt][c + 2]);
-#pragma unroll
-                            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
-                            const float now = fmaxf(ref[nt][c], mx);
-                            alpha[nt][c] = exp2f(ref[nt][c] - now);
-                            ref[nt][c] = now;
-                            l[nt][c] *= alpha[nt][c];
-                            keep = fmaxf(keep, alpha[nt][c]);
-#pragma unroll
-                            for (int i = 0; i < NG; ++i) om[nt][c][i] *= alpha[nt][c];
-                        }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) pr[nt][c] = exp2f(sc[nt][c] - ref[nt][c & 1]);
-                    float ratio[NG];
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) {
-                        float mx = 0.f;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) mx = fmaxf(mx, pr[nt][c] * sv[c >> 1][i]);
-                        mx = fmaxf(mx, keep * S[i]);
-#pragma unroll
-                        for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
-                        const float now = pow2_above(mx);
-                        ratio[i] = S[i] / now;
-                        S[i] = now;
-                        inv[i] = 0x1p7f / now;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) w[nt][i][c] = pr[nt][c] * (sv[c >> 1][i] * inv[i]);
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const float r = ratio[G == 64 ? mt / 4 : mt / 2];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) o[mt][nt][c] *= alpha[nt][c & 1] * r;
-                    }
                 }
+                float top[NG];
+#pragma unroll
+                for (int i = 0; i < NG; ++i) top[i] = keep * S[i];
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float sv[NG], mv[NG], most_p = 0.0625f;
+                        load_pairs<NG, SPLIT>(stage + HALF_BYTES + par_0 + half * par_half +
+                                                  (row_g + 8 * r) * F::PARAM_BYTES, sv, mv);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            most_p = fmaxf(most_p, fmaxf(pr[half][nt][2 * r], pr[half][nt][2 * r + 1]));
+#pragma unroll
+                        for (int i = 0; i < NG; ++i) top[i] = fmaxf(top[i], most_p * sv[i]);
+                    }
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    float mx = top[i];
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
+                    const float now = pow2_above(mx), ratio = S[i] / now;
+                    S[i] = now;
+                    inv[i] = 4.f / now;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+                        if ((G == 64 ? mt / 4 : mt / 2) == i)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) o[mt][nt][c] *= alpha[nt][c & 1] * ratio;
+                }
+            }
+
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
                 uint32_t pb[PARTS][NT][NG][2];
+                float sv[2][NG], mv[2][NG];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    load_pairs<NG, SPLIT>(stage + HALF_BYTES + par_0 + half * par_half +
+                                              (row_g + 8 * r) * F::PARAM_BYTES, sv[r], mv[r]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        l[nt][c] += pr[nt][c] + pr[nt][c + 2];
+                        if (half == 0) l[nt][c] += sum[nt][c];
 #pragma unroll
                         for (int i = 0; i < NG; ++i)
-                            om[nt][c][i] = fmaf(pr[nt][c], mv[0][i], fmaf(pr[nt][c + 2], mv[1][i], om[nt][c][i]));
+                            om[nt][c][i] = fmaf(pr[half][nt][c], mv[0][i], fmaf(pr[half][nt][c + 2], mv[1][i], om[nt][c][i]));
                     }
 #pragma unroll
                     for (int i = 0; i < NG; ++i)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const float x = w[nt][i][2 * r], y = w[nt][i][2 * r + 1];
+                            const float sw = sv[r][i] * inv[i];
+                            const float x = pr[half][nt][2 * r] * sw, y = pr[half][nt][2 * r + 1] * sw;
                             const uint32_t h = pack_f16(x, y);
                             pb[0][nt][i][r] = movmatrix_trans(h);
                             if constexpr (SPLIT) {
@@ -481,88 +725,97 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<HD, NT>::CPS)
                 }
 
                 // ---- O += V^T W: rows are values, k is the tokens.
-                {
-                    const uint8_t *va = Vc + g * 4 * W;
-                    uint32_t x[4][W];   // tokens of matrix rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+                const uint8_t *va = stage + HALF_BYTES + half * code_half + g * 4 * W;
+                uint32_t x[4][W];   // tokens of matrix rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int tok = (i & 1 ? tok_b : tok_a) + (i & 2 ? 8 : 0);
-                        const uint8_t *at = va + tok * F::CODE_BYTES;
-                        if constexpr (W == 2) {
-                            const uint2 v = *reinterpret_cast<const uint2 *>(at);
-                            x[i][0] = v.x, x[i][1] = v.y;
-                        } else {
-                            x[i][0] = *reinterpret_cast<const uint32_t *>(at);
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = (i & 1 ? tok_b : tok_a) + (i & 2 ? 8 : 0);
+                    const uint8_t *at = va + tok * F::CODE_BYTES;
+                    if constexpr (W == 2) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(at);
+                        x[i][0] = v.x, x[i][1] = v.y;
+                    } else {
+                        x[i][0] = *reinterpret_cast<const uint32_t *>(at);
+                    }
+                }
+#pragma unroll
+                for (int wd = 0; wd < W; ++wd)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t sel = hf ? 0x7632 : 0x5410;
+                        uint32_t y[4], z[4];
+                        codes_or_bytes_f16<SPLIT>(__byte_perm(x[0][wd], x[1][wd], sel), y);
+                        codes_or_bytes_f16<SPLIT>(__byte_perm(x[2][wd], x[3][wd], sel), z);
+                        const int i = G == 64 ? wd : 2 * wd + hf;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t a[4] = {y[2 * e], y[2 * e + 1], z[2 * e], z[2 * e + 1]};
+                            const int mt = 4 * wd + 2 * hf + e;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int q = 0; q < PARTS; ++q)
+                                    mma_f16_16816(o[mt][nt], a, pb[q][nt][i][0], pb[q][nt][i][1]);
                         }
                     }
-#pragma unroll
-                    for (int wd = 0; wd < W; ++wd)
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const uint32_t sel = hf ? 0x7632 : 0x5410;
-                            uint32_t y[4], z[4];
-                            codes_f16<SPLIT>(__byte_perm(x[0][wd], x[1][wd], sel), y);
-                            codes_f16<SPLIT>(__byte_perm(x[2][wd], x[3][wd], sel), z);
-                            const int i = G == 64 ? wd : 2 * wd + hf;
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t a[4] = {y[2 * e], y[2 * e + 1], z[2 * e], z[2 * e + 1]};
-                                const int mt = 4 * wd + 2 * hf + e;
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                    for (int q = 0; q < PARTS; ++q)
-                                        mma_f16_16816(o[mt][nt], a, pb[q][nt][i][0], pb[q][nt][i][1]);
-                            }
-                        }
-                }
             }
             __syncwarp();
-            if (k + NSTAGE < my_n) issue(k + NSTAGE);
+            if (asked < units)
+                issue(page_a, page_b, asked++);
+            else if (asked_next < next_units)
+                issue(next_a, next_b, asked_next++);
         }
 
-        // Epilogue: undo the scalings, add the minima's part, publish this
-        // warp's state in its (now idle) stages.
-        __syncwarp();
-        {
-            float *eo = reinterpret_cast<float *>(wbuf);
+        // Undo the scalings, add the minima's part, and store: the final rows,
+        // or the row's partial.
+        if (it.last) {
+        const bool whole = it.whole;
+        const long long out0 = (long long)it.seq * p.num_q_heads + it.qh0;
+        const long long part0 = ((blockIdx.x * kQ4Warps + warp) * 2ll + it.begins) * ROWS;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) {
-                        l[nt][c] += __shfl_xor_sync(kFull, l[nt][c], d);
+                for (int d = 4; d < 32; d <<= 1) {
+                    l[nt][c] += __shfl_xor_sync(kFull, l[nt][c], d);
 #pragma unroll
-                        for (int i = 0; i < NG; ++i) om[nt][c][i] += __shfl_xor_sync(kFull, om[nt][c][i], d);
-                    }
-                    const int head = 8 * nt + 2 * t + c;
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const int u = 16 * (mt / 4) + 8 * (mt / 2 % 2) + g;
-                        const int i = G == 64 ? mt / 4 : mt / 2;
-                        const float even = fmaf(o[mt][nt][c] * (SPLIT ? 0x1p-7f : 0x1p17f), S[i], om[nt][c][i]);
-                        const float odd = fmaf(o[mt][nt][c + 2] * (SPLIT ? 0x1p-7f : 0x1p13f), S[i], om[nt][c][i]);
-                        *reinterpret_cast<float2 *>(eo + head * LD + 4 * u + 2 * (mt & 1)) = make_float2(even, odd);
-                    }
-                    if (g == 0) {
-                        eo[ROWS * LD + head] = ref[nt][c];
-                        eo[ROWS * LD + ROWS + head] = l[nt][c];
-                    }
+                    for (int i = 0; i < NG; ++i) om[nt][c][i] += __shfl_xor_sync(kFull, om[nt][c][i], d);
                 }
-        }
-        if (threadIdx.x == 0) s_next[nb] = dynamic ? ahead : item + gridDim.x;
-        __syncthreads();
-        merge_and_store<T, HD, kWarps, ROWS>(smem, WARP_BYTES, p, it.seq, it.part, it.qh0, it.rows, it.single);
-        fence_proxy_async_smem();
-        __syncthreads();
-        item = s_next[nb];
-        nb ^= 1;
-        if (dynamic && threadIdx.x == 0) ahead = gridDim.x + next_handout(p.work_ctr);
+                const int head = 8 * nt + 2 * t + c;
+                if (head >= it.rows) continue;
+                // a row without a token has l = 0 and zero sums; NaN stays NaN
+                const float norm = !whole ? 1.f : l[nt][c] == 0.f ? 0.f : 1.f / l[nt][c];
+#pragma unroll
+                for (int m2 = 0; m2 < MT / 2; ++m2) {   // a unit of four values: m-tiles 2 m2 and 2 m2 + 1
+                    const int u = 16 * (m2 / 2) + 8 * (m2 % 2) + g;
+                    const int i = G == 64 ? m2 / 2 : m2;
+                    float y[4];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float *acc = o[2 * m2 + e][nt];
+                        y[2 * e] = fmaf(acc[c] * (SPLIT ? 0x1p-2f : 0x1p22f), S[i], om[nt][c][i]) * norm;
+                        const float odd = SPLIT ? acc[c + 2] * 0x1p-2f : (acc[c + 2] - acc[c]) * 0x1p18f;
+                        y[2 * e + 1] = fmaf(odd, S[i], om[nt][c][i]) * norm;
+                    }
+                    const float4 v = make_float4(y[0], y[1], y[2], y[3]);
+                    if (whole)
+                        store4(static_cast<T *>(p.out) + (out0 + head) * HD + 4 * u, v);
+                    else
+                        store4(split.acc + (part0 + head) * HD + 4 * u, v);
+                }
+                if (!whole && g == 0)
+                    *reinterpret_cast<float2 *>(split.ml + (part0 + head) * 2) = make_float2(ref[nt][c], l[nt][c]);
+            }
+        }   // last
+        slot ^= 1;
+        units = next_units;
+        page_a = next_a;
+        page_b = next_b;
+        asked = asked_next;
+        asked_next = 0;
     }
     griddep_launch_dependents();
-    if (dynamic && threadIdx.x == 0) finish_handouts(p.work_ctr);
-
     // A wait gave up: let copies still in flight land before the CTA exits.
     if (failed && lane == 0) {
         for (uint32_t gi = n_done; gi < n_issued; ++gi)
@@ -570,47 +823,145 @@ __global__ void __launch_bounds__(kWarps * 32, Q4Shape<HD, NT>::CPS)
     }
 }
 
+// Joins the partials of every row that stretches cut: one warp per (sequence,
+// query head).  out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
+constexpr int kJoinWarps = 4;
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_q4_kernel(const DecodeParams p, const Q4Split split, int rows) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const long long me = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    const int seq = static_cast<int>(me / p.num_q_heads), qh = static_cast<int>(me - (long long)seq * p.num_q_heads);
+    if (seq >= p.num_seqs) return;
+    const uint32_t share = *split.share, ru = row_units(seq_view<true>(p, seq).seen);
+    const int kvh = qh / p.group, in_group = qh - kvh * p.group, ht = in_group / rows, r = in_group - ht * rows;
+    const uint32_t begin = split.bases[seq] + (kvh * p.head_tiles + ht) * (ru + kRowCost) + kRowCost;
+    const uint32_t w0 = begin / share, w1 = (begin + ru - 1) / share;
+    if (w0 == w1) return;   // stored whole
+    const int parts = static_cast<int>(w1 - w0) + 1;
+    // the stretch that begins the row keeps it in its second slot, the others in their first
+    auto at = [&](int i) { return ((long long)(w0 + i) * 2 + (i == 0)) * rows + r; };
+    float M = -INFINITY, L = 0.f;
+    for (int i = lane; i < parts; i += 32) M = fmaxf(M, split.ml[at(i) * 2]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    constexpr int E = HD / 32;   // values per lane
+    float acc[E] = {};
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        float f = 0.f;
+        if (i0 + lane < parts) {
+            const float2 ml = *reinterpret_cast<const float2 *>(split.ml + at(i0 + lane) * 2);
+            f = exp2f(ml.x - M);
+            L = fmaf(f, ml.y, L);
+        }
+        const int n = min(32, parts - i0);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float w = __shfl_sync(kFull, f, i);
+            const float *a = split.acc + at(i0 + i) * HD + lane * E;
+            if constexpr (E == 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(a);
+                acc[0] = fmaf(w, v.x, acc[0]);
+                acc[1] = fmaf(w, v.y, acc[1]);
+                acc[E - 2] = fmaf(w, v.z, acc[E - 2]);
+                acc[E - 1] = fmaf(w, v.w, acc[E - 1]);
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(a);
+                acc[0] = fmaf(w, v.x, acc[0]);
+                acc[1] = fmaf(w, v.y, acc[1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(kFull, L, o);
+    const float norm = L == 0.f ? 0.f : 1.f / L;
+    T *to = static_cast<T *>(p.out) + me * HD + lane * E;
+    if constexpr (E == 4) {
+        store4(to, make_float4(acc[0] * norm, acc[1] * norm, acc[E - 2] * norm, acc[E - 1] * norm));
+    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float2 *>(to) = make_float2(acc[0] * norm, acc[1] * norm);
+    } else {
+        *reinterpret_cast<__nv_bfloat162 *>(to) = __floats2bfloat162_rn(acc[0] * norm, acc[1] * norm);
+    }
+}
+
 using namespace host;
 
+// Warps of the partition pass at most: the stretches that a workspace has room
+// for (152 SMs x 16).
+constexpr long long kMaxStretches = 2432;
+
+// Stretches of a call, at most: rows of up to walk_cap tokens, cut no finer
+// than P tokens.  1 or less: nothing is cut.
+long long stretches(int num_seqs, long long heads, int walk_cap, int P) {
+    if (walk_cap <= P) return 0;
+    const long long units = static_cast<long long>(num_seqs) * heads * ((walk_cap + static_cast<long long>(kUnit) - 1) / kUnit);
+    const long long n = (units + P / kUnit - 1) / (P / kUnit);
+    return n < kMaxStretches ? n : kMaxStretches;
+}
+
+struct Q4Launch {
+    const void *k_cache, *v_cache;
+    Q4Split split;
+    long long stretches;   // 0: rows are not cut
+    int min_share, dev, phase;
+    cudaStream_t stream;
+};
+
 template <typename T, int HD, int G, int NT>
-int launch_one(const DecodeParams &p, const void *k_cache, const void *v_cache, long long items, int dev,
-               cudaStream_t st) {
-    constexpr int NS = Q4Shape<HD, NT>::NSTAGE;
-    constexpr int SMEM = kWarps * NS * (2 * kUnit * Q4Format<HD, G>::ROW_BYTES + 8);
-    static KernelSlot slot;
-    auto kernel = decode_q4_kernel<T, HD, G, NT>;
-    const int occ = ensure_kernel(kernel, slot, SMEM, dev);
-    if (occ == 0) return pa_fail(PA_ERR_CUDA, "pa_decode_q4: cannot configure the kernel");
-    const long long cap = static_cast<long long>(sm_count(dev)) * occ;
-    const cudaError_t e = launch_dependent(kernel, static_cast<int>(items < cap ? items : cap), kWarps * 32, SMEM, st,
-                                           static_cast<const uint8_t *>(k_cache),
-                                           static_cast<const uint8_t *>(v_cache), p);
-    return e == cudaSuccess ? PA_OK : pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
+int launch_one(const DecodeParams &p, const Q4Launch &c) {
+    if (c.phase != PA_PHASE_REDUCE) {
+        constexpr int NS = Q4Shape<HD, NT>::NSTAGE;
+        constexpr int SMEM = kQ4Warps * NS * (2 * kUnit * Q4Format<HD, G>::ROW_BYTES + 8);
+        static KernelSlot slot;
+        auto kernel = decode_q4_kernel<T, HD, G, NT>;
+        const int occ = ensure_kernel(kernel, slot, SMEM, c.dev, kQ4Warps * 32);
+        if (occ == 0) return pa_fail(PA_ERR_CUDA, "pa_decode_q4: cannot configure the kernel");
+        const long long rows = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.head_tiles;
+        long long warps = static_cast<long long>(sm_count(c.dev)) * occ * kQ4Warps;
+        if (warps > kMaxStretches) warps = kMaxStretches;
+        const long long most = c.stretches ? c.stretches : rows;
+        if (warps > most) warps = most;
+        const cudaError_t e = launch_dependent(kernel, static_cast<int>((warps + kQ4Warps - 1) / kQ4Warps),
+                                               kQ4Warps * 32, SMEM, c.stream, static_cast<const uint8_t *>(c.k_cache),
+                                               static_cast<const uint8_t *>(c.v_cache), p, c.split, static_cast<uint32_t>(warps),
+                                               static_cast<uint32_t>(c.min_share));
+        if (e != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
+    }
+    if (c.stretches && c.phase != PA_PHASE_PARTITIONS) {
+        const long long ctas = (static_cast<long long>(p.num_seqs) * p.num_q_heads + kJoinWarps - 1) / kJoinWarps;
+        const cudaError_t e = launch_dependent(join_q4_kernel<T, HD>, static_cast<int>(ctas), kJoinWarps * 32, 0,
+                                               c.stream, p, c.split, 8 * NT);
+        if (e != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
+    }
+    return PA_OK;
 }
 
 template <typename T, int HD, int G>
-int launch_tile(const DecodeParams &p, const void *k, const void *v, long long items, int dev, cudaStream_t st) {
-    return p.group > 8 ? launch_one<T, HD, G, 2>(p, k, v, items, dev, st)
-                       : launch_one<T, HD, G, 1>(p, k, v, items, dev, st);
+int launch_tile(const DecodeParams &p, const Q4Launch &c) {
+    return p.group > 8 ? launch_one<T, HD, G, 2>(p, c) : launch_one<T, HD, G, 1>(p, c);
 }
 
 template <typename T>
-int launch_any(const DecodeParams &p, const void *k, const void *v, int head_dim, int group_size, long long items,
-               int dev, cudaStream_t st) {
-    if (head_dim == 128)
-        return group_size == 64 ? launch_tile<T, 128, 64>(p, k, v, items, dev, st)
-                                : launch_tile<T, 128, 32>(p, k, v, items, dev, st);
-    return group_size == 64 ? launch_tile<T, 64, 64>(p, k, v, items, dev, st)
-                            : launch_tile<T, 64, 32>(p, k, v, items, dev, st);
+int launch_any(const DecodeParams &p, const Q4Launch &c, int head_dim, int group_size) {
+    if (head_dim == 128) return group_size == 64 ? launch_tile<T, 128, 64>(p, c) : launch_tile<T, 128, 32>(p, c);
+    return group_size == 64 ? launch_tile<T, 64, 64>(p, c) : launch_tile<T, 64, 32>(p, c);
 }
 
-int q4_partition(int partition_size) { return partition_size == 0 ? 512 : partition_size; }
+int q4_partition(int partition_size) { return partition_size == 0 ? PA_Q4_MINP : partition_size; }
 
-size_t workspace_bytes(int num_seqs, int num_q_heads, int head_dim, int walk_cap, int P, size_t *acc_at) {
-    const long long max_parts = (static_cast<long long>(walk_cap) + P - 1) / P;
-    if (max_parts <= 1) return 0;
-    const size_t rows = static_cast<size_t>(num_seqs) * max_parts * num_q_heads;
-    *acc_at = kWorkspaceHeader + align256(rows * 2 * sizeof(float));
+// Query heads per row: a tile of 8, or two for larger groups.
+int q4_tile(int group) { return group > 8 ? 16 : 8; }
+
+// Workspace: [header: the units per warp at byte 16] [first unit of each
+// sequence] [(max, sum)] [accumulators], two rows of heads per stretch.
+size_t workspace_bytes(int num_seqs, int tile, int head_dim, long long n, size_t *ml_at, size_t *acc_at) {
+    if (n == 0) return 0;
+    const size_t rows = static_cast<size_t>(n) * 2 * tile;
+    *ml_at = kWorkspaceHeader + align256(static_cast<size_t>(num_seqs) * sizeof(uint32_t));
+    *acc_at = *ml_at + align256(rows * 2 * sizeof(float));
     return *acc_at + align256(rows * head_dim * sizeof(float));
 }
 
@@ -624,12 +975,16 @@ constexpr int kQ4MaxBlock = 32;
 extern "C" size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                               int max_context_len, int partition_size, int window, int num_sinks) {
     const int P = pa::q4_partition(partition_size);
-    if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_context_len <= 0 || P <= 0 ||
-        window < 0 || num_sinks < 0)
+    if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || head_dim <= 0 ||
+        max_context_len <= 0 || P < pa::kUnit || window < 0 || num_sinks < 0)
         return 0;
-    size_t acc_at;
-    return pa::workspace_bytes(num_seqs, num_q_heads, head_dim,
-                               pa::host::seen_cap(max_context_len, window, num_sinks, pa::kQ4MaxBlock), P, &acc_at);
+    const int group = num_q_heads / num_kv_heads, tile = pa::q4_tile(group);
+    const long long heads = static_cast<long long>(num_kv_heads) * ((group + tile - 1) / tile);
+    size_t ml_at, acc_at;
+    return pa::workspace_bytes(num_seqs, tile, head_dim,
+                               pa::stretches(num_seqs, heads,
+                                             pa::host::seen_cap(max_context_len, window, num_sinks, pa::kQ4MaxBlock), P),
+                               &ml_at, &acc_at);
 }
 
 extern "C" int pa_decode_q4(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -659,8 +1014,8 @@ extern "C" int pa_decode_q4(void *out, const void *q, const void *k_cache, const
     if (window < 0 || num_sinks < 0)
         return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_q4: window and num_sinks must not be negative");
     const int P = pa::q4_partition(a->partition_size);
-    if (P < 32 || P > 4096 || P % 32 != 0)
-        return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_q4: partition_size must be a multiple of 32 in [32, 4096]");
+    if (P < 32 || P > 1024 || P % 32 != 0)
+        return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_q4: partition_size must be a multiple of 32 in [32, 1024]");
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
         return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_q4: out, q and caches must be 16-byte aligned");
 
@@ -670,19 +1025,7 @@ extern "C" int pa_decode_q4(void *out, const void *q, const void *k_cache, const
     if (window == 0 || window > ctx_cap) window = ctx_cap > 0 ? ctx_cap : 1;
     if (num_sinks > ctx_cap) num_sinks = ctx_cap;
     const int walk_cap = seen_cap(ctx_cap, window, num_sinks, block_size);
-    const int max_parts = walk_cap <= P ? 1 : static_cast<int>((static_cast<long long>(walk_cap) + P - 1) / P);
     pa::DecodeParams p{};
-    if (max_parts > 1) {
-        size_t acc_at;
-        const size_t need = pa::workspace_bytes(a->num_seqs, num_q_heads, head_dim, walk_cap, P, &acc_at);
-        if (!a->workspace || a->workspace_bytes < need || !aligned16(a->workspace))
-            return pa_fail(PA_ERR_WORKSPACE, "pa_decode_q4: workspace missing, unaligned or smaller than "
-                                             "pa_decode_q4_workspace_size()");
-        char *ws = static_cast<char *>(a->workspace);
-        p.work_ctr = reinterpret_cast<unsigned long long *>(ws);
-        p.part_ml = reinterpret_cast<float *>(ws + kWorkspaceHeader);
-        p.part_acc = reinterpret_cast<float *>(ws + acc_at);
-    }
     p.out = out;
     p.q = q;
     p.block_tables = block_tables;
@@ -695,41 +1038,40 @@ extern "C" int pa_decode_q4(void *out, const void *q, const void *k_cache, const
     p.block_size = block_size;
     p.num_blocks = a->num_blocks;
     p.max_blocks_per_seq = a->max_blocks_per_seq;
-    p.partition_size = P;
-    p.max_parts = max_parts;
     p.ctx_cap = ctx_cap;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.window = window;
     p.num_sinks = num_sinks;
     p.view_gran = block_size;
+    // pages are counted in 31 bits
+    if (static_cast<long long>(a->num_blocks) * num_kv_heads >= INT_MAX)
+        return pa_fail(PA_ERR_UNSUPPORTED, "pa_decode_q4: cache has 2^31 or more pages");
     p.sink_end = round_up_int(num_sinks, block_size);
-    const int tile = p.group > 8 ? 16 : 8;   // query heads per work item, as launch_tile picks them
+    const int tile = pa::q4_tile(p.group);
     p.tile_rows = p.group < tile ? p.group : tile;
     p.head_tiles = (p.group + tile - 1) / tile;
-
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return pa_fail(PA_ERR_CUDA, "pa_decode_q4: no CUDA device");
-    if (sm_count(dev) <= 0) return pa_fail(PA_ERR_CUDA, "pa_decode_q4: cannot query the SM count");
-    cudaStream_t st = static_cast<cudaStream_t>(a->stream);
-    const long long items = static_cast<long long>(a->num_seqs) * max_parts * num_kv_heads * p.head_tiles;
-    const long long partial_bytes =
-        static_cast<long long>(a->num_seqs) * max_parts * num_q_heads * (head_dim + 2) * 4;
-    p.reduce_newest_first = max_parts > 1 && partial_bytes > l2_bytes(dev) ? 1 : 0;
-    if (items >= (1ll << 31)) p.work_ctr = nullptr;   // hand-out indices are 32 bits wide
-    int rc = PA_OK;
-    if (a->phase != PA_PHASE_REDUCE) {
-        if (p.work_ctr && !a->skip_counter_reset &&
-            cudaMemsetAsync(p.work_ctr, 0, sizeof(unsigned long long), st) != cudaSuccess)
-            return pa_fail(PA_ERR_CUDA, "pa_decode_q4: cannot reset the work counter");
-        rc = a->dtype == PA_F32
-                 ? pa::launch_any<float>(p, k_cache, v_cache, head_dim, group_size, items, dev, st)
-                 : pa::launch_any<__nv_bfloat16>(p, k_cache, v_cache, head_dim, group_size, items, dev, st);
+    // units are counted in 31 bits, and the join's CTAs too
+    const long long heads = static_cast<long long>(num_kv_heads) * p.head_tiles;
+    if (static_cast<long long>(a->num_seqs) * heads * (walk_cap / pa::kUnit + 1ll + pa::kRowCost) >= INT_MAX ||
+        static_cast<long long>(a->num_seqs) * num_q_heads >= INT_MAX)
+        return pa_fail(PA_ERR_UNSUPPORTED, "pa_decode_q4: 2^31 or more units of 32 tokens");
+    pa::Q4Launch c{k_cache, v_cache, {}, pa::stretches(a->num_seqs, heads, walk_cap, P), P / pa::kUnit, 0, a->phase,
+                   static_cast<cudaStream_t>(a->stream)};
+    if (c.stretches) {
+        size_t ml_at, acc_at;
+        const size_t need = pa::workspace_bytes(a->num_seqs, tile, head_dim, c.stretches, &ml_at, &acc_at);
+        if (!a->workspace || a->workspace_bytes < need || !aligned16(a->workspace))
+            return pa_fail(PA_ERR_WORKSPACE, "pa_decode_q4: workspace missing, unaligned or smaller than "
+                                             "pa_decode_q4_workspace_size()");
+        char *ws = static_cast<char *>(a->workspace);
+        c.split = {reinterpret_cast<uint32_t *>(ws + 16), reinterpret_cast<uint32_t *>(ws + kWorkspaceHeader),
+                   reinterpret_cast<float *>(ws + ml_at), reinterpret_cast<float *>(ws + acc_at)};
     }
+    if (cudaGetDevice(&c.dev) != cudaSuccess) return pa_fail(PA_ERR_CUDA, "pa_decode_q4: no CUDA device");
+    if (sm_count(c.dev) <= 0) return pa_fail(PA_ERR_CUDA, "pa_decode_q4: cannot query the SM count");
+    const int rc = a->dtype == PA_F32 ? pa::launch_any<float>(p, c, head_dim, group_size)
+                                      : pa::launch_any<__nv_bfloat16>(p, c, head_dim, group_size);
     if (rc != PA_OK) return rc;
-    if (max_parts > 1 && a->phase != PA_PHASE_PARTITIONS) {
-        const cudaError_t le = pa::launch_merge(p, a->dtype == PA_F32, head_dim, st);
-        if (le != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(le));
-    }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
     return PA_OK;

@@ -31,7 +31,7 @@ def pa():
 
 @pytest.mark.parametrize("change,code", [
     (dict(hd=96), -2), (dict(bs=8), -2), (dict(group=16), -2), (dict(hq=6, hkv=4), -1), (dict(hkv=0), -1),
-    (dict(dtype=5), -1), (dict(P=16), -1), (dict(P=48), -1), (dict(P=8192), -1), (dict(phase=3), -1),
+    (dict(dtype=5), -1), (dict(P=16), -1), (dict(P=48), -1), (dict(P=2048), -1), (dict(phase=3), -1),
     (dict(window=-1), -1), (dict(sinks=-1), -1), (dict(ctx=4096, P=512), -7), (dict(ctx=4096, P=512, window=600), -7),
     (dict(q=None), -1), (dict(kc=FAKE + 8), -1), (dict(simt=1), -2), (dict(k_new=FAKE), -2), (dict(seqs=-1), -1),
     (dict(nb=0), -1), (dict(width=0), -1), (dict(ctx=-1), -1), (dict(seqs=0), 0),
@@ -51,18 +51,26 @@ def test_bad_arguments_are_refused_on_the_host(pa, change, code):
 
 
 def test_workspace_sizes(pa):
+    """A header and a word per sequence, then two rows of heads (a tile of 8, or 16
+    for groups above 8) for each stretch: at most 2432 of them, and at most one
+    per partition_size tokens of what the batch can hold."""
     size = pa.pa_decode_q4_workspace_size
     assert size(4, 8, 2, 128, 512, 512) == 0 and size(4, 8, 2, 128, 0) == 0 and size(0, 8, 2, 128, 4096) == 0
+    assert size(4, 9, 2, 128, 4096) == 0        # refused: 9 heads over 2
     a256 = lambda x: (x + 255) // 256 * 256
-    rows = 4 * 3 * 8
-    assert size(4, 8, 2, 128, 1025, 512) == 256 + a256(rows * 8) + a256(rows * 128 * 4)
-    # a window bounds what is walked: 600 + 31 + 32 tokens at most, two partitions of 512
-    rows = 4 * 2 * 8
-    assert size(4, 8, 2, 128, 10**6, 512, window=600, num_sinks=5) == 256 + a256(rows * 8) + a256(rows * 128 * 4)
+
+    def want(seqs, rows, tile, hd, tokens, P):
+        n = min(2432, -(-(seqs * rows * -(-tokens // 32)) // (P // 32)))
+        return 256 + a256(4 * seqs) + a256(n * 2 * tile * 8) + a256(n * 2 * tile * hd * 4)
+
+    assert size(4, 8, 2, 128, 1025, 512) == want(4, 2, 8, 128, 1025, 512)
+    assert size(300, 64, 8, 64, 10**6, 512) == want(300, 8, 8, 64, 10**6, 512)
+    assert size(4, 40, 2, 128, 1025, 512) == want(4, 4, 16, 128, 1025, 512)
+    # a window bounds what is walked: 600 tokens, 5 sinks, and blocks of 32 at their edges
+    assert size(4, 8, 2, 128, 10**6, 512, window=600, num_sinks=5) == want(4, 2, 8, 128, 32 + 600 + 31, 512)
     big = 2**31 - 1
-    parts = -(-big // 4096)
-    assert size(1, 1, 1, 64, big, 4096) == 256 + a256(parts * 8) + a256(parts * 256)
-    assert size(1, 1, 1, 64, big, 4096, window=big, num_sinks=big) == size(1, 1, 1, 64, big, 4096)
+    assert size(1, 1, 1, 64, big, 1024) == want(1, 1, 8, 64, big, 1024)
+    assert size(1, 1, 1, 64, big, 1024, window=big, num_sinks=big) == size(1, 1, 1, 64, big, 1024)
 
 
 def test_binding_refuses_cpu_tensors(pa):
