@@ -29,6 +29,7 @@
 #include <climits>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "pa_decode_common.cuh"
 #include "pa_q4.cuh"
@@ -479,8 +480,9 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
 
         for (int k = 0; k < units; ++k) {
             const int s = n_done % NSTAGE;
-            bool ok = mbar_wait_bounded(bar_s + 8 * s, (n_done / NSTAGE) & 1u);
-            if (__any_sync(kFull, !ok)) {
+            const uint32_t parity = (n_done / NSTAGE) & 1u;
+            if (!__all_sync(kFull, mbar_try_wait(bar_s + 8 * s, parity)) &&
+                !__all_sync(kFull, mbar_wait_bounded(bar_s + 8 * s, parity))) {
                 if (lane == 0) flag_status(p.status, PA_STATUS_WAIT_TIMEOUT);
                 failed = true;
                 break;
@@ -601,7 +603,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
             // as they are.  What would pass fp16's range is seen by sums, which the
             // FMA pipe has room for: while this lane's p sum to at most 2^5 a head and
             // its s inv to at most 2^10, no w passes 2^15.
-            float pr[2][NT][4];
+            float pr[2][NT][4], sw[2][2][NG];   // p, and s inv of this lane's tokens
             float sum[NT][2], most = 0.f, wide = 0.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) sum[nt][0] = sum[nt][1] = 0.f;
@@ -613,7 +615,10 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                     float sv[NG], mv[NG];
                     load_pairs<NG, SPLIT>(Vp + (row_g + 8 * r) * F::PARAM_BYTES, sv, mv);
 #pragma unroll
-                    for (int i = 0; i < NG; ++i) wide = fmaf(sv[i], inv[i], wide);
+                    for (int i = 0; i < NG; ++i) {
+                        sw[half][r][i] = sv[i] * inv[i];
+                        wide += sw[half][r][i];
+                    }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -658,30 +663,34 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                             sum[nt][c & 1] += pr[half][nt][c];
                         }
                 }
+                // (s inv is back to s by 1 / inv = S / 4, exactly)
                 float top[NG];
 #pragma unroll
-                for (int i = 0; i < NG; ++i) top[i] = keep * S[i];
+                for (int i = 0; i < NG; ++i) top[i] = keep * 4.f;
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        float sv[NG], mv[NG], most_p = 0.0625f;
-                        load_pairs<NG, SPLIT>(stage + HALF_BYTES + par_0 + half * par_half +
-                                                  (row_g + 8 * r) * F::PARAM_BYTES, sv, mv);
+                        float most_p = 0.0625f;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             most_p = fmaxf(most_p, fmaxf(pr[half][nt][2 * r], pr[half][nt][2 * r + 1]));
 #pragma unroll
-                        for (int i = 0; i < NG; ++i) top[i] = fmaxf(top[i], most_p * sv[i]);
+                        for (int i = 0; i < NG; ++i) top[i] = fmaxf(top[i], most_p * sw[half][r][i]);
                     }
 #pragma unroll
                 for (int i = 0; i < NG; ++i) {
                     float mx = top[i];
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
-                    const float now = pow2_above(mx), ratio = S[i] / now;
+                    const float now = pow2_above(mx * (0.25f * S[i])), ratio = S[i] / now;
                     S[i] = now;
                     inv[i] = 4.f / now;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        sw[half][0][i] *= ratio;
+                        sw[half][1][i] *= ratio;
+                    }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
                         if ((G == 64 ? mt / 4 : mt / 2) == i)
@@ -713,8 +722,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                     for (int i = 0; i < NG; ++i)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const float sw = sv[r][i] * inv[i];
-                            const float x = pr[half][nt][2 * r] * sw, y = pr[half][nt][2 * r + 1] * sw;
+                            const float x = pr[half][nt][2 * r] * sw[half][r][i], y = pr[half][nt][2 * r + 1] * sw[half][r][i];
                             const uint32_t h = pack_f16(x, y);
                             pb[0][nt][i][r] = movmatrix_trans(h);
                             if constexpr (SPLIT) {
@@ -843,34 +851,38 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_q4_kernel(const DecodePa
     const int parts = static_cast<int>(w1 - w0) + 1;
     // the stretch that begins the row keeps it in its second slot, the others in their first
     auto at = [&](int i) { return ((long long)(w0 + i) * 2 + (i == 0)) * rows + r; };
-    float M = -INFINITY, L = 0.f;
-    for (int i = lane; i < parts; i += 32) M = fmaxf(M, split.ml[at(i) * 2]);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
     constexpr int E = HD / 32;   // values per lane
+    using Vec = typename std::conditional<E == 4, float4, float2>::type;
+    constexpr int FETCH = 16;    // partials on their way at a time
+    float M = -INFINITY, L = 0.f;
     float acc[E] = {};
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-        float f = 0.f;
-        if (i0 + lane < parts) {
-            const float2 ml = *reinterpret_cast<const float2 *>(split.ml + at(i0 + lane) * 2);
-            f = exp2f(ml.x - M);
-            L = fmaf(f, ml.y, L);
-        }
-        const int n = min(32, parts - i0);
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
+    for (int i0 = 0; i0 < parts; i0 += FETCH) {
+        const int n = min(FETCH, parts - i0);
+        const float2 ml = lane < n ? *reinterpret_cast<const float2 *>(split.ml + at(i0 + lane) * 2)
+                                   : make_float2(-INFINITY, 0.f);
+        Vec v[FETCH];
+#pragma unroll
+        for (int i = 0; i < FETCH; ++i)
+            if (i < n) v[i] = *reinterpret_cast<const Vec *>(split.acc + at(i0 + i) * HD + lane * E);
+        float top = ml.x;
+#pragma unroll
+        for (int o = 1; o < FETCH; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        top = __shfl_sync(kFull, top, 0);
+        const float now = fmaxf(M, top), alpha = exp2f(M - now);   // the first M is -inf: alpha 0
+        M = now;
+        const float f = lane < n ? exp2f(ml.x - now) : 0.f;
+        L = L * alpha + f * ml.y;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= alpha;
+#pragma unroll
+        for (int i = 0; i < FETCH; ++i) {
+            if (i >= n) break;
             const float w = __shfl_sync(kFull, f, i);
-            const float *a = split.acc + at(i0 + i) * HD + lane * E;
+            acc[0] = fmaf(w, v[i].x, acc[0]);
+            acc[1] = fmaf(w, v[i].y, acc[1]);
             if constexpr (E == 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(a);
-                acc[0] = fmaf(w, v.x, acc[0]);
-                acc[1] = fmaf(w, v.y, acc[1]);
-                acc[E - 2] = fmaf(w, v.z, acc[E - 2]);
-                acc[E - 1] = fmaf(w, v.w, acc[E - 1]);
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(a);
-                acc[0] = fmaf(w, v.x, acc[0]);
-                acc[1] = fmaf(w, v.y, acc[1]);
+                acc[E - 2] = fmaf(w, v[i].z, acc[E - 2]);
+                acc[E - 1] = fmaf(w, v[i].w, acc[E - 1]);
             }
         }
     }
