@@ -184,17 +184,20 @@ def _ptr(t: torch.Tensor | None):
 
 def _on_device(dev: torch.device):
     """Makes dev the current device for a call; nothing to do when it is."""
-    if torch.cuda.current_device() == dev.index:
-        return contextlib.nullcontext()
+    if torch._C._cuda_getDevice() == dev.index:
+        return _NOWHERE
     return torch.cuda.device(dev)
+
+
+_NOWHERE = contextlib.nullcontext()
 
 
 def _check_cuda(t: torch.Tensor, name: str, dtypes, dev=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
-    if dev is not None and t.device != dev:
+    if dev is not None and t.get_device() != dev.index:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtypes}")
@@ -299,7 +302,7 @@ class _PreparedCall:
         a.stream = _stream_ptr(stream, self._device)
         if phase is not None:
             a.phase = phase
-        if torch.cuda.current_device() == self._device.index:
+        if torch._C._cuda_getDevice() == self._device.index:
             rc = self._fn(*self._operands, *self._sizes, self._ref)
         else:
             with torch.cuda.device(self._device):
@@ -514,8 +517,9 @@ def _q4_geometry(k_cache: torch.Tensor, v_cache: torch.Tensor, head_dim: int, gr
     if k_cache.dim() != 3 or v_cache.shape != k_cache.shape:
         raise ValueError("4-bit caches must be uint8 [num_blocks, Hkv, page_bytes], both of one shape")
     nb, Hkv, page = k_cache.shape
-    for bs in (16, 32):
-        if page == _lib.pa_q4_page_bytes(head_dim, bs, group_size):
+    if head_dim in (64, 128) and group_size in (32, 64):
+        bs, rest = divmod(page, head_dim // 2 + 4 * (head_dim // group_size))
+        if rest == 0 and bs in (16, 32):
             return nb, Hkv, bs
     raise ValueError(f"page_bytes {page} is not pa_q4_page_bytes({head_dim}, 16 or 32, {group_size})")
 

@@ -1,13 +1,19 @@
 // Cache write and read of the 4-bit cache for sm_103a (include/pa.h states the
 // format and the quantisation).
 //
-// Both are one pass over the rows.  HD / 8 lanes share a head row; lane (w, g)
-// of them owns 32-bit code word g * W + w, whose halves are the units of four
-// values 16 w + g and 16 w + 8 + g.  So a lane loads two 8-byte (bf16) or
-// 16-byte (fp32) pieces, a row's eight lanes of one w cover 64 consecutive
-// bytes per load, and the group minimum and maximum are three shuffles over
-// those eight lanes (the eight lanes of one w hold one group of 64 or two of
-// 32).
+// Both are one pass over the rows.  Eight lanes share a head row; lane g of them
+// owns code words g * W .. g * W + W - 1 (W = HD / 64), whose halves are the
+// units of four values 16 w + g and 16 w + 8 + g.  So a lane loads 2 W pieces of
+// four values, the eight lanes' pieces of one unit row are contiguous, and a
+// group is what the eight lanes hold of one word (64) or one half-word (32):
+// its minimum and maximum are three shuffles.  bf16 values are compared packed,
+// two groups' extremes to a register.
+//
+// The write is bound by instructions before bytes, so each group's parameters
+// (a division and a reciprocal) are worked out by one lane, lane i group i's,
+// and handed round, and a code costs four instructions: subtract, multiply, add
+// 1.5 * 2^23 (which rounds half to even and leaves the code in the low mantissa
+// bits), and a multiply-add that packs it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -43,30 +49,85 @@ __device__ __forceinline__ void put4(__nv_bfloat16 *p, const float (&x)[4]) {
     *reinterpret_cast<uint2 *>(p) = u;
 }
 
-struct Range {
-    float lo, hi;
-    bool bad;
+// The extremes of a lane's (then an octet's) two half-words of one word w:
+// element 0 the unit 16 w + g, element 1 the unit 16 w + 8 + g.  `top` is the
+// largest magnitude, by which something not finite shows.
+template <typename T>
+struct Extremes;
+
+template <>
+struct Extremes<float> {
+    float lo[2], hi[2], top[2];
+    __device__ __forceinline__ void take(const float *p) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float x[4];
+            load4(p + 32 * h, x);
+            lo[h] = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
+            hi[h] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            // comparisons with NaN are false, so NaN counts as infinite
+            const bool fine = fabsf(x[0]) < 0x1p126f && fabsf(x[1]) < 0x1p126f && fabsf(x[2]) < 0x1p126f &&
+                              fabsf(x[3]) < 0x1p126f;
+            top[h] = fine ? 0.f : INFINITY;
+        }
+    }
+    __device__ __forceinline__ void join_octet() {
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                lo[h] = fminf(lo[h], __shfl_xor_sync(kFull, lo[h], o));
+                hi[h] = fmaxf(hi[h], __shfl_xor_sync(kFull, hi[h], o));
+                top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], o));
+            }
+    }
+    __device__ __forceinline__ float low(int h) const { return lo[h]; }
+    __device__ __forceinline__ float high(int h) const { return hi[h]; }
+    __device__ __forceinline__ bool bad(int h) const { return top[h] != 0.f; }
 };
 
-// Minimum, maximum and "holds something not finite" over the eight lanes of one w.
-__device__ __forceinline__ Range octet_range(Range r, int lane) {
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-        r.lo = fminf(r.lo, __shfl_xor_sync(kFull, r.lo, o));
-        r.hi = fmaxf(r.hi, __shfl_xor_sync(kFull, r.hi, o));
-    }
-    r.bad = ((__ballot_sync(kFull, r.bad) >> (lane & ~7)) & 0xffu) != 0u;
-    return r;
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
-__device__ __forceinline__ Range range_of(const float (&x)[4]) {
-    Range r;
-    r.lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
-    r.hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-    const float big = 0x1p126f;   // comparisons with NaN are false, so NaN is bad too
-    r.bad = !(fabsf(x[0]) < big && fabsf(x[1]) < big && fabsf(x[2]) < big && fabsf(x[3]) < big);
-    return r;
-}
+template <>
+struct Extremes<__nv_bfloat16> {
+    uint32_t lo, hi, top;   // half h of each: half-word h
+    __device__ __forceinline__ void take(const __nv_bfloat16 *p) {
+        const uint2 a = *reinterpret_cast<const uint2 *>(p), b = *reinterpret_cast<const uint2 *>(p + 32);
+        constexpr uint32_t kAbs = 0x7fff7fffu;
+        const uint32_t la = min_bf16x2(a.x, a.y), lb = min_bf16x2(b.x, b.y);
+        const uint32_t ha = max_bf16x2(a.x, a.y), hb = max_bf16x2(b.x, b.y);
+        const uint32_t ta = max_u16x2(a.x & kAbs, a.y & kAbs), tb = max_u16x2(b.x & kAbs, b.y & kAbs);
+        // each register holds two partial extremes of one unit: one of each unit instead
+        lo = min_bf16x2(__byte_perm(la, lb, 0x5410), __byte_perm(la, lb, 0x7632));
+        hi = max_bf16x2(__byte_perm(ha, hb, 0x5410), __byte_perm(ha, hb, 0x7632));
+        top = max_u16x2(__byte_perm(ta, tb, 0x5410), __byte_perm(ta, tb, 0x7632));
+    }
+    __device__ __forceinline__ void join_octet() {
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+            lo = min_bf16x2(lo, __shfl_xor_sync(kFull, lo, o));
+            hi = max_bf16x2(hi, __shfl_xor_sync(kFull, hi, o));
+            top = max_u16x2(top, __shfl_xor_sync(kFull, top, o));
+        }
+    }
+    __device__ __forceinline__ float low(int h) const { return __uint_as_float(h ? lo & 0xffff0000u : lo << 16); }
+    __device__ __forceinline__ float high(int h) const { return __uint_as_float(h ? hi & 0xffff0000u : hi << 16); }
+    __device__ __forceinline__ bool bad(int h) const { return (h ? top >> 16 : top & 0xffffu) >= 0x7e80u; }   // 2^126
+};
 
 struct Group {
     float m, inv;
@@ -74,15 +135,17 @@ struct Group {
 };
 
 // The group's parameters.  Only this rounds in a direction: m down and s up,
-// so that [m, m + 15 s] covers the group and no code needs a clamp.
-__device__ __forceinline__ Group group_of(const Range &r) {
+// so that [m, m + 15 s] covers the group and no code needs a clamp.  A bad
+// group's m and inv are zero, so that its codes are, unless a value times zero
+// is NaN, whose bits the caller masks off like any other's.
+__device__ __forceinline__ Group group_of(float low, float high, bool bad) {
     Group g{0.f, 0.f, 0x7fc00000u};   // step 0, minimum NaN
-    if (r.bad) return g;
-    const uint32_t lo = __float_as_uint(r.lo);
+    if (bad) return g;
+    const uint32_t lo = __float_as_uint(low);
     uint32_t m = lo & 0xffff0000u;
     if ((lo >> 31) && (lo & 0xffffu)) m += 0x10000u;   // negative: towards the larger magnitude
     g.m = __uint_as_float(m);
-    const float far = __fsub_rn(r.hi, g.m);
+    const float far = __fsub_rn(high, g.m);
     float s = 0.f;
     if (far > 0.f) {
         s = __uint_as_float((__float_as_uint(__fdiv_rn(far, 15.f)) + 0xffffu) & 0xffff0000u);
@@ -93,15 +156,13 @@ __device__ __forceinline__ Group group_of(const Range &r) {
     return g;
 }
 
-// Codes of four values in the low 16 bits.  Adding 1.5 * 2^23 rounds to an
-// integer, half to even, and leaves it in the low mantissa bits.
-__device__ __forceinline__ uint32_t encode4(const float (&x)[4], const Group &g) {
+// Codes of four values in the low 16 bits.  Each sum's bits are 0x4b400000 plus
+// the code; the constant's low 22 bits are zero and stay so when multiplied.
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], float m, float inv) {
     uint32_t u = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float t = __fadd_rn(__fmul_rn(__fsub_rn(x[j], g.m), g.inv), 12582912.f);
-        u |= (__float_as_uint(t) & 15u) << (4 * j);
-    }
+    for (int j = 3; j >= 0; --j)
+        u = u * 16u + __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(x[j], m), inv), 12582912.f));
     return u;
 }
 
@@ -109,81 +170,116 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], const Group &g)
 template <typename T, int HD, int G>
 __global__ void __launch_bounds__(kQ4Threads)
     q4_write_kernel(const T *__restrict__ k, const T *__restrict__ v, uint8_t *__restrict__ k_cache,
-                    uint8_t *__restrict__ v_cache, const int64_t *__restrict__ slot_mapping, long long rows,
-                    int num_kv_heads, int bs_shift, long long num_slots, int32_t *status) {
+                    uint8_t *__restrict__ v_cache, const int64_t *__restrict__ slot_mapping, uint32_t rows,
+                    uint32_t num_kv_heads, int bs_shift, long long num_slots, int32_t *status) {
     using F = Q4Format<HD, G>;
-    constexpr int LPR = HD / 8;
-    const int lane = threadIdx.x & 31, li = threadIdx.x % LPR, w = li >> 3, g = li & 7;
-    const long long r = (long long)blockIdx.x * (kQ4Threads / LPR) + threadIdx.x / LPR;
+    constexpr int W = F::W, NG = F::GROUPS;
+    const int lane = threadIdx.x & 31, g = lane & 7;
+    const uint32_t r = blockIdx.x * (kQ4Threads / 8) + threadIdx.x / 8;
     const bool live = r < rows;
-    const int64_t slot = live ? slot_mapping[r / num_kv_heads] : -1;
-    const int h = static_cast<int>(r % num_kv_heads);
+    const uint32_t t = (live ? r : 0u) / num_kv_heads, h = r - t * num_kv_heads;
+    const int64_t slot = live ? slot_mapping[t] : -1;
     const bool ok = slot >= 0 && slot < num_slots;
-    if (slot >= num_slots && li == 0 && h == 0 && blockIdx.y == 0) flag_status(status, PA_STATUS_BAD_SLOT);
+    if (slot >= num_slots && g == 0 && h == 0 && blockIdx.y == 0) flag_status(status, PA_STATUS_BAD_SLOT);
 
-    const T *src = (blockIdx.y ? v : k) + (live ? r : 0) * HD + 64 * w + 4 * g;
-    float a[4], b[4];
-    load4(src, a);
-    load4(src + 32, b);
-    Range ra = range_of(a), rb = range_of(b);
-    if (G == 64) {
-        ra.lo = fminf(ra.lo, rb.lo);
-        ra.hi = fmaxf(ra.hi, rb.hi);
-        ra.bad |= rb.bad;
+    const T *src = (blockIdx.y ? v : k) + static_cast<long long>(live ? r : 0u) * HD + 4 * g;
+    Extremes<T> ends[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) ends[w].take(src + 64 * w);
+#pragma unroll
+    for (int w = 0; w < W; ++w) ends[w].join_octet();
+    // Lane i of the octet (modulo the groups) works out group i.
+    float low = 0.f, high = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+        const Extremes<T> &e = ends[G == 64 ? i : i / 2];
+        const float l = G == 64 ? fminf(e.low(0), e.low(1)) : e.low(i & 1);
+        const float u = G == 64 ? fmaxf(e.high(0), e.high(1)) : e.high(i & 1);
+        const bool b = G == 64 ? e.bad(0) || e.bad(1) : e.bad(i & 1);
+        if ((g & (NG - 1)) == i) {
+            low = l;
+            high = u;
+            bad = b;
+        }
     }
-    const Group ga = group_of(octet_range(ra, lane));
-    const Group gb = G == 64 ? ga : group_of(octet_range(rb, lane));
-    const bool bad_a = (ga.pair & 0xffff0000u) == 0x7fc00000u, bad_b = (gb.pair & 0xffff0000u) == 0x7fc00000u;
-    const uint32_t word = (bad_a ? 0u : encode4(a, ga)) | (bad_b ? 0u : encode4(b, gb) << 16);
+    const Group mine = group_of(low, high, bad);
+    const unsigned bads = __ballot_sync(kFull, bad) >> (lane & ~7);
+    uint32_t word[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        word[w] = 0;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int i = G == 64 ? w : 2 * w + hf;
+            const float m = __shfl_sync(kFull, mine.m, (lane & ~7) + i), inv = __shfl_sync(kFull, mine.inv, (lane & ~7) + i);
+            float x[4];
+            load4(src + 64 * w + 32 * hf, x);   // again: in a register or the L1
+            const uint32_t codes = (bads >> i) & 1u ? 0u : encode4(x, m, inv);
+            word[w] |= hf ? codes << 16 : codes & 0xffffu;
+        }
+    }
     if (!ok) return;
     const int bs = 1 << bs_shift;
     const int row = static_cast<int>(slot & (bs - 1));
     uint8_t *page = (blockIdx.y ? v_cache : k_cache) +
-                    ((slot >> bs_shift) * num_kv_heads + h) * ((long long)F::ROW_BYTES << bs_shift);
-    *reinterpret_cast<uint32_t *>(page + row * F::CODE_BYTES + (g * F::W + w) * 4) = word;
-    uint32_t *par = reinterpret_cast<uint32_t *>(page + bs * F::CODE_BYTES + row * F::PARAM_BYTES);
-    if (g == 0) {
-        if (G == 64)
-            par[w] = ga.pair;
-        else
-            *reinterpret_cast<uint2 *>(par + 2 * w) = make_uint2(ga.pair, gb.pair);
-    }
+                    ((slot >> bs_shift) * num_kv_heads + h) * (static_cast<long long>(F::ROW_BYTES) << bs_shift);
+    uint32_t *to = reinterpret_cast<uint32_t *>(page + row * F::CODE_BYTES) + g * W;
+    if constexpr (W == 2)
+        *reinterpret_cast<uint2 *>(to) = make_uint2(word[0], word[W - 1]);
+    else
+        *to = word[0];
+    if (g < NG) reinterpret_cast<uint32_t *>(page + bs * F::CODE_BYTES + row * F::PARAM_BYTES)[g] = mine.pair;
 }
 
 template <typename T, int HD, int G>
 __global__ void __launch_bounds__(kQ4Threads)
     q4_gather_kernel(T *__restrict__ k, T *__restrict__ v, const uint8_t *__restrict__ k_cache,
-                     const uint8_t *__restrict__ v_cache, const int64_t *__restrict__ slot_mapping, long long rows,
-                     int num_kv_heads, int bs_shift, long long num_slots, int32_t *status) {
+                     const uint8_t *__restrict__ v_cache, const int64_t *__restrict__ slot_mapping, uint32_t rows,
+                     uint32_t num_kv_heads, int bs_shift, long long num_slots, int32_t *status) {
     using F = Q4Format<HD, G>;
-    constexpr int LPR = HD / 8;
-    const int li = threadIdx.x % LPR, w = li >> 3, g = li & 7;
-    const long long r = (long long)blockIdx.x * (kQ4Threads / LPR) + threadIdx.x / LPR;
+    constexpr int W = F::W, NG = F::GROUPS;
+    const int g = threadIdx.x & 7;
+    const uint32_t r = blockIdx.x * (kQ4Threads / 8) + threadIdx.x / 8;
     if (r >= rows) return;
-    const int64_t slot = slot_mapping[r / num_kv_heads];
+    const uint32_t t = r / num_kv_heads, h = r - t * num_kv_heads;
+    const int64_t slot = slot_mapping[t];
     if (slot < 0) return;
-    const int h = static_cast<int>(r % num_kv_heads);
     if (slot >= num_slots) {
-        if (li == 0 && h == 0 && blockIdx.y == 0) flag_status(status, PA_STATUS_BAD_SLOT);
+        if (g == 0 && h == 0 && blockIdx.y == 0) flag_status(status, PA_STATUS_BAD_SLOT);
         return;
     }
     const int bs = 1 << bs_shift;
     const int row = static_cast<int>(slot & (bs - 1));
     const uint8_t *page = (blockIdx.y ? v_cache : k_cache) +
-                          ((slot >> bs_shift) * num_kv_heads + h) * ((long long)F::ROW_BYTES << bs_shift);
-    const uint32_t word = *reinterpret_cast<const uint32_t *>(page + row * F::CODE_BYTES + (g * F::W + w) * 4);
-    const uint32_t *par = reinterpret_cast<const uint32_t *>(page + bs * F::CODE_BYTES + row * F::PARAM_BYTES);
-    const uint32_t pa = G == 64 ? par[w] : par[2 * w], pb = G == 64 ? pa : par[2 * w + 1];
-    float a[4], b[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        // step * code is exact in fp32 (8 by 4 bits), so this rounds once
-        a[j] = fmaf(static_cast<float>((word >> (4 * j)) & 15u), q4_step(pa), q4_min(pa));
-        b[j] = fmaf(static_cast<float>((word >> (16 + 4 * j)) & 15u), q4_step(pb), q4_min(pb));
+                          ((slot >> bs_shift) * num_kv_heads + h) * (static_cast<long long>(F::ROW_BYTES) << bs_shift);
+    const uint32_t *from = reinterpret_cast<const uint32_t *>(page + row * F::CODE_BYTES) + g * W;
+    uint32_t word[W], pair[NG];
+    if constexpr (W == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(from);
+        word[0] = x.x;
+        word[W - 1] = x.y;
+    } else {
+        word[0] = *from;
     }
-    T *dst = (blockIdx.y ? v : k) + r * HD + 64 * w + 4 * g;
-    put4(dst, a);
-    put4(dst + 32, b);
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+        pair[i] = reinterpret_cast<const uint32_t *>(page + bs * F::CODE_BYTES + row * F::PARAM_BYTES)[i];
+    T *dst = (blockIdx.y ? v : k) + static_cast<long long>(r) * HD + 4 * g;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t p = pair[G == 64 ? w : 2 * w + hf], u = hf ? word[w] >> 16 : word[w];
+            float x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // 2^23 + code; step * code is exact in fp32 (8 by 4 bits), so the sum rounds once
+                const float c = __uint_as_float(((u >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f;
+                x[j] = fmaf(c, q4_step(p), q4_min(p));
+            }
+            put4(dst + 64 * w + 32 * hf, x);
+        }
 }
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -201,8 +297,8 @@ int check(const char *const (&msg)[5], const void *k, const void *v, const void 
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
         (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
         return pa_fail(PA_ERR_INVALID_ARG, msg[4]);
-    // the grid counts tiles of at least 16 rows in 31 bits
-    if (static_cast<long long>(num_tokens) * num_kv_heads > (1ll << 34))
+    // rows are counted in 31 bits
+    if (static_cast<long long>(num_tokens) * num_kv_heads >= (1ll << 31))
         return pa_fail(PA_ERR_UNSUPPORTED, msg[1]);
     *rows = static_cast<long long>(num_tokens) * num_kv_heads;
     return PA_OK;
@@ -234,9 +330,8 @@ struct Call {
     int num_kv_heads, bs_shift;
     int32_t *status;
     cudaStream_t stream;
-    template <int HD>
     dim3 grid() const {
-        constexpr int per = kQ4Threads / (HD / 8);
+        constexpr int per = kQ4Threads / 8;
         return dim3(static_cast<unsigned>((rows + per - 1) / per), 2);
     }
 };
@@ -244,18 +339,20 @@ struct Call {
 struct WriteLaunch : Call {
     template <typename T, int HD, int G>
     void run() const {
-        q4_write_kernel<T, HD, G><<<grid<HD>(), kQ4Threads, 0, stream>>>(
+        q4_write_kernel<T, HD, G><<<grid(), kQ4Threads, 0, stream>>>(
             static_cast<const T *>(k), static_cast<const T *>(v), static_cast<uint8_t *>(k_cache),
-            static_cast<uint8_t *>(v_cache), slot_mapping, rows, num_kv_heads, bs_shift, num_slots, status);
+            static_cast<uint8_t *>(v_cache), slot_mapping, static_cast<uint32_t>(rows),
+            static_cast<uint32_t>(num_kv_heads), bs_shift, num_slots, status);
     }
 };
 
 struct GatherLaunch : Call {
     template <typename T, int HD, int G>
     void run() const {
-        q4_gather_kernel<T, HD, G><<<grid<HD>(), kQ4Threads, 0, stream>>>(
+        q4_gather_kernel<T, HD, G><<<grid(), kQ4Threads, 0, stream>>>(
             static_cast<T *>(k), static_cast<T *>(v), static_cast<const uint8_t *>(k_cache),
-            static_cast<const uint8_t *>(v_cache), slot_mapping, rows, num_kv_heads, bs_shift, num_slots, status);
+            static_cast<const uint8_t *>(v_cache), slot_mapping, static_cast<uint32_t>(rows),
+            static_cast<uint32_t>(num_kv_heads), bs_shift, num_slots, status);
     }
 };
 
