@@ -29,6 +29,20 @@ namespace {
 
 constexpr int kQ4Threads = 256;
 
+// r / d for r < 2^31 by a product: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d),
+// m d - 2^(31 + s) < 2^s, so r m / 2^(31 + s) is over r / d by less than 1 / d.
+struct Divisor {
+    uint32_t m;
+    int shift;   // s - 1; -1 for d = 1
+    explicit Divisor(uint32_t d) {
+        int s = 0;
+        while ((1u << s) < d) ++s;
+        m = static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d);
+        shift = s - 1;
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t r) const { return shift < 0 ? r : __umulhi(r, m) >> shift; }
+};
+
 __device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
     const float4 v = *reinterpret_cast<const float4 *>(p);
     x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
@@ -49,26 +63,43 @@ __device__ __forceinline__ void put4(__nv_bfloat16 *p, const float (&x)[4]) {
     *reinterpret_cast<uint2 *>(p) = u;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t min_nan(uint32_t a, uint32_t b) {   // of two bf16
+    uint32_t d;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // The extremes of a lane's (then an octet's) two half-words of one word w:
-// element 0 the unit 16 w + g, element 1 the unit 16 w + 8 + g.  `top` is the
-// largest magnitude, by which something not finite shows.
+// element 0 the unit 16 w + g, element 1 the unit 16 w + 8 + g.  NaN where one
+// of the values is.
 template <typename T>
 struct Extremes;
 
 template <>
 struct Extremes<float> {
-    float lo[2], hi[2], top[2];
+    float lo[2], hi[2];
     __device__ __forceinline__ void take(const float *p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float x[4];
             load4(p + 32 * h, x);
-            lo[h] = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
-            hi[h] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-            // comparisons with NaN are false, so NaN counts as infinite
-            const bool fine = fabsf(x[0]) < 0x1p126f && fabsf(x[1]) < 0x1p126f && fabsf(x[2]) < 0x1p126f &&
-                              fabsf(x[3]) < 0x1p126f;
-            top[h] = fine ? 0.f : INFINITY;
+            lo[h] = min_nan(min_nan(x[0], x[1]), min_nan(x[2], x[3]));
+            hi[h] = max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
         }
     }
     __device__ __forceinline__ void join_octet() {
@@ -76,57 +107,43 @@ struct Extremes<float> {
         for (int o = 1; o < 8; o <<= 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                lo[h] = fminf(lo[h], __shfl_xor_sync(kFull, lo[h], o));
-                hi[h] = fmaxf(hi[h], __shfl_xor_sync(kFull, hi[h], o));
-                top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], o));
+                lo[h] = min_nan(lo[h], __shfl_xor_sync(kFull, lo[h], o));
+                hi[h] = max_nan(hi[h], __shfl_xor_sync(kFull, hi[h], o));
             }
     }
-    __device__ __forceinline__ float low(int h) const { return lo[h]; }
-    __device__ __forceinline__ float high(int h) const { return hi[h]; }
-    __device__ __forceinline__ bool bad(int h) const { return top[h] != 0.f; }
+    // Both half-words as one group.
+    __device__ __forceinline__ void join_halves() {
+        lo[0] = min_nan(lo[0], lo[1]);
+        hi[0] = max_nan(hi[0], hi[1]);
+    }
+    __device__ __forceinline__ float low(bool h) const { return h ? lo[1] : lo[0]; }
+    __device__ __forceinline__ float high(bool h) const { return h ? hi[1] : hi[0]; }
 };
-
-__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
 
 template <>
 struct Extremes<__nv_bfloat16> {
-    uint32_t lo, hi, top;   // half h of each: half-word h
+    uint32_t lo, hi;   // half h of each: half-word h
     __device__ __forceinline__ void take(const __nv_bfloat16 *p) {
         const uint2 a = *reinterpret_cast<const uint2 *>(p), b = *reinterpret_cast<const uint2 *>(p + 32);
-        constexpr uint32_t kAbs = 0x7fff7fffu;
-        const uint32_t la = min_bf16x2(a.x, a.y), lb = min_bf16x2(b.x, b.y);
-        const uint32_t ha = max_bf16x2(a.x, a.y), hb = max_bf16x2(b.x, b.y);
-        const uint32_t ta = max_u16x2(a.x & kAbs, a.y & kAbs), tb = max_u16x2(b.x & kAbs, b.y & kAbs);
+        const uint32_t la = min_nan(a.x, a.y), lb = min_nan(b.x, b.y);
+        const uint32_t ha = max_nan(a.x, a.y), hb = max_nan(b.x, b.y);
         // each register holds two partial extremes of one unit: one of each unit instead
-        lo = min_bf16x2(__byte_perm(la, lb, 0x5410), __byte_perm(la, lb, 0x7632));
-        hi = max_bf16x2(__byte_perm(ha, hb, 0x5410), __byte_perm(ha, hb, 0x7632));
-        top = max_u16x2(__byte_perm(ta, tb, 0x5410), __byte_perm(ta, tb, 0x7632));
+        lo = min_nan(__byte_perm(la, lb, 0x5410), __byte_perm(la, lb, 0x7632));
+        hi = max_nan(__byte_perm(ha, hb, 0x5410), __byte_perm(ha, hb, 0x7632));
     }
     __device__ __forceinline__ void join_octet() {
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) {
-            lo = min_bf16x2(lo, __shfl_xor_sync(kFull, lo, o));
-            hi = max_bf16x2(hi, __shfl_xor_sync(kFull, hi, o));
-            top = max_u16x2(top, __shfl_xor_sync(kFull, top, o));
+            lo = min_nan(lo, __shfl_xor_sync(kFull, lo, o));
+            hi = max_nan(hi, __shfl_xor_sync(kFull, hi, o));
         }
     }
-    __device__ __forceinline__ float low(int h) const { return __uint_as_float(h ? lo & 0xffff0000u : lo << 16); }
-    __device__ __forceinline__ float high(int h) const { return __uint_as_float(h ? hi & 0xffff0000u : hi << 16); }
-    __device__ __forceinline__ bool bad(int h) const { return (h ? top >> 16 : top & 0xffffu) >= 0x7e80u; }   // 2^126
+    __device__ __forceinline__ void join_halves() {
+        lo = min_nan(lo, __byte_perm(lo, 0u, 0x1032));
+        hi = max_nan(hi, __byte_perm(hi, 0u, 0x1032));
+    }
+    __device__ __forceinline__ float low(bool h) const { return __uint_as_float(h ? lo & 0xffff0000u : lo << 16); }
+    __device__ __forceinline__ float high(bool h) const { return __uint_as_float(h ? hi & 0xffff0000u : hi << 16); }
 };
 
 struct Group {
@@ -135,12 +152,14 @@ struct Group {
 };
 
 // The group's parameters.  Only this rounds in a direction: m down and s up,
-// so that [m, m + 15 s] covers the group and no code needs a clamp.  A bad
-// group's m and inv are zero, so that its codes are, unless a value times zero
-// is NaN, whose bits the caller masks off like any other's.
-__device__ __forceinline__ Group group_of(float low, float high, bool bad) {
-    Group g{0.f, 0.f, 0x7fc00000u};   // step 0, minimum NaN
-    if (bad) return g;
+// so that [m, m + 15 s] covers the group and no code needs a clamp.  A group
+// that holds something not finite (or 2^126 and more) has pair kBad, and the
+// caller masks its codes off.
+constexpr uint32_t kBad = 0x7fc00000u;   // step 0, minimum NaN
+
+__device__ __forceinline__ Group group_of(float low, float high) {
+    Group g{0.f, 0.f, kBad};
+    if (!(low > -0x1p126f && high < 0x1p126f)) return g;   // NaN compares false
     const uint32_t lo = __float_as_uint(low);
     uint32_t m = lo & 0xffff0000u;
     if ((lo >> 31) && (lo & 0xffffu)) m += 0x10000u;   // negative: towards the larger magnitude
@@ -166,120 +185,134 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], float m, float 
     return u;
 }
 
-// grid (row tiles, 2): blockIdx.y selects K or V.
+// Eight lanes take the K and the V row of one (token, head).
 template <typename T, int HD, int G>
 __global__ void __launch_bounds__(kQ4Threads)
     q4_write_kernel(const T *__restrict__ k, const T *__restrict__ v, uint8_t *__restrict__ k_cache,
                     uint8_t *__restrict__ v_cache, const int64_t *__restrict__ slot_mapping, uint32_t rows,
-                    uint32_t num_kv_heads, int bs_shift, long long num_slots, int32_t *status) {
+                    uint32_t num_kv_heads, const Divisor by_heads, int bs_shift, long long num_slots, int32_t *status) {
     using F = Q4Format<HD, G>;
     constexpr int W = F::W, NG = F::GROUPS;
     const int lane = threadIdx.x & 31, g = lane & 7;
     const uint32_t r = blockIdx.x * (kQ4Threads / 8) + threadIdx.x / 8;
     const bool live = r < rows;
-    const uint32_t t = (live ? r : 0u) / num_kv_heads, h = r - t * num_kv_heads;
+    const uint32_t t = by_heads.of(live ? r : 0u), h = r - t * num_kv_heads;
     const int64_t slot = live ? slot_mapping[t] : -1;
     const bool ok = slot >= 0 && slot < num_slots;
-    if (slot >= num_slots && g == 0 && h == 0 && blockIdx.y == 0) flag_status(status, PA_STATUS_BAD_SLOT);
+    if (slot >= num_slots && g == 0 && h == 0) flag_status(status, PA_STATUS_BAD_SLOT);
 
-    const T *src = (blockIdx.y ? v : k) + static_cast<long long>(live ? r : 0u) * HD + 4 * g;
-    Extremes<T> ends[W];
+    const long long at = static_cast<long long>(live ? r : 0u) * HD + 4 * g;
+    const T *src[2] = {k + at, v + at};
+    Extremes<T> ends[2][W];
 #pragma unroll
-    for (int w = 0; w < W; ++w) ends[w].take(src + 64 * w);
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int w = 0; w < W; ++w) ends[w].join_octet();
-    // Lane i of the octet (modulo the groups) works out group i.
-    float low = 0.f, high = 0.f;
-    bool bad = false;
+        for (int w = 0; w < W; ++w) ends[c][w].take(src[c] + 64 * w);
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-        const Extremes<T> &e = ends[G == 64 ? i : i / 2];
-        const float l = G == 64 ? fminf(e.low(0), e.low(1)) : e.low(i & 1);
-        const float u = G == 64 ? fmaxf(e.high(0), e.high(1)) : e.high(i & 1);
-        const bool b = G == 64 ? e.bad(0) || e.bad(1) : e.bad(i & 1);
-        if ((g & (NG - 1)) == i) {
-            low = l;
-            high = u;
-            bad = b;
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            ends[c][w].join_octet();
+            if constexpr (G == 64) ends[c][w].join_halves();
         }
-    }
-    const Group mine = group_of(low, high, bad);
-    const unsigned bads = __ballot_sync(kFull, bad) >> (lane & ~7);
-    uint32_t word[W];
+    // Lane i of the octet's first four (modulo the groups) works out K's group
+    // i, the last four V's.
+    const bool of_v = g & 4, second = W == 2 && (g & (NG / 2)), upper = G == 32 && (g & 1);
+    const Extremes<T> ek = second ? ends[0][W - 1] : ends[0][0], ev = second ? ends[1][W - 1] : ends[1][0];
+    const Extremes<T> e = of_v ? ev : ek;
+    const Group mine = group_of(e.low(upper), e.high(upper));
+    const unsigned bads = __ballot_sync(kFull, mine.pair == kBad) >> (lane & ~7);
+    uint32_t word[2][W];
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-        word[w] = 0;
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const int i = G == 64 ? w : 2 * w + hf;
-            const float m = __shfl_sync(kFull, mine.m, (lane & ~7) + i), inv = __shfl_sync(kFull, mine.inv, (lane & ~7) + i);
-            float x[4];
-            load4(src + 64 * w + 32 * hf, x);   // again: in a register or the L1
-            const uint32_t codes = (bads >> i) & 1u ? 0u : encode4(x, m, inv);
-            word[w] |= hf ? codes << 16 : codes & 0xffffu;
+        for (int w = 0; w < W; ++w) {
+            word[c][w] = 0;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int from = 4 * c + (G == 64 ? w : 2 * w + hf);
+                const float m = __shfl_sync(kFull, mine.m, (lane & ~7) + from);
+                const float inv = __shfl_sync(kFull, mine.inv, (lane & ~7) + from);
+                float x[4];
+                load4(src[c] + 64 * w + 32 * hf, x);   // again: in a register or the L1
+                const uint32_t codes = encode4(x, m, inv) & ((bads >> from) & 1u ? 0u : 0xffffu);
+                word[c][w] |= codes << (16 * hf);
+            }
         }
-    }
     if (!ok) return;
     const int bs = 1 << bs_shift;
     const int row = static_cast<int>(slot & (bs - 1));
-    uint8_t *page = (blockIdx.y ? v_cache : k_cache) +
-                    ((slot >> bs_shift) * num_kv_heads + h) * (static_cast<long long>(F::ROW_BYTES) << bs_shift);
-    uint32_t *to = reinterpret_cast<uint32_t *>(page + row * F::CODE_BYTES) + g * W;
-    if constexpr (W == 2)
-        *reinterpret_cast<uint2 *>(to) = make_uint2(word[0], word[W - 1]);
-    else
-        *to = word[0];
-    if (g < NG) reinterpret_cast<uint32_t *>(page + bs * F::CODE_BYTES + row * F::PARAM_BYTES)[g] = mine.pair;
+    const long long page = ((slot >> bs_shift) * num_kv_heads + h) * (static_cast<long long>(F::ROW_BYTES) << bs_shift);
+    const long long code_at = page + row * F::CODE_BYTES + 4 * W * g;
+    if constexpr (W == 2) {
+        *reinterpret_cast<uint2 *>(k_cache + code_at) = make_uint2(word[0][0], word[0][W - 1]);
+        *reinterpret_cast<uint2 *>(v_cache + code_at) = make_uint2(word[1][0], word[1][W - 1]);
+    } else {
+        *reinterpret_cast<uint32_t *>(k_cache + code_at) = word[0][0];
+        *reinterpret_cast<uint32_t *>(v_cache + code_at) = word[1][0];
+    }
+    if ((g & 3) < NG)
+        *reinterpret_cast<uint32_t *>((of_v ? v_cache : k_cache) + page + bs * F::CODE_BYTES + row * F::PARAM_BYTES +
+                                      4 * (g & 3)) = mine.pair;
 }
 
 template <typename T, int HD, int G>
 __global__ void __launch_bounds__(kQ4Threads)
     q4_gather_kernel(T *__restrict__ k, T *__restrict__ v, const uint8_t *__restrict__ k_cache,
                      const uint8_t *__restrict__ v_cache, const int64_t *__restrict__ slot_mapping, uint32_t rows,
-                     uint32_t num_kv_heads, int bs_shift, long long num_slots, int32_t *status) {
+                     uint32_t num_kv_heads, const Divisor by_heads, int bs_shift, long long num_slots, int32_t *status) {
     using F = Q4Format<HD, G>;
     constexpr int W = F::W, NG = F::GROUPS;
     const int g = threadIdx.x & 7;
     const uint32_t r = blockIdx.x * (kQ4Threads / 8) + threadIdx.x / 8;
     if (r >= rows) return;
-    const uint32_t t = r / num_kv_heads, h = r - t * num_kv_heads;
+    const uint32_t t = by_heads.of(r), h = r - t * num_kv_heads;
     const int64_t slot = slot_mapping[t];
     if (slot < 0) return;
     if (slot >= num_slots) {
-        if (g == 0 && h == 0 && blockIdx.y == 0) flag_status(status, PA_STATUS_BAD_SLOT);
+        if (g == 0 && h == 0) flag_status(status, PA_STATUS_BAD_SLOT);
         return;
     }
     const int bs = 1 << bs_shift;
     const int row = static_cast<int>(slot & (bs - 1));
-    const uint8_t *page = (blockIdx.y ? v_cache : k_cache) +
-                          ((slot >> bs_shift) * num_kv_heads + h) * (static_cast<long long>(F::ROW_BYTES) << bs_shift);
-    const uint32_t *from = reinterpret_cast<const uint32_t *>(page + row * F::CODE_BYTES) + g * W;
-    uint32_t word[W], pair[NG];
-    if constexpr (W == 2) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(from);
-        word[0] = x.x;
-        word[W - 1] = x.y;
-    } else {
-        word[0] = *from;
-    }
+    const long long page = ((slot >> bs_shift) * num_kv_heads + h) * (static_cast<long long>(F::ROW_BYTES) << bs_shift);
+    const long long code_at = page + row * F::CODE_BYTES + 4 * W * g, par_at = page + bs * F::CODE_BYTES + row * F::PARAM_BYTES;
+    uint32_t word[2][W], pair[2][NG];
 #pragma unroll
-    for (int i = 0; i < NG; ++i)
-        pair[i] = reinterpret_cast<const uint32_t *>(page + bs * F::CODE_BYTES + row * F::PARAM_BYTES)[i];
-    T *dst = (blockIdx.y ? v : k) + static_cast<long long>(r) * HD + 4 * g;
-#pragma unroll
-    for (int w = 0; w < W; ++w)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t p = pair[G == 64 ? w : 2 * w + hf], u = hf ? word[w] >> 16 : word[w];
-            float x[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                // 2^23 + code; step * code is exact in fp32 (8 by 4 bits), so the sum rounds once
-                const float c = __uint_as_float(((u >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f;
-                x[j] = fmaf(c, q4_step(p), q4_min(p));
-            }
-            put4(dst + 64 * w + 32 * hf, x);
+    for (int c = 0; c < 2; ++c) {
+        const uint8_t *cache = c ? v_cache : k_cache;
+        if constexpr (W == 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(cache + code_at);
+            word[c][0] = x.x;
+            word[c][W - 1] = x.y;
+        } else {
+            word[c][0] = *reinterpret_cast<const uint32_t *>(cache + code_at);
         }
+        if constexpr (NG == 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(cache + par_at);
+            pair[c][0] = x.x, pair[c][1] = x.y, pair[c][NG - 2] = x.z, pair[c][NG - 1] = x.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NG; ++i) pair[c][i] = reinterpret_cast<const uint32_t *>(cache + par_at)[i];
+        }
+    }
+    const long long at = static_cast<long long>(r) * HD + 4 * g;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t p = pair[c][G == 64 ? w : 2 * w + hf], u = word[c][w];
+                float x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // 2^23 + code; step * code is exact in fp32 (8 by 4 bits), so the sum rounds once
+                    const float code = __uint_as_float(((u >> (16 * hf + 4 * j)) & 15u) | 0x4b000000u) - 8388608.f;
+                    x[j] = fmaf(code, q4_step(p), q4_min(p));
+                }
+                put4((c ? v : k) + at + 64 * w + 32 * hf, x);
+            }
 }
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -332,7 +365,7 @@ struct Call {
     cudaStream_t stream;
     dim3 grid() const {
         constexpr int per = kQ4Threads / 8;
-        return dim3(static_cast<unsigned>((rows + per - 1) / per), 2);
+        return dim3(static_cast<unsigned>((rows + per - 1) / per));
     }
 };
 
@@ -342,7 +375,7 @@ struct WriteLaunch : Call {
         q4_write_kernel<T, HD, G><<<grid(), kQ4Threads, 0, stream>>>(
             static_cast<const T *>(k), static_cast<const T *>(v), static_cast<uint8_t *>(k_cache),
             static_cast<uint8_t *>(v_cache), slot_mapping, static_cast<uint32_t>(rows),
-            static_cast<uint32_t>(num_kv_heads), bs_shift, num_slots, status);
+            static_cast<uint32_t>(num_kv_heads), Divisor(num_kv_heads), bs_shift, num_slots, status);
     }
 };
 
@@ -352,7 +385,7 @@ struct GatherLaunch : Call {
         q4_gather_kernel<T, HD, G><<<grid(), kQ4Threads, 0, stream>>>(
             static_cast<T *>(k), static_cast<T *>(v), static_cast<const uint8_t *>(k_cache),
             static_cast<const uint8_t *>(v_cache), slot_mapping, static_cast<uint32_t>(rows),
-            static_cast<uint32_t>(num_kv_heads), bs_shift, num_slots, status);
+            static_cast<uint32_t>(num_kv_heads), Divisor(num_kv_heads), bs_shift, num_slots, status);
     }
 };
 
