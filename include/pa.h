@@ -187,8 +187,9 @@ size_t pa_decode_workspace_size(int num_seqs, int num_q_heads, int head_dim,
  * blocks between the sinks and the window may have been given back: their
  * table entries may hold anything.  The fused cache write works as in
  * pa_decode.  args->simt must be 0 for PA_BF16 (PA_ERR_UNSUPPORTED).
- * Everything else, types, layouts, checks, determinism, as pa_decode; the
- * workspace is sized by what is visible. */
+ * args->partition_size 0 picks by the batch's sizes (equal partitions of what
+ * the window shows).  Everything else, types, layouts, checks, determinism, as
+ * pa_decode; the workspace is sized by what is visible. */
 int pa_decode_window(void *out, const void *q, const void *k_cache, const void *v_cache,
                      const int32_t *block_tables, const int32_t *context_lens,
                      int num_q_heads, int num_kv_heads, int head_dim, int block_size,
@@ -196,8 +197,9 @@ int pa_decode_window(void *out, const void *q, const void *k_cache, const void *
 
 /* Bytes of workspace pa_decode_window needs (0 when no sequence can show it
  * more than one partition, and for a window or sink count it refuses). */
-size_t pa_decode_window_workspace_size(int num_seqs, int num_q_heads, int head_dim, int max_context_len,
-                                       int partition_size, int window, int num_sinks);
+size_t pa_decode_window_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                       int max_context_len, int partition_size, int window, int num_sinks,
+                                       int dtype);
 
 /* ---- decode attention without a caller workspace ----------------------
  * The paper has no counterpart to this call; it is a convenience of this
@@ -465,7 +467,11 @@ int pa_gather_q4(void *k, void *v, const void *k_cache, const void *v_cache, con
  * the cache holds.  args->dtype is the type of q and out; products and sums
  * are in fp32 or more.  A block id out of range reads as zeros (flagged).
  * args->partition_size is 0 (the library picks) or a multiple of 32 in
- * [32, 1024]; args->simt must be 0 and k_new, v_new and slot_mapping NULL
+ * [32, 1024]: contexts of up to so many tokens are never split, longer ones are
+ * cut wherever that makes the GPU's warps' shares equal, no finer than that.
+ * Results are deterministic for given inputs, sizes and GPU.  No counter is
+ * used, so skip_counter_reset says nothing, and a workspace may be shared with
+ * pa_decode under the same rule of one call at a time; args->simt must be 0 and k_new, v_new and slot_mapping NULL
  * (PA_ERR_UNSUPPORTED): pa_reshape_and_cache_q4 writes the step's tokens. */
 int pa_decode_q4(void *out, const void *q, const void *k_cache, const void *v_cache,
                  const int32_t *block_tables, const int32_t *context_lens, int num_q_heads, int num_kv_heads,

@@ -125,7 +125,7 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.pa_decode_window.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, i32, i32,
                                      ctypes.POINTER(_DecodeArgs)]
     lib.pa_decode_window_workspace_size.restype = sz
-    lib.pa_decode_window_workspace_size.argtypes = [i32] * 7
+    lib.pa_decode_window_workspace_size.argtypes = [i32] * 9
     lib.pa_decode_q4.restype = i32
     lib.pa_decode_q4.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, i32,
                                  ctypes.POINTER(_DecodeArgs)]
@@ -263,10 +263,11 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache
     return call(stream)
 
 
-def pa_decode_window_workspace_size(num_seqs: int, num_q_heads: int, head_dim: int, max_context_len: int,
-                                    partition_size: int = 0, *, window: int, num_sinks: int = 0) -> int:
-    return int(_lib.pa_decode_window_workspace_size(num_seqs, num_q_heads, head_dim, max_context_len,
-                                                    partition_size, window, num_sinks))
+def pa_decode_window_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                    max_context_len: int, partition_size: int = 0, *, window: int,
+                                    num_sinks: int = 0, dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(_lib.pa_decode_window_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                                                    partition_size, window, num_sinks, _dtype_code(dtype)))
 
 
 def pa_decode_window(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -331,8 +332,8 @@ def _decode_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, ma
             or block_tables.shape[0] != S or tuple(context_lens.shape) != (S,)):
         raise ValueError("inconsistent shapes")
     if window:
-        need = pa_decode_window_workspace_size(S, Hq, hd, max_context_len, partition_size, window=window,
-                                               num_sinks=num_sinks)
+        need = pa_decode_window_workspace_size(S, Hq, Hkv, hd, max_context_len, partition_size, window=window,
+                                               num_sinks=num_sinks, dtype=q.dtype)
     else:
         need = pa_decode_workspace_size(S, Hq, hd, max_context_len, partition_size)
     workspace, skip_counter_reset = _workspace(workspace, need, skip_counter_reset, dev)

@@ -565,6 +565,41 @@ int launch_bf16_any(const DecodeParams &p, const void *k_cache, const void *v_ca
 
 int effective_partition(int partition_size) { return partition_size == 0 ? 512 : partition_size; }
 
+// Partition size of a windowed call that leaves it to the library.  A window
+// makes every long sequence's walk the same length, so equal partitions exist
+// and the time of each count n of them can be estimated before the launch.
+// With rows = (sequence, KV head, head tile), `slots` CTAs at a time and T =
+// walk / n tokens per item, a wave of `a` items takes T max(t1, a t2), where t1
+// is a CTA's time per token with the memory to itself and a t2 its share of the
+// bandwidth; items come in waves, each costing `start` more, and n > 1 adds the
+// merge launch and its partials.  Constants measured at head_dim 128 (bf16 12.2
+// ns, fp32 30 ns per token alone; 6.6 TB/s), window 512 to 4096, 8 to 1024 rows;
+// e.g. 8 rows x 531 tokens: n = 9 takes 7.5 us, n = 1 10.6; 256 x 1043: n = 1
+// 25.0, n = 2 39.5; 512 x 4115: n = 4 166, n = 9 172, n = 33 212.
+int window_partition(int num_seqs, int num_kv_heads, int group, int head_dim, bool f32, int walk) {
+    constexpr double start = 0.5, first = 4.0, merge = 2.2, bytes_per_us = 6.6e6;
+    const int tile = f32 ? 8 : 16;
+    const double rows = static_cast<double>(num_seqs) * num_kv_heads * ((group + tile - 1) / tile);
+    const double slots = 152.0 * (head_dim == 128 ? 3 : 4);
+    const double t1 = (f32 ? 30e-3 : 12.2e-3) * head_dim / 128, t2 = 2.0 * head_dim * (f32 ? 4 : 2) / bytes_per_us;
+    const int least = (walk + 4095) / 4096, most = (walk + 63) / 64 < 64 ? (walk + 63) / 64 : 64;
+    int best = 4096;
+    double best_us = 1e30;
+    for (int n = least; n <= (most > least ? most : least); ++n) {
+        const int T = ((walk + n - 1) / n + 15) / 16 * 16;
+        const double items = rows * n, waves = static_cast<double>(static_cast<long long>(items / slots));
+        const double rest = items - waves * slots;
+        const auto wave = [&](double a) { return T * (a * t2 > t1 ? a * t2 : t1); };
+        double us = first + waves * (wave(slots) + start) + (rest > 0 ? wave(rest) + start : 0);
+        if (n > 1) us += merge + rows * n * group / ((group + tile - 1) / tile) * (head_dim + 2) * 8 / bytes_per_us;
+        if (us < best_us) {
+            best_us = us;
+            best = T < 4096 ? T : 4096;
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 cudaError_t pa::launch_merge(const DecodeParams &p, bool f32, int head_dim, cudaStream_t st) {
@@ -636,9 +671,13 @@ int decode_any(void *out, const void *q, const void *k_cache, const void *v_cach
     const int arc = check_decode_args(out, q, k_cache, v_cache, block_tables, context_lens, num_q_heads,
                                       num_kv_heads, head_dim, block_size, a);
     if (arc != PA_OK) return arc;
-    const int P = effective_partition(a->partition_size);
     const long long total_rows = static_cast<long long>(a->num_blocks) * num_kv_heads * block_size;
     const int ctx_cap = context_cap(a, block_size);
+    // Chosen by max_context_len, not by the table's width, as the workspace is sized.
+    const int P = window && a->partition_size == 0
+                      ? window_partition(a->num_seqs, num_kv_heads, num_q_heads / num_kv_heads, head_dim,
+                                         a->dtype == PA_F32, seen_cap(a->max_context_len, window, num_sinks, pa::kChunk))
+                      : effective_partition(a->partition_size);
     // A window longer than any sequence, or sinks past its end, change nothing.
     if (window > ctx_cap) window = ctx_cap > 0 ? ctx_cap : 1;
     if (num_sinks > ctx_cap) num_sinks = ctx_cap;
@@ -735,11 +774,17 @@ extern "C" int pa_decode(void *out, const void *q, const void *k_cache, const vo
                       block_size, scale, 0, 0, a);
 }
 
-extern "C" size_t pa_decode_window_workspace_size(int num_seqs, int num_q_heads, int head_dim, int max_context_len,
-                                                  int partition_size, int window, int num_sinks) {
-    if (window <= 0 || num_sinks < 0) return 0;
-    return pa_decode_workspace_size(num_seqs, num_q_heads, head_dim, seen_cap(max_context_len, window, num_sinks, pa::kChunk),
-                                    partition_size);
+extern "C" size_t pa_decode_window_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                                  int max_context_len, int partition_size, int window, int num_sinks,
+                                                  int dtype) {
+    if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || head_dim <= 0 ||
+        max_context_len <= 0 || window <= 0 || num_sinks < 0 || (dtype != PA_F32 && dtype != PA_BF16))
+        return 0;
+    const int walk = seen_cap(max_context_len, window, num_sinks, pa::kChunk);
+    const int P = partition_size == 0 ? window_partition(num_seqs, num_kv_heads, num_q_heads / num_kv_heads, head_dim,
+                                                         dtype == PA_F32, walk)
+                                      : partition_size;
+    return pa_decode_workspace_size(num_seqs, num_q_heads, head_dim, walk, P);
 }
 
 extern "C" int pa_decode_window(void *out, const void *q, const void *k_cache, const void *v_cache,

@@ -37,9 +37,6 @@
 #ifndef PA_Q4_CPS
 #define PA_Q4_CPS 3
 #endif
-#ifndef PA_Q4_MINP
-#define PA_Q4_MINP 128
-#endif
 #ifndef PA_Q4_WARPS
 #define PA_Q4_WARPS 4
 #endif
@@ -962,7 +959,14 @@ int launch_any(const DecodeParams &p, const Q4Launch &c, int head_dim, int group
     return group_size == 64 ? launch_tile<T, 64, 64>(p, c) : launch_tile<T, 64, 32>(p, c);
 }
 
-int q4_partition(int partition_size) { return partition_size == 0 ? PA_Q4_MINP : partition_size; }
+// Contexts of up to so many tokens are not split, others no finer.  Splitting
+// costs the join (about 2 us) and is worth it where rows alone do not fill the
+// GPU: of 8 x 300 tokens P = 64 takes 8.9 us, unsplit 12.1; of 512 x 300, 16.2
+// and 12.7; of 8 x 100, 9.4 and 7.2; of 512 x 1000, 25 and 31.
+int q4_partition(int partition_size, long long rows, int walk_cap) {
+    if (partition_size != 0) return partition_size;
+    return walk_cap <= 128 ? 128 : rows >= 512 && walk_cap <= 512 ? 512 : 64;
+}
 
 // Query heads per row: a tile of 8, or two for larger groups.
 int q4_tile(int group) { return group > 8 ? 16 : 8; }
@@ -986,17 +990,15 @@ constexpr int kQ4MaxBlock = 32;
 
 extern "C" size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                               int max_context_len, int partition_size, int window, int num_sinks) {
-    const int P = pa::q4_partition(partition_size);
     if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || head_dim <= 0 ||
-        max_context_len <= 0 || P < pa::kUnit || window < 0 || num_sinks < 0)
+        max_context_len <= 0 || window < 0 || num_sinks < 0 || (partition_size != 0 && partition_size < pa::kUnit))
         return 0;
     const int group = num_q_heads / num_kv_heads, tile = pa::q4_tile(group);
     const long long heads = static_cast<long long>(num_kv_heads) * ((group + tile - 1) / tile);
+    const int walk = pa::host::seen_cap(max_context_len, window, num_sinks, pa::kQ4MaxBlock);
+    const int P = pa::q4_partition(partition_size, num_seqs * heads, walk);
     size_t ml_at, acc_at;
-    return pa::workspace_bytes(num_seqs, tile, head_dim,
-                               pa::stretches(num_seqs, heads,
-                                             pa::host::seen_cap(max_context_len, window, num_sinks, pa::kQ4MaxBlock), P),
-                               &ml_at, &acc_at);
+    return pa::workspace_bytes(num_seqs, tile, head_dim, pa::stretches(num_seqs, heads, walk, P), &ml_at, &acc_at);
 }
 
 extern "C" int pa_decode_q4(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -1025,14 +1027,15 @@ extern "C" int pa_decode_q4(void *out, const void *q, const void *k_cache, const
         return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_q4: bad num_blocks, max_blocks_per_seq or max_context_len");
     if (window < 0 || num_sinks < 0)
         return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_q4: window and num_sinks must not be negative");
-    const int P = pa::q4_partition(a->partition_size);
-    if (P < 32 || P > 1024 || P % 32 != 0)
+    if (a->partition_size != 0 && (a->partition_size < 32 || a->partition_size > 1024 || a->partition_size % 32 != 0))
         return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_q4: partition_size must be a multiple of 32 in [32, 1024]");
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
         return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_q4: out, q and caches must be 16-byte aligned");
 
     const long long table_cap = static_cast<long long>(a->max_blocks_per_seq) * block_size;
     const int ctx_cap = static_cast<int>(a->max_context_len < table_cap ? a->max_context_len : table_cap);
+    // The walk the workspace is sized for, which also picks the split.
+    const int sized_walk = seen_cap(a->max_context_len, window, num_sinks, pa::kQ4MaxBlock);
     // No window is one that no sequence outgrows; sinks past the end change nothing.
     if (window == 0 || window > ctx_cap) window = ctx_cap > 0 ? ctx_cap : 1;
     if (num_sinks > ctx_cap) num_sinks = ctx_cap;
@@ -1067,6 +1070,7 @@ extern "C" int pa_decode_q4(void *out, const void *q, const void *k_cache, const
     if (static_cast<long long>(a->num_seqs) * heads * (walk_cap / pa::kUnit + 1ll + pa::kRowCost) >= INT_MAX ||
         static_cast<long long>(a->num_seqs) * num_q_heads >= INT_MAX)
         return pa_fail(PA_ERR_UNSUPPORTED, "pa_decode_q4: 2^31 or more units of 32 tokens");
+    const int P = pa::q4_partition(a->partition_size, a->num_seqs * heads, sized_walk);
     pa::Q4Launch c{k_cache, v_cache, {}, pa::stretches(a->num_seqs, heads, walk_cap, P), P / pa::kUnit, 0, a->phase,
                    static_cast<cudaStream_t>(a->stream)};
     if (c.stretches) {

@@ -47,8 +47,8 @@ class DecodeStep:
         self.out = torch.empty_like(q)
         S, Hq, hd = q.shape
         if window:
-            ws = binding.pa_decode_window_workspace_size(S, Hq, hd, max_context_len, partition_size, window=window,
-                                                         num_sinks=num_sinks)
+            ws = binding.pa_decode_window_workspace_size(S, Hq, k_cache.shape[1], hd, max_context_len, partition_size,
+                                                         window=window, num_sinks=num_sinks, dtype=q.dtype)
         else:
             ws = binding.pa_decode_workspace_size(S, Hq, hd, max_context_len, partition_size)
         self.workspace = _own_workspace(workspace, ws, q.device)

@@ -39,11 +39,28 @@ def test_bad_arguments_are_refused_on_the_host(pa, change, code):
 
 
 def test_workspace_is_sized_by_what_is_visible(pa):
-    size = pa.pa_decode_window_workspace_size
-    assert size(4, 8, 128, 10**6, 512, window=400, num_sinks=4) == 0
-    assert size(4, 8, 128, 10**6, 512, window=600, num_sinks=4) == pa.pa_decode_workspace_size(4, 8, 128, 631, 512)
-    assert size(4, 8, 128, 700, 512, window=10**9, num_sinks=10**9) == pa.pa_decode_workspace_size(4, 8, 128, 700, 512)
-    assert size(4, 8, 128, 700, 512, window=0) == 0
+    size = lambda *a, **k: pa.pa_decode_window_workspace_size(4, 8, 2, 128, *a, **k)
+    plain = lambda tokens, P: pa.pa_decode_workspace_size(4, 8, 128, tokens, P)
+    assert size(10**6, 512, window=400, num_sinks=4) == 0
+    assert size(10**6, 512, window=600, num_sinks=4) == plain(631, 512)
+    assert size(700, 512, window=10**9, num_sinks=10**9) == plain(700, 512)
+    assert size(700, 512, window=0) == 0 and size(700, 0, window=5, num_sinks=-1) == 0
+    assert pa.pa_decode_window_workspace_size(4, 8, 3, 128, 700, 0, window=64) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_library_picks_equal_partitions(pa, dtype):
+    """partition_size 0: few rows are cut finely, many short ones not at all, and
+    the longest windows fit the largest partition."""
+    size = lambda S, W: pa.pa_decode_window_workspace_size(S, 64, 8, 128, 10**6, 0, window=W, num_sinks=4, dtype=dtype)
+    a256 = lambda x: (x + 255) // 256 * 256
+    parts = lambda S, W: next(n for n in range(2, 10**5) if size(S, W) ==
+                              256 + a256(S * n * 64 * 8) + a256(S * n * 64 * 128 * 4))
+    assert parts(1, 512) >= 5
+    if dtype == torch.bfloat16:
+        assert size(32, 512) == 0 and size(64, 512) == 0
+    assert 2 <= parts(64, 4096) <= 9
+    assert parts(1, 10**6) >= 10**6 // 4096
 
 
 def test_binding_and_step_refuse_bad_windows(pa):
