@@ -345,16 +345,19 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
             const int s = n_issued % NSTAGE;
             const uint32_t dst = wbuf_s + s * STAGE_BYTES, bar = bar_s + 8 * s;
             fence_proxy_async_smem();
-            mbar_arrive_expect_tx(bar, ((a >= 0) + (b >= 0)) * 2 * page_bytes);
-            if (a >= 0) {
-                const long long at = (long long)a * page_bytes;
-                bulk_load_hint(dst, k_cache + at, page_bytes, bar, kv_policy);
-                bulk_load_hint(dst + HALF_BYTES, v_cache + at, page_bytes, bar, kv_policy);
-            }
-            if (b >= 0) {
-                const long long at = (long long)b * page_bytes;
-                bulk_load_hint(dst + page_bytes, k_cache + at, page_bytes, bar, kv_policy);
-                bulk_load_hint(dst + HALF_BYTES + page_bytes, v_cache + at, page_bytes, bar, kv_policy);
+            auto copy = [&](int page, uint32_t to) {
+                const long long at = (long long)page * page_bytes;
+                bulk_load_hint(to, k_cache + at, page_bytes, bar, kv_policy);
+                bulk_load_hint(to + HALF_BYTES, v_cache + at, page_bytes, bar, kv_policy);
+            };
+            if ((a | (bs == 16 ? b : 0)) >= 0) {   // a unit's usual case: all its pages
+                mbar_arrive_expect_tx(bar, STAGE_BYTES);
+                copy(a, dst);
+                if (bs == 16) copy(b, dst + page_bytes);
+            } else {
+                mbar_arrive_expect_tx(bar, ((a >= 0) + (b >= 0)) * 2 * page_bytes);
+                if (a >= 0) copy(a, dst);
+                if (b >= 0) copy(b, dst + page_bytes);
             }
         }
         ++n_issued;
