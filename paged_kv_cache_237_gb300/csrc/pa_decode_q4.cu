@@ -181,8 +181,8 @@ constexpr uint32_t kRowCost = PA_Q4_ROWCOST;
 __device__ __forceinline__ uint32_t row_places(int seen) { return row_units(seen) + kRowCost; }
 
 // T: type of q and out.  fp32 splits q and the weights into two fp16 parts.
-// NT: tiles of 8 query heads per work item.
-template <typename T, int HD, int G, int NT>
+// NT: tiles of 8 query heads per row.  bs: block size.
+template <typename T, int HD, int G, int NT, int bs>
 __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
     decode_q4_kernel(const uint8_t *__restrict__ k_cache, const uint8_t *__restrict__ v_cache, const DecodeParams p,
                      const Q4Split split, uint32_t warps, uint32_t min_share) {
@@ -211,10 +211,10 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
     __syncwarp();
 
     // Where the 16-token halves of a stage begin: two pages, or one of 32 rows.
-    const int bs = p.block_size, bs_shift = bs == 32 ? 5 : 4;
-    const int page_bytes = bs * F::ROW_BYTES;
-    const int code_half = bs == 16 ? page_bytes : 16 * F::CODE_BYTES;
-    const int par_0 = bs * F::CODE_BYTES, par_half = bs == 16 ? page_bytes : 16 * F::PARAM_BYTES;
+    constexpr int bs_shift = bs == 32 ? 5 : 4;
+    constexpr int page_bytes = bs * F::ROW_BYTES;
+    constexpr int code_half = bs == 16 ? page_bytes : 16 * F::CODE_BYTES;
+    constexpr int par_0 = bs * F::CODE_BYTES, par_half = bs == 16 ? page_bytes : 16 * F::PARAM_BYTES;
     // Token of matrix row g (row g + 8 is 8 further): neighbours swapped in
     // every other pair, so that a lane octet's reads of V hit both halves of
     // the banks.
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
     uint32_t qm[NT][2];
     float o[MT][NT][4];         // [row g or g + 8][column]: sums of w * code, see below
     float om[NT][2][NG];        // this lane's tokens' sum of p * m
-    float ref[NT][2], l[NT][2];
+    float less[NT][4], l[NT][2];   // minus the columns' references, as an accumulator; sums of p
     float S[NG], inv[NG];       // w = p * s * inv, inv = 4 / S
 
     int slot = 0, page_a, page_b, next_a, next_b;
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
             for (int mt = 0; mt < MT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                ref[nt][c] = 0.f;
+                less[nt][c] = less[nt][c + 2] = 0.f;
                 l[nt][c] = 0.f;
 #pragma unroll
                 for (int i = 0; i < NG; ++i) om[nt][c][i] = 0.f;
@@ -490,8 +490,9 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
             ++n_done;
             uint8_t *stage = wbuf + s * STAGE_BYTES;
             const int v0 = tok_begin + k * kUnit;
-            float bias[2][2] = {{0.f, 0.f}, {0.f, 0.f}};   // of this lane's tokens' scores: -inf where masked
-            if (some_bad || v0 < all_from || v0 + kUnit > all_to) {
+            uint32_t hidden = 0;   // bits of this lane's tokens: 2 half + row, set where masked
+            const bool masked = some_bad || v0 < all_from || v0 + kUnit > all_to;
+            if (masked) {
                 // A block id out of range reads as zeros, and a masked token's
                 // parameters become zeros (its codes are finite whatever they are).
                 const bool bad[2] = {__shfl_sync(kFull, page_a, k) == -1, __shfl_sync(kFull, page_b, k) == -1};
@@ -510,8 +511,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                             *reinterpret_cast<uint32_t *>(at) = 0u;
                             *reinterpret_cast<uint32_t *>(at + HALF_BYTES) = 0u;
                         }
-                    bias[half][0] = (mask >> row_g) & 1u ? 0.f : -INFINITY;
-                    bias[half][1] = (mask >> (row_g + 8)) & 1u ? 0.f : -INFINITY;
+                    hidden |= ((~mask >> row_g) & 1u) << (2 * half) | ((~mask >> (row_g + 8)) & 1u) << (2 * half + 1);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -526,7 +526,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < NG; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
+                    for (int i = 0; i < NG; ++i)
+                        if (SPLIT) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
                 uint32_t w0[OW], w1[OW];   // the lane's words of rows g and g + 8
                 const uint8_t *r0 = Kc + row_g * F::CODE_BYTES + t * 4 * OW, *r1 = r0 + 8 * F::CODE_BYTES;
                 if constexpr (OW == 4) {
@@ -559,23 +560,27 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int q = 0; q < PARTS; ++q) {
-                            mma_f16_16816(acc[nt][i], a0, qf[q][nt][j][0], qf[q][nt][j][1]);
+                            if (!SPLIT && (G == 32 || (j & 1) == 0))   // the group's first
+                                mma_f16_16816(acc[nt][i], a0, qf[q][nt][j][0], qf[q][nt][j][1], 0.f);
+                            else
+                                mma_f16_16816(acc[nt][i], a0, qf[q][nt][j][0], qf[q][nt][j][1]);
                             mma_f16_16816(acc[nt][i], a1, qf[q][nt][j][2], qf[q][nt][j][3]);
                         }
                 }
                 // sc: the scores less their references
                 float y[NT][4];
+                if constexpr (SPLIT) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) y[nt][c] = bias[half][c >> 1] - ref[nt][c & 1];
-                if constexpr (!SPLIT) {
+                        for (int c = 0; c < 4; ++c) y[nt][c] = less[nt][c];
+                } else {
                     const uint8_t *at = Kp + row_g * F::PARAM_BYTES + 4 * (t & (NG - 1));
                     const uint32_t a0 = *reinterpret_cast<const uint32_t *>(at);
                     const uint32_t a1 = *reinterpret_cast<const uint32_t *>(at + 8 * F::PARAM_BYTES);
                     const uint32_t a[4] = {a0, a1, a0, a1};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(y[nt], a, qm[nt][0], qm[nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(y[nt], a, qm[nt][0], qm[nt][1], less[nt]);
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
@@ -596,6 +601,16 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                             sc[half][nt][c] = fmaf(x, qs[nt][col], y[nt][c]);
                         }
                 }
+            }
+
+            if (masked) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if ((hidden >> (2 * half + (c >> 1))) & 1u) sc[half][nt][c] = -INFINITY;
             }
 
             // ---- weights.  w = p s inv in fp16 (inv = 4 / S, S a power of two)
@@ -646,7 +661,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                         // by how much; a column of NaN alone stays where it is
                         rise[nt][c] = !fresh ? fmaxf(mx, 0.f) : mx == -INFINITY ? 0.f : mx;
                         alpha[nt][c] = !fresh ? ex2(-rise[nt][c]) : 0.f;
-                        ref[nt][c] += rise[nt][c];
+                        less[nt][c] -= rise[nt][c];
+                        less[nt][c + 2] = less[nt][c];
                         l[nt][c] *= alpha[nt][c];
                         keep = fmaxf(keep, alpha[nt][c]);
 #pragma unroll
@@ -813,7 +829,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                         store4(split.acc + (part0 + head) * HD + 4 * u, v);
                 }
                 if (!whole && g == 0)
-                    *reinterpret_cast<float2 *>(split.ml + (part0 + head) * 2) = make_float2(ref[nt][c], l[nt][c]);
+                    *reinterpret_cast<float2 *>(split.ml + (part0 + head) * 2) = make_float2(-less[nt][c], l[nt][c]);
             }
         }   // last
         slot ^= 1;
@@ -922,13 +938,13 @@ struct Q4Launch {
     cudaStream_t stream;
 };
 
-template <typename T, int HD, int G, int NT>
+template <typename T, int HD, int G, int NT, int bs>
 int launch_one(const DecodeParams &p, const Q4Launch &c) {
     if (c.phase != PA_PHASE_REDUCE) {
         constexpr int NS = Q4Shape<HD, NT>::NSTAGE;
         constexpr int SMEM = kQ4Warps * NS * (2 * kUnit * Q4Format<HD, G>::ROW_BYTES + 8);
         static KernelSlot slot;
-        auto kernel = decode_q4_kernel<T, HD, G, NT>;
+        auto kernel = decode_q4_kernel<T, HD, G, NT, bs>;
         const int occ = ensure_kernel(kernel, slot, SMEM, c.dev, kQ4Warps * 32);
         if (occ == 0) return pa_fail(PA_ERR_CUDA, "pa_decode_q4: cannot configure the kernel");
         const long long rows = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.head_tiles;
@@ -953,7 +969,8 @@ int launch_one(const DecodeParams &p, const Q4Launch &c) {
 
 template <typename T, int HD, int G>
 int launch_tile(const DecodeParams &p, const Q4Launch &c) {
-    return p.group > 8 ? launch_one<T, HD, G, 2>(p, c) : launch_one<T, HD, G, 1>(p, c);
+    if (p.block_size == 32) return p.group > 8 ? launch_one<T, HD, G, 2, 32>(p, c) : launch_one<T, HD, G, 1, 32>(p, c);
+    return p.group > 8 ? launch_one<T, HD, G, 2, 16>(p, c) : launch_one<T, HD, G, 1, 16>(p, c);
 }
 
 template <typename T>
