@@ -34,16 +34,6 @@
 #include "pa_decode_common.cuh"
 #include "pa_q4.cuh"
 
-#ifndef PA_Q4_CPS
-#define PA_Q4_CPS 3
-#endif
-#ifndef PA_Q4_WARPS
-#define PA_Q4_WARPS 4
-#endif
-#ifndef PA_Q4_NST
-#define PA_Q4_NST 2
-#endif
-
 namespace pa {
 namespace {
 
@@ -137,15 +127,20 @@ __device__ __forceinline__ float pow2_above(float x) {
     return __uint_as_float((__float_as_uint(c) + 0x800000u) & 0x7f800000u);
 }
 
-// Launch shape per head_dim: stages per warp and the CTAs per SM the kernel is
-// built for.
+constexpr int kQ4Warps = 4;   // per CTA; they are independent
+
+// Launch shape: stages per warp, and the CTAs per SM the kernel is built for.
+// The pass is bound by instruction issue, so it wants registers (161 of 168)
+// before warps: 3 CTAs of 4 warps take 206 us on 256 sequences x 16..8192
+// tokens (GQA 64/8, groups of 64), 4 CTAs at 128 registers 218.  Four warps per
+// CTA keep the SM's four schedulers evenly loaded, which equal stretches need:
+// 12 or 14 CTAs of one warp take 10 to 15 % longer.
 template <int HD, int NT>
 struct Q4Shape {
-    static constexpr int NSTAGE = HD == 128 ? PA_Q4_NST : PA_Q4_NST + 1;
-    static constexpr int CPS = NT == 2 ? 8 / PA_Q4_WARPS : PA_Q4_CPS;
+    static constexpr int NSTAGE = HD == 128 ? 2 : 3;
+    static constexpr int CPS = NT == 2 ? 2 : 3;
 };
 
-constexpr int kQ4Warps = PA_Q4_WARPS;   // per CTA; they are independent
 constexpr int kUnit = 32;   // tokens per stage: one block of 32 or two of 16
 
 // Where a warp stands on the axis, kept in shared memory.
@@ -174,10 +169,7 @@ __device__ __forceinline__ uint32_t row_units(int seen) { return seen > kUnit ? 
 
 // A row takes kRowCost more places on the axis than it has units, before them:
 // what beginning and ending a row costs a warp, in units.
-#ifndef PA_Q4_ROWCOST
-#define PA_Q4_ROWCOST 3
-#endif
-constexpr uint32_t kRowCost = PA_Q4_ROWCOST;
+constexpr uint32_t kRowCost = 3;   // 256 sequences x 16..8192 tokens: 0 takes 244 us, 3 211, 5 212, 8 216
 __device__ __forceinline__ uint32_t row_places(int seen) { return row_units(seen) + kRowCost; }
 
 // T: type of q and out.  fp32 splits q and the weights into two fp16 parts.
@@ -869,7 +861,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_q4_kernel(const DecodePa
     auto at = [&](int i) { return ((long long)(w0 + i) * 2 + (i == 0)) * rows + r; };
     constexpr int E = HD / 32;   // values per lane
     using Vec = typename std::conditional<E == 4, float4, float2>::type;
-    constexpr int FETCH = 16;    // partials on their way at a time
+    // Partials on their way at a time (registers for 16 halve the warps per SM:
+    // 256 sequences' 16384 rows 9.4 us against 7.2; 4 lengthen the longest rows).
+    constexpr int FETCH = 8;
     float M = -INFINITY, L = 0.f;
     float acc[E] = {};
     for (int i0 = 0; i0 < parts; i0 += FETCH) {

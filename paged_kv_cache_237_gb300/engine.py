@@ -101,12 +101,14 @@ class DecodeStep:
         return self.decode(stream)
 
 
-def _own_workspace(workspace: torch.Tensor | None, need: int, device) -> torch.Tensor | None:
-    """The workspace a step keeps: the one given (checked), a zeroed one, or None when it needs none."""
+def _own_workspace(workspace: torch.Tensor | None, need: int, device, zeroed: int | None = None):
+    """The workspace a step keeps: the one given (checked), a new one (its first
+    ``zeroed`` bytes, or all of it, zero), or None when it needs none."""
     if workspace is not None and workspace.numel() < need:
         raise ValueError(f"workspace has {workspace.numel()} bytes, {need} needed")
     if workspace is None and need:
-        workspace = torch.zeros(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace[:zeroed].zero_()
     return workspace if need else None
 
 
@@ -131,7 +133,8 @@ class Q4DecodeStep:
         _, Hkv, self.block_size = binding._q4_geometry(k_cache, v_cache, hd, group_size, q.device)
         ws = binding.pa_decode_q4_workspace_size(S, Hq, Hkv, hd, max_context_len, partition_size, window=window,
                                                  num_sinks=num_sinks)
-        self.workspace = _own_workspace(workspace, ws, q.device)
+        # only the header has to be zero, for a pa_decode call that may use it later
+        self.workspace = _own_workspace(workspace, ws, q.device, zeroed=256)
         self._call = binding._decode_q4_call(self.out, q, k_cache, v_cache, block_tables, context_lens, scale,
                                              max_context_len, group_size, window, num_sinks, partition_size,
                                              self.workspace, self.status, binding.PA_PHASE_ALL, True)

@@ -277,6 +277,26 @@ def test_bad_blocks_and_lengths_are_flagged(pa, bs, group):
     check(out, case, 0.09, bs, group, what="clamped length")
 
 
+@pytest.mark.gpu
+def test_batches_of_nothing_and_of_many_short_rows(pa):
+    """No token anywhere; and more rows than the GPU has warps, most of them empty or short, split and unsplit."""
+    for dtype in (torch.bfloat16, torch.float32):
+        case = make([0, 0, 0], 8, 2, 128, 16, 64, dtype, 1)
+        for ctx in (1, 5000):
+            q, kc, vc, tables, lens = case
+            out = torch.full(q.shape, 5.0, dtype=dtype, device="cuda")
+            pa.pa_decode_q4(out, q.cuda(), torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(),
+                            torch.from_numpy(np.repeat(tables, 320, 1)).cuda(), torch.from_numpy(lens).cuda(), 0.09,
+                            max_context_len=ctx, group_size=64)
+            assert (out == 0).all()
+        lens = np.random.default_rng(2).choice([0, 1, 2, 16, 31, 33, 64, 70, 130], size=700).tolist()
+        case = make(lens, 8, 8, 64, 16, 32, dtype, 2)
+        for P in (0, 32, 256):
+            out, flags = on_gpu(pa, case, 0.125, 32, dtype, partition_size=P)
+            assert flags == 0
+            check(out, case, 0.125, 16, 32, what=f"{dtype} P {P}")
+
+
 def step(pa, case, group, **kw):
     from paged_kv_cache_237_gb300.engine import Q4DecodeStep
     q, kc, vc, tables, lens = case
