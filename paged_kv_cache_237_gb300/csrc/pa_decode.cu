@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kWarps * 32, bf16_ctas_per_sm<HD>())
 // One CTA per (query head, sequence): the threads first take M over all
 // partitions, then each warp sums a strided subset of the partitions (lanes own
 // 4 consecutive head_dim values) and the warps' sums are added in shared memory.
-template <typename OutT, int HD, int kReduceWarps>
+template <typename OutT, int HD, int kReduceWarps, bool WIN>
 __global__ void __launch_bounds__(kReduceWarps * 32) decode_reduce_kernel(const DecodeParams p) {
     // A following pass may be scheduled as soon as every merge CTA is running
     // (it waits for this grid before reading anything).
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) decode_reduce_kernel(const 
     // writes them in sequence order, so the last sequences' are still in L2.
     const int seq = p.reduce_newest_first ? p.num_seqs - 1 - static_cast<int>(blockIdx.y)
                                           : static_cast<int>(blockIdx.y);
-    const int n = p.window ? seq_view<true>(p, seq).seen : seq_len(p, seq);
+    const int n = seq_view<WIN>(p, seq).seen;
     if (n <= p.partition_size) return;
     const int np = (n + p.partition_size - 1) / p.partition_size;
     const long long base = (long long)seq * p.max_parts * p.num_q_heads + qh;
@@ -536,8 +536,8 @@ int launch_bf16(const DecodeParams &p, const void *k_cache, const void *v_cache,
 // partitions over more warps, read as they are summed).
 constexpr int kReduceMaxPartsSmall = 64;
 
-template <typename OutT, int HD>
-cudaError_t launch_reduce(const DecodeParams &p, cudaStream_t st) {
+template <typename OutT, int HD, bool WIN>
+cudaError_t launch_reduce_as(const DecodeParams &p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     const bool small = p.max_parts <= kReduceMaxPartsSmall;
     cfg.gridDim = dim3(p.num_q_heads, p.num_seqs);
@@ -549,8 +549,13 @@ cudaError_t launch_reduce(const DecodeParams &p, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return small ? cudaLaunchKernelEx(&cfg, pa::decode_reduce_kernel<OutT, HD, 4>, p)
-                 : cudaLaunchKernelEx(&cfg, pa::decode_reduce_kernel<OutT, HD, 8>, p);
+    return small ? cudaLaunchKernelEx(&cfg, pa::decode_reduce_kernel<OutT, HD, 4, WIN>, p)
+                 : cudaLaunchKernelEx(&cfg, pa::decode_reduce_kernel<OutT, HD, 8, WIN>, p);
+}
+
+template <typename OutT, int HD>
+cudaError_t launch_reduce(const DecodeParams &p, cudaStream_t st) {
+    return p.window ? launch_reduce_as<OutT, HD, true>(p, st) : launch_reduce_as<OutT, HD, false>(p, st);
 }
 
 template <int HD>
@@ -600,12 +605,12 @@ int window_partition(int num_seqs, int num_kv_heads, int group, int head_dim, bo
     return best;
 }
 
-}  // namespace
-
-cudaError_t pa::launch_merge(const DecodeParams &p, bool f32, int head_dim, cudaStream_t st) {
+cudaError_t launch_merge(const DecodeParams &p, bool f32, int head_dim, cudaStream_t st) {
     if (f32) return head_dim == 128 ? launch_reduce<float, 128>(p, st) : launch_reduce<float, 64>(p, st);
     return head_dim == 128 ? launch_reduce<__nv_bfloat16, 128>(p, st) : launch_reduce<__nv_bfloat16, 64>(p, st);
 }
+
+}  // namespace
 
 extern "C" size_t pa_decode_workspace_size(int num_seqs, int num_q_heads, int head_dim,
                                            int max_context_len, int partition_size) {
@@ -755,7 +760,7 @@ int decode_any(void *out, const void *q, const void *k_cache, const void *v_cach
     }
     if (rc != PA_OK) return rc;
     if (max_parts > 1 && a->phase != PA_PHASE_PARTITIONS) {
-        const cudaError_t le = pa::launch_merge(p, a->dtype == PA_F32, head_dim, st);
+        const cudaError_t le = launch_merge(p, a->dtype == PA_F32, head_dim, st);
         if (le != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(le));
     }
     cudaError_t e = cudaGetLastError();

@@ -101,9 +101,9 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *dst, float4 v) {
 }
 
 // Merge the NW per-warp softmax states held in shared memory (each warp's
-// region starts with float O[ROWS][HD + kEpiPad], then M[ROWS], then L[ROWS])
-// and store either the final rows or the item's partial.
-template <typename OutT, int HD, int NW = kWarps, int ROWS = 16>
+// region starts with float O[16][HD + kEpiPad], then M[16], then L[16]) and
+// store either the final rows or the item's partial.
+template <typename OutT, int HD, int NW = kWarps>
 __device__ void merge_and_store(const uint8_t *smem, int warp_bytes, const DecodeParams &p, int seq,
                                 int part, int qh0, int rows, bool single) {
     constexpr int LD = HD + kEpiPad;
@@ -113,7 +113,7 @@ __device__ void merge_and_store(const uint8_t *smem, int warp_bytes, const Decod
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float *em = reinterpret_cast<const float *>(smem + w * warp_bytes) + ROWS * LD;
+            const float *em = reinterpret_cast<const float *>(smem + w * warp_bytes) + 16 * LD;
             M = fmaxf(M, em[r]);
         }
         float L = 0.f;
@@ -122,8 +122,8 @@ __device__ void merge_and_store(const uint8_t *smem, int warp_bytes, const Decod
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 const float *eo = reinterpret_cast<const float *>(smem + w * warp_bytes);
-                const float f = exp2f(eo[ROWS * LD + r] - M);
-                L += f * eo[ROWS * LD + ROWS + r];
+                const float f = exp2f(eo[16 * LD + r] - M);
+                L += f * eo[16 * LD + 16 + r];
                 const float4 v = *reinterpret_cast<const float4 *>(eo + r * LD + d);
                 acc.x += f * v.x;
                 acc.y += f * v.y;
@@ -248,9 +248,6 @@ __device__ __forceinline__ void finish_handouts(unsigned long long *ctr) {
 // defined in pa_decode_simt.cu.  Enqueues one launch on `st`.
 int launch_simt_pass(const DecodeParams &p, const void *k_cache, const void *v_cache, bool f32, int head_dim,
                      long long items, int dev, cudaStream_t st);
-
-// The split-K merge of a pass's partials (pa_decode.cu).
-cudaError_t launch_merge(const DecodeParams &p, bool f32, int head_dim, cudaStream_t st);
 
 // ------------------------------------------------------- host helpers ---
 namespace host {
