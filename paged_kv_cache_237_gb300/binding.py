@@ -11,7 +11,6 @@ over ``pa_bm_*``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -182,17 +181,24 @@ def _ptr(t: torch.Tensor | None):
     return t.data_ptr() if t is not None else None
 
 
-def _on_device(dev: torch.device):
-    """Makes dev the current device for a call; nothing to do when it is."""
-    if torch._C._cuda_getDevice() == dev.index:
-        return _NOWHERE
-    return torch.cuda.device(dev)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
-_NOWHERE = contextlib.nullcontext()
+def _call(dev: torch.device, fn, *args) -> None:
+    """Calls a library function with dev as the current device."""
+    if _current_device() == dev.index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    if rc:
+        _raise(rc)
 
 
 def _check_cuda(t: torch.Tensor, name: str, dtypes, dev=None):
+    if t.__class__ is torch.Tensor and t.dtype in dtypes and t.is_contiguous() and \
+            (t.device == dev if dev is not None else t.is_cuda):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
@@ -303,12 +309,7 @@ class _PreparedCall:
         a.stream = _stream_ptr(stream, self._device)
         if phase is not None:
             a.phase = phase
-        if torch._C._cuda_getDevice() == self._device.index:
-            rc = self._fn(*self._operands, *self._sizes, self._ref)
-        else:
-            with torch.cuda.device(self._device):
-                rc = self._fn(*self._operands, *self._sizes, self._ref)
-        _raise(rc)
+        _call(self._device, self._fn, *self._operands, *self._sizes, self._ref)
         return self._out
 
 
@@ -471,24 +472,21 @@ def pa_build_tables(block_tables: torch.Tensor, slot_mapping: torch.Tensor, posi
         _check_cuda(t, name, (torch.int32,), dev)
     if block_tables.dim() != 2 or slot_mapping.dim() != 1 or block_ids.dim() != 1:
         raise ValueError("block_tables must be [S, max_blocks], slot_mapping [T], block_ids [N]")
-    S, T = block_tables.shape[0], slot_mapping.shape[0]
-    if tuple(context_lens.shape) != (S,) or tuple(new_lens.shape) != (S,):
+    (S, width), T = block_tables.shape, slot_mapping.shape[0]
+    if context_lens.shape != (S,) or new_lens.shape != (S,):
         raise ValueError("context_lens and new_lens must be [S]")
     if positions is not None:
         _check_cuda(positions, "positions", (torch.int32,), dev)
-        if tuple(positions.shape) != (T,):
+        if positions.shape != (T,):
             raise ValueError("positions must be [T] like slot_mapping")
     if query_start is not None:
         _check_cuda(query_start, "query_start", (torch.int32,), dev)
-        if tuple(query_start.shape) != (S + 1,):
+        if query_start.shape != (S + 1,):
             raise ValueError("query_start must be [S + 1]")
-    with _on_device(dev):
-        rc = _lib.pa_build_tables(block_tables.data_ptr(), slot_mapping.data_ptr(), _ptr(positions),
-                                  _ptr(query_start), block_ids.data_ptr(), context_lens.data_ptr(),
-                                  new_lens.data_ptr(), S, block_tables.shape[1], T, block_ids.shape[0], block_size,
-                                  num_blocks, status.ptr() if status is not None else None,
-                                  _stream_ptr(stream, dev))
-    _raise(rc)
+    _call(dev, _lib.pa_build_tables, block_tables.data_ptr(), slot_mapping.data_ptr(), _ptr(positions),
+          _ptr(query_start), block_ids.data_ptr(), context_lens.data_ptr(), new_lens.data_ptr(), S, width, T,
+          block_ids.shape[0], block_size, num_blocks, status.ptr() if status is not None else None,
+          _stream_ptr(stream, dev))
 
 
 def pa_q4_page_bytes(head_dim: int, block_size: int, group_size: int = 64) -> int:
@@ -597,17 +595,15 @@ def _q4_rows_call(fn, k, v, k_cache, v_cache, slot_mapping, group_size, status, 
     dev = k.device
     _check_cuda(v, "v", (k.dtype,), dev)
     _check_cuda(slot_mapping, "slot_mapping", (torch.int64,), dev)
-    if k.dim() != 3 or v.shape != k.shape or tuple(slot_mapping.shape) != (k.shape[0],):
+    if k.dim() != 3 or v.shape != k.shape or slot_mapping.shape != (k.shape[0],):
         raise ValueError("k, v must be [T, Hkv, hd] and slot_mapping [T]")
     T, Hkv, hd = k.shape
     nb, heads, bs = _q4_geometry(k_cache, v_cache, hd, group_size, dev)
     if heads != Hkv:
         raise ValueError("inconsistent shapes")
-    with _on_device(dev):
-        rc = fn(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, Hkv,
-                hd, bs, group_size, nb, _dtype_code(k.dtype), status.ptr() if status is not None else None,
-                _stream_ptr(stream, dev))
-    _raise(rc)
+    _call(dev, fn, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T,
+          Hkv, hd, bs, group_size, nb, _dtype_code(k.dtype), status.ptr() if status is not None else None,
+          _stream_ptr(stream, dev))
 
 
 class BlockManager:
