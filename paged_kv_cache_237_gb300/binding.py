@@ -265,7 +265,7 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache
     """
     call = _decode_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
                         partition_size, workspace, status, phase, k_new, v_new, slot_mapping, simt,
-                        skip_counter_reset)
+                        skip_counter_reset, stream=stream)
     return call(stream)
 
 
@@ -291,7 +291,7 @@ def pa_decode_window(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, 
         raise ValueError("window must be at least 1 and num_sinks at least 0")
     call = _decode_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
                         partition_size, workspace, status, phase, k_new, v_new, slot_mapping, False,
-                        skip_counter_reset, window, num_sinks)
+                        skip_counter_reset, window, num_sinks, stream)
     return call(stream)
 
 
@@ -315,7 +315,7 @@ class _PreparedCall:
 
 def _decode_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, partition_size,
                  workspace, status, phase, k_new, v_new, slot_mapping, simt, skip_counter_reset, window=0,
-                 num_sinks=0) -> _PreparedCall:
+                 num_sinks=0, stream=None) -> _PreparedCall:
     """The checks and arguments of pa_decode (window 0) and pa_decode_window."""
     fdt = (torch.float32, torch.bfloat16)
     _check_cuda(q, "q", fdt)
@@ -337,7 +337,7 @@ def _decode_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, ma
                                                num_sinks=num_sinks, dtype=q.dtype)
     else:
         need = pa_decode_workspace_size(S, Hq, hd, max_context_len, partition_size)
-    workspace, skip_counter_reset = _workspace(workspace, need, skip_counter_reset, dev)
+    workspace, skip_counter_reset = _workspace(workspace, need, skip_counter_reset, dev, stream)
     fused = (k_new, v_new, slot_mapping)
     if any(t is not None for t in fused):
         if any(t is None for t in fused):
@@ -366,10 +366,17 @@ def _decode_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, ma
     return _PreparedCall(_lib.pa_decode, out, operands, sizes, args, dev, keep)
 
 
-def _workspace(workspace, need, skip_counter_reset, dev):
-    """The caller's workspace, checked, or a zeroed one when one is needed."""
+def _workspace(workspace, need, skip_counter_reset, dev, stream):
+    """The caller's workspace, checked, or a zeroed one when one is needed: made
+    on the stream that uses it, so that its zeros are there in time and its
+    memory is not handed out again before the call is done with it."""
     if need and workspace is None:
-        return torch.zeros(need, dtype=torch.uint8, device=dev), True
+        if stream is None:
+            return torch.zeros(need, dtype=torch.uint8, device=dev), True
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
+        with torch.cuda.stream(stream):
+            return torch.zeros(need, dtype=torch.uint8, device=dev), True
     if workspace is not None:
         _check_cuda(workspace, "workspace", (torch.uint8,), dev)
     return workspace, skip_counter_reset
@@ -561,11 +568,13 @@ def pa_decode_q4(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_ca
     arguments are those of ``pa_decode``.
     """
     return _decode_q4_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, group_size,
-                           window, num_sinks, partition_size, workspace, status, phase, skip_counter_reset)(stream)
+                           window, num_sinks, partition_size, workspace, status, phase, skip_counter_reset,
+                           stream)(stream)
 
 
 def _decode_q4_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, group_size,
-                    window, num_sinks, partition_size, workspace, status, phase, skip_counter_reset) -> _PreparedCall:
+                    window, num_sinks, partition_size, workspace, status, phase, skip_counter_reset,
+                    stream=None) -> _PreparedCall:
     """The checks and arguments of pa_decode_q4."""
     _check_cuda(q, "q", (torch.float32, torch.bfloat16))
     dev = q.device
@@ -580,7 +589,7 @@ def _decode_q4_call(out, q, k_cache, v_cache, block_tables, context_lens, scale,
         raise ValueError("inconsistent shapes")
     need = pa_decode_q4_workspace_size(S, Hq, Hkv, hd, max_context_len, partition_size, window=window,
                                        num_sinks=num_sinks)
-    workspace, skip_counter_reset = _workspace(workspace, need, skip_counter_reset, dev)
+    workspace, skip_counter_reset = _workspace(workspace, need, skip_counter_reset, dev, stream)
     args = _DecodeArgs(S, block_tables.shape[1], nb, _dtype_code(q.dtype), partition_size, max_context_len,
                        _ptr(workspace), workspace.numel() if workspace is not None else 0,
                        status.ptr() if status is not None else None, None, phase, None, None, None, 0,

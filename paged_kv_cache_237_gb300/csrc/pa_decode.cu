@@ -587,11 +587,12 @@ int window_partition(int num_seqs, int num_kv_heads, int group, int head_dim, bo
     const double rows = static_cast<double>(num_seqs) * num_kv_heads * ((group + tile - 1) / tile);
     const double slots = 152.0 * (head_dim == 128 ? 3 : 4);
     const double t1 = (f32 ? 30e-3 : 12.2e-3) * head_dim / 128, t2 = 2.0 * head_dim * (f32 ? 4 : 2) / bytes_per_us;
-    const int least = (walk + 4095) / 4096, most = (walk + 63) / 64 < 64 ? (walk + 63) / 64 : 64;
+    const int least = walk > 4096 ? (walk - 1) / 4096 + 1 : 1, cuts = walk > 64 ? (walk - 1) / 64 + 1 : 1;
+    const int most = cuts < 64 ? cuts : 64;   // partitions of 64 tokens at least, and not above 64 of them
     int best = 4096;
     double best_us = 1e30;
     for (int n = least; n <= (most > least ? most : least); ++n) {
-        const int T = ((walk + n - 1) / n + 15) / 16 * 16;
+        const int even = walk > 0 ? (walk - 1) / n + 1 : 1, T = (even + 15) / 16 * 16;
         const double items = rows * n, waves = static_cast<double>(static_cast<long long>(items / slots));
         const double rest = items - waves * slots;
         const auto wave = [&](double a) { return T * (a * t2 > t1 ? a * t2 : t1); };

@@ -57,8 +57,8 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t u) {
     return __half22float2(h);
 }
 
-// 2^x to about 2^-22, results below the normals flushed to zero: a weight that
-// small adds nothing to a sum that holds one of 2^-8 or more.
+// 2^x to about 2^-22, results below the normals flushed to zero: weights are
+// relative to one of 1, or more than 2^-5 once others have outgrown it.
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

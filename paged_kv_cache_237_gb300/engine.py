@@ -26,7 +26,9 @@ class DecodeStep:
     status word: pass them in.
 
     With ``window`` (and ``num_sinks``) the step attends to each sequence's
-    last ``window`` tokens and its first ``num_sinks`` (``pa_decode_window``)."""
+    last ``window`` tokens and its first ``num_sinks`` (``pa_decode_window``).
+    A windowed call without a fused write is checked once, so the tensors given
+    are that step's for its life: update them in place."""
 
     def __init__(self, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,

@@ -220,3 +220,46 @@ def test_steps_graphs_and_streams(pa, dtype):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(s.out, first) and s.status.read() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("q4", [False, True])
+def test_a_bound_of_zero_tokens(pa, dtype, q4):
+    """max_context_len 0: every row is empty, and any length is flagged."""
+    q = torch.randn(3, 8, 128).to(dtype).cuda()
+    tables = torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    status = pa.DeviceStatus()
+    for lens, flag in (([0, 0, 0], 0), ([0, 5, 0], pa.STATUS_BAD_CONTEXT_LEN)):
+        out = torch.full_like(q, 3.0)
+        ctx = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        if q4:
+            c = torch.zeros(2, 2, pa.pa_q4_page_bytes(128, 16), dtype=torch.uint8, device="cuda")
+            pa.pa_decode_q4(out, q, c, c, tables, ctx, 0.1, max_context_len=0, status=status, window=4)
+        else:
+            c = torch.zeros(2, 2, 16, 128, dtype=dtype, device="cuda")
+            pa.pa_decode_window(out, q, c, c, tables, ctx, 0.1, max_context_len=0, status=status, window=4)
+        assert (out == 0).all() and status.read() == flag
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_call_on_another_stream_makes_its_workspace_there(pa, raw):
+    """No workspace given, and the current stream is busy: the zeroed workspace
+    has to be made on the stream of the call."""
+    case = make([3000, 700, 2500], 8, 2, 128, 16, torch.bfloat16, 4, 2000, 4)
+    q, kc, vc, tables, lens = [x.cuda() if isinstance(x, torch.Tensor) else torch.from_numpy(x).cuda() for x in case]
+    ref = reference(case, 0.09, 2000, 4)
+    side = torch.cuda.Stream()
+    outs = [torch.empty_like(q) for _ in range(3)]
+    junk = torch.full((64 << 20,), 0xAB, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del junk
+    for out in outs:
+        torch.cuda._sleep(20_000_000)
+        pa.pa_decode_window(out, q, kc, vc, tables, lens, 0.09, window=2000, num_sinks=4, max_context_len=3000,
+                            partition_size=64, stream=side.cuda_stream if raw else side)
+    side.synchronize()
+    for out in outs:
+        assert_decode_close(out, ref, torch.bfloat16)
+    torch.cuda.synchronize()
