@@ -19,9 +19,11 @@
 // ands, and the powers of two are undone where they cost nothing, in q and in
 // the output.  The tensor core aligns a subnormal's products by its nominal
 // exponent, which leaves sums about 17 bits: plenty for a bf16 result (8), not
-// for fp32.  fp32 q and out take codes as the normal value 16 + code (the 16
-// goes into the minimum: s c + m = s (16 + c) + (m - 16 s)), and two fp16 parts
-// of q and of the weights.
+// for fp32.  fp32 q and out take codes as the normal values c - 8 and the
+// middle of the range for the minimum, s c + m = s (c - 8) + (m + 8 s), so that
+// long flat sums do not cancel what a code's offset brought in; two fp16 parts
+// of q and of the weights; and each pair of products in an accumulator of its
+// own, added in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -65,7 +67,7 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// A token's steps and minima; NORMAL codes carry 16 steps more than the value.
+// A token's steps and minima, or (NORMAL: codes less 8) the middles of its ranges.
 template <int NG, bool NORMAL>
 __device__ __forceinline__ void load_pairs(const uint8_t *at, float (&s)[NG], float (&m)[NG]) {
     uint32_t pair[NG];
@@ -81,7 +83,7 @@ __device__ __forceinline__ void load_pairs(const uint8_t *at, float (&s)[NG], fl
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
         s[i] = q4_step(pair[i]);
-        m[i] = NORMAL ? fmaf(-16.f, s[i], q4_min(pair[i])) : q4_min(pair[i]);
+        m[i] = NORMAL ? fmaf(8.f, s[i], q4_min(pair[i])) : q4_min(pair[i]);
     }
 }
 
@@ -89,14 +91,20 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_ca
 
 // The two nibble pairs (a nibble of each half-word) at a time that make the
 // codes of two units fp16 operands: values 0, 1, 2, 3 of both units.  NORMAL:
-// 16 + code.  Otherwise code * 2^-24, and code * 2^-20 for values 1 and 3.
+// code - 8, exactly, by way of 16 + code (whose mantissa holds the code in its
+// upper bits).  Otherwise code * 2^-24, and code * 2^-20 for values 1 and 3.
 template <bool NORMAL>
 __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&r)[4]) {
     if constexpr (NORMAL) {
-        r[0] = ((x << 6) & 0x03c003c0u) | 0x4c004c00u;
-        r[1] = ((x << 2) & 0x03c003c0u) | 0x4c004c00u;
-        r[2] = ((x >> 2) & 0x03c003c0u) | 0x4c004c00u;
-        r[3] = ((x >> 6) & 0x03c003c0u) | 0x4c004c00u;
+        r[0] = x << 6;
+        r[1] = x << 2;
+        r[2] = x >> 2;
+        r[3] = x >> 6;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            r[i] = (r[i] & 0x03c003c0u) | 0x4c004c00u;
+            asm("sub.f16x2 %0, %0, %1;" : "+r"(r[i]) : "r"(0x4e004e00u));   // 24
+        }
     } else {
         r[0] = x & 0x000f000fu;
         r[1] = x & 0x00f000f0u;
@@ -769,9 +777,17 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                             const int mt = 4 * wd + 2 * hf + e;
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
+{
+                                    if constexpr (SPLIT) {
+                                        float d[4];
+                                        mma_f16_16816(d, a, pb[0][nt][i][0], pb[0][nt][i][1], 0.f);
+                                        mma_f16_16816(d, a, pb[PARTS - 1][nt][i][0], pb[PARTS - 1][nt][i][1]);
 #pragma unroll
-                                for (int q = 0; q < PARTS; ++q)
-                                    mma_f16_16816(o[mt][nt], a, pb[q][nt][i][0], pb[q][nt][i][1]);
+                                        for (int c = 0; c < 4; ++c) o[mt][nt][c] += d[c];
+                                    } else {
+                                        mma_f16_16816(o[mt][nt], a, pb[0][nt][i][0], pb[0][nt][i][1]);
+                                    }
+                                }
                         }
                     }
             }

@@ -233,6 +233,36 @@ def test_peaked_and_flat_scores(pa, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hd,group", [(128, 64), (64, 32)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_long_flat_sums_keep_their_precision(pa, dtype, hd, group):
+    """20000 tokens of nearly equal weight and values of mean zero: the output is a
+    hundredth of the values, so an error of the sums' size rather than the
+    output's shows.  In the 2-norm, weights' errors are independent of each
+    other: fp32 parts of a few 2^-23 each (the exponential, the weight's two
+    fp16 parts) stay below 2^-19 relative; for bf16, half a step of the result
+    spread evenly is 2^-8 / sqrt(3), the fp16 weights' 2^-11 / sqrt(3) times the
+    code part's size against the value's (3), and as much again for the sums."""
+    rng = np.random.default_rng(12)
+    case = list(make([20000, 9000], 8, 1, hd, 16, group, dtype, 12))
+    cut = 16 * hd // 2
+    par = case[2][..., cut:].copy().view(np.uint16).reshape(case[2].shape[0], 1, 16, -1, 2)
+    s = torch.from_numpy(par[..., 0].view(np.int16).copy()).view(torch.bfloat16).double().numpy()
+    par[..., 1] = q4_ref.bf16_bits(np.where(np.isfinite(s), -7.5 * s, np.nan))    # ranges about zero
+    case[2] = case[2].copy()
+    case[2][..., cut:] = par.view(np.uint8).reshape(case[2].shape[0], 1, -1)
+    scale = 0.02 * hd ** -0.5
+    out, flags = on_gpu(pa, case, scale, group, dtype)
+    assert flags == 0
+    q, kc, vc, tables, lens = case
+    with np.errstate(invalid="ignore"):
+        k, v = q4_ref.values(kc, 16, hd, group), q4_ref.values(vc, 16, hd, group)
+    ref = q4_ref.attend(q.double().numpy(), k, v, tables, lens, scale, 16)
+    rel = np.linalg.norm(out.double().cpu().numpy() - ref) / np.linalg.norm(ref)
+    assert rel <= (2.0 ** -19 if dtype == torch.float32 else (2.0 ** -8 + 6 * 2.0 ** -11) / 3 ** 0.5), rel
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_nan_in_a_visible_group_shows_in_its_columns_only(pa, dtype):
     """A NaN value group poisons its 32 columns, a NaN key group its whole rows, as an unquantised cache would."""
