@@ -45,11 +45,11 @@ L2_BYTES = 129 * 2**20
 # seeded slice of the same length mix (--num-seqs), scaled to the full launch
 # by the ratio of algorithmic bytes.  Valid only while the kernel source is
 # the one captured.
-TRAFFIC_CAPTURE = {"source_sha256_prefix": "d560969f6ba47ba1",
-                   # 48-sequence slice: 4,143,340,288 B read + 26,654,976 B written
+TRAFFIC_CAPTURE = {"source_sha256_prefix": "ff5a5363b931ec97",
+                   # 48-sequence slice: 4,143,336,448 B read + 26,424,576 B written
                    # over 4,141,526,704 algorithmic bytes, scaled to 20,791,665,640
-                   "bytes_per_launch": {"long_context": 20934586070,
-                                        "gqa_llama3_70b": 902411008 + 6055936}}
+                   "bytes_per_launch": {"long_context": 20933410118,
+                                        "gqa_llama3_70b": 902361600 + 6084096}}
 
 
 KERNEL_FILES = ("pa_decode.cu", "pa_decode_common.cuh", "pa_internal.h")
