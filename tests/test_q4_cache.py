@@ -241,3 +241,32 @@ def test_write_on_another_stream_and_in_a_graph(pa):
     s = sm.cpu().numpy()
     want = torch.from_numpy(q4_ref.values(ref, 16, 128, 64)[s // 16, :, s % 16]).to(x.dtype)
     assert torch.equal(k.cpu(), want) and torch.equal(v.cpu(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wrong,error", [
+    (dict(k=torch.zeros(4, 2, 64, dtype=torch.float16)), TypeError), (dict(v=torch.zeros(4, 2, 64)), TypeError),
+    (dict(v=torch.zeros(4, 2, 128, dtype=torch.bfloat16)), ValueError),
+    (dict(slot_mapping=torch.zeros(4, dtype=torch.int32)), TypeError),
+    (dict(slot_mapping=torch.zeros(3, dtype=torch.int64)), ValueError),
+    (dict(k_cache=torch.zeros(3, 2, 640)), TypeError), (dict(v_cache=torch.zeros(2, 2, 640, dtype=torch.uint8)), ValueError),
+    (dict(k=torch.zeros(4, 64, 2, dtype=torch.bfloat16).transpose(1, 2)), ValueError),
+    (dict(k_cache=torch.zeros(3, 2, 641, dtype=torch.uint8), v_cache=torch.zeros(3, 2, 641, dtype=torch.uint8)), ValueError),
+    (dict(k_cache=torch.zeros(3, 1, 640, dtype=torch.uint8), v_cache=torch.zeros(3, 1, 640, dtype=torch.uint8)), ValueError),
+])
+def test_binding_refuses_wrong_tensors(pa, wrong, error):
+    a = dict(k=torch.zeros(4, 2, 64, dtype=torch.bfloat16), v=torch.zeros(4, 2, 64, dtype=torch.bfloat16),
+             k_cache=torch.zeros(3, 2, 640, dtype=torch.uint8), v_cache=torch.zeros(3, 2, 640, dtype=torch.uint8),
+             slot_mapping=torch.arange(4))
+    a = {k: v.cuda() for k, v in a.items()}
+    for fn in (pa.pa_reshape_and_cache_q4, pa.pa_gather_q4):
+        fn(**a, group_size=32)
+        with pytest.raises(error):
+            fn(**{**a, **{k: v.cuda() for k, v in wrong.items()}}, group_size=32)
+        with pytest.raises(ValueError):
+            fn(**{**a, "v": a["v"].cpu()}, group_size=32)
+        with pytest.raises(ValueError):
+            fn(**a, group_size=48)
+        with pytest.raises(TypeError):
+            fn(**{**a, "k": None}, group_size=32)
+    torch.cuda.synchronize()

@@ -75,6 +75,34 @@ def test_binding_refuses_cpu_tensors(pa):
     with pytest.raises(ValueError):
         pa.pa_build_tables(torch.zeros(2, 3, dtype=torch.int32), i64, None, None, i32, i32, i32, block_size=16,
                            num_blocks=4)
+    with pytest.raises(TypeError):
+        pa.pa_build_tables(None, i64, None, None, i32, i32, i32, block_size=16, num_blocks=4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wrong,error", [
+    (dict(block_tables=torch.zeros(2, 3)), TypeError), (dict(slot_mapping=torch.zeros(4, dtype=torch.int32)), TypeError),
+    (dict(positions=torch.zeros(4)), TypeError), (dict(block_ids=torch.zeros(2, 2, dtype=torch.int32)), ValueError),
+    (dict(context_lens=torch.zeros(3, dtype=torch.int32)), ValueError), (dict(new_lens=torch.zeros(2, 1, dtype=torch.int32)), ValueError),
+    (dict(query_start=torch.zeros(2, dtype=torch.int32)), ValueError), (dict(positions=torch.zeros(3, dtype=torch.int32)), ValueError),
+    (dict(block_tables=torch.zeros(6, dtype=torch.int32)), ValueError),
+    (dict(slot_mapping=torch.zeros(4, 1, dtype=torch.int64)), ValueError),
+    (dict(block_tables=torch.zeros(3, 2, dtype=torch.int32).t()), ValueError),
+])
+def test_binding_refuses_wrong_tensors(pa, wrong, error):
+    a = dict(block_tables=torch.zeros(2, 3, dtype=torch.int32), slot_mapping=torch.zeros(4, dtype=torch.int64),
+             positions=torch.zeros(4, dtype=torch.int32), query_start=torch.zeros(3, dtype=torch.int32),
+             block_ids=torch.zeros(2, dtype=torch.int32), context_lens=torch.zeros(2, dtype=torch.int32),
+             new_lens=torch.zeros(2, dtype=torch.int32))
+    a = {k: v.cuda() for k, v in a.items()}
+    pa.pa_build_tables(**a, block_size=16, num_blocks=4)
+    a.update({k: v.cuda() for k, v in wrong.items()})
+    with pytest.raises(error):
+        pa.pa_build_tables(**a, block_size=16, num_blocks=4)
+    a["context_lens"] = torch.zeros(2, dtype=torch.int32)          # on the CPU
+    with pytest.raises((ValueError, TypeError)):
+        pa.pa_build_tables(**a, block_size=16, num_blocks=4)
+    torch.cuda.synchronize()
 
 
 def test_flat_blocks_lists_every_sequence_in_order(pa):
