@@ -1,19 +1,24 @@
 // Cache write and read of the 4-bit cache for sm_103a (include/pa.h states the
 // format and the quantisation).
 //
-// Both are one pass over the rows.  Eight lanes share a head row; lane g of them
-// owns code words g * W .. g * W + W - 1 (W = HD / 64), whose halves are the
-// units of four values 16 w + g and 16 w + 8 + g.  So a lane loads 2 W pieces of
-// four values, the eight lanes' pieces of one unit row are contiguous, and a
-// group is what the eight lanes hold of one word (64) or one half-word (32):
-// its minimum and maximum are three shuffles.  bf16 values are compared packed,
-// two groups' extremes to a register.
+// Both are one pass over the rows.  Eight lanes take the K and the V row of one
+// (token, head); lane g of them owns code words g * W .. g * W + W - 1 (W = HD /
+// 64), whose halves are the units of four values 16 w + g and 16 w + 8 + g.  So
+// a lane loads 2 W pieces of four values, the eight lanes' pieces of one unit
+// row are contiguous, and a group is what the eight lanes hold of one word (64)
+// or one half-word (32): its minimum and maximum are three shuffles.  bf16
+// values are compared packed, two groups' extremes to a register.
 //
-// The write is bound by instructions before bytes, so each group's parameters
-// (a division and a reciprocal) are worked out by one lane, lane i group i's,
-// and handed round, and a code costs four instructions: subtract, multiply, add
-// 1.5 * 2^23 (which rounds half to even and leaves the code in the low mantissa
-// bits), and a multiply-add that packs it.
+// The write has about as many instructions to issue as bytes to move, so each
+// group's parameters (a division and a reciprocal) are worked out by one lane
+// (lane i K's group i, lane 4 + i V's) and handed round, and a code costs four
+// instructions: subtract, multiply, add 1.5 * 2^23 (which rounds half to even
+// and leaves the code in the low mantissa bits), and a multiply-add that packs
+// it.  Measured on 30011 tokens x 8 heads of 128 bf16 values in groups of 32 (161
+// MB either way, 24 us at the copy peak): write 33.8 us (82.6 with sixteen lanes
+// a row, every lane at the parameters and 64-bit divisions; 37 with 256 threads
+// per CTA), read 28.4 us (50.6; two or four rows a lane change nothing).  32
+// tokens: 1.9 and 1.7 us, the launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -27,7 +32,7 @@
 namespace pa {
 namespace {
 
-constexpr int kQ4Threads = 256;
+constexpr int kQ4Threads = 128;
 
 // r / d for r < 2^31 by a product: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d),
 // m d - 2^(31 + s) < 2^s, so r m / 2^(31 + s) is over r / d by less than 1 / d.
@@ -187,7 +192,7 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], float m, float 
 
 // Eight lanes take the K and the V row of one (token, head).
 template <typename T, int HD, int G>
-__global__ void __launch_bounds__(kQ4Threads)
+__global__ void __launch_bounds__(kQ4Threads, sizeof(T) == 2 ? 12 : 8)
     q4_write_kernel(const T *__restrict__ k, const T *__restrict__ v, uint8_t *__restrict__ k_cache,
                     uint8_t *__restrict__ v_cache, const int64_t *__restrict__ slot_mapping, uint32_t rows,
                     uint32_t num_kv_heads, const Divisor by_heads, int bs_shift, long long num_slots, int32_t *status) {
