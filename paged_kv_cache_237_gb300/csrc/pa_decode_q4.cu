@@ -182,6 +182,7 @@ struct Q4Split {
     uint32_t *bases;             // [S] first place of each sequence
     float *ml, *acc;             // [warps][2][rows][2] and [..][HD]: a row that the stretch
                                  // does not begin (0) or does not end (1)
+    uint32_t stretches;          // that there is room for
 };
 
 __device__ __forceinline__ uint32_t row_units(int seen) { return seen > kUnit ? (seen + kUnit - 1) / kUnit : 1; }
@@ -878,11 +879,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_q4_kernel(const DecodePa
     const long long me = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
     const int seq = static_cast<int>(me / p.num_q_heads), qh = static_cast<int>(me - (long long)seq * p.num_q_heads);
     if (seq >= p.num_seqs) return;
-    const uint32_t share = *split.share, ru = row_units(seq_view<true>(p, seq).seen);
+    const uint32_t share = max(1u, *split.share), ru = row_units(seq_view<true>(p, seq).seen);
     const int kvh = qh / p.group, in_group = qh - kvh * p.group, ht = in_group / rows, r = in_group - ht * rows;
     const uint32_t begin = split.bases[seq] + (kvh * p.head_tiles + ht) * (ru + kRowCost) + kRowCost;
     const uint32_t w0 = begin / share, w1 = (begin + ru - 1) / share;
-    if (w0 == w1) return;   // stored whole
+    // Equal: stored whole.  Past the room, or reversed: a pass that gave up on a
+    // wait, or did not run, left the bases unwritten.
+    if (w0 >= w1 || w1 >= split.stretches) return;
     const int parts = static_cast<int>(w1 - w0) + 1;
     // the stretch that begins the row keeps it in its second slot, the others in their first
     auto at = [&](int i) { return ((long long)(w0 + i) * 2 + (i == 0)) * rows + r; };
@@ -1122,7 +1125,8 @@ extern "C" int pa_decode_q4(void *out, const void *q, const void *k_cache, const
                                              "pa_decode_q4_workspace_size()");
         char *ws = static_cast<char *>(a->workspace);
         c.split = {reinterpret_cast<uint32_t *>(ws + 16), reinterpret_cast<uint32_t *>(ws + kWorkspaceHeader),
-                   reinterpret_cast<float *>(ws + ml_at), reinterpret_cast<float *>(ws + acc_at)};
+                   reinterpret_cast<float *>(ws + ml_at), reinterpret_cast<float *>(ws + acc_at),
+                   static_cast<uint32_t>(c.stretches)};
     }
     if (cudaGetDevice(&c.dev) != cudaSuccess) return pa_fail(PA_ERR_CUDA, "pa_decode_q4: no CUDA device");
     if (sm_count(c.dev) <= 0) return pa_fail(PA_ERR_CUDA, "pa_decode_q4: cannot query the SM count");

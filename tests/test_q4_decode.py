@@ -362,6 +362,21 @@ def test_repeats_phases_and_graphs_give_the_same_bits(pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("word", [-1, 0, 1, 1 << 30, -(1 << 31)])
+def test_a_join_without_its_pass_stays_inside_the_workspace(pa, word):
+    """Places left unwritten (as by a pass that gave up on a wait) are whatever
+    the workspace held: rows that they put past its end are left out."""
+    case = make([900, 33, 2000, 0, 640], 16, 2, 128, 16, 64, torch.bfloat16, 11)
+    s = step(pa, case, 64, partition_size=128)
+    s.workspace.view(torch.int32).fill_(word)
+    s.decode(phase=pa.PA_PHASE_REDUCE)
+    torch.cuda.synchronize()
+    s.out.fill_(float("nan"))
+    check(s.decode(), case, 0.09, 16, 64)
+    assert s.status.read() == 0
+
+
+@pytest.mark.gpu
 def test_two_calls_at_once_on_streams_of_their_own(pa):
     cases = [make([3000, 500], 8, 1, 128, 16, 64, torch.bfloat16, 20 + i) for i in range(2)]
     steps = [step(pa, c, 64, partition_size=64) for c in cases]
