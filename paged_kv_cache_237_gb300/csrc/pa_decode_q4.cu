@@ -193,8 +193,10 @@ constexpr uint32_t kRowCost = 3;   // 256 sequences x 16..8192 tokens: 0 takes 2
 __device__ __forceinline__ uint32_t row_places(int seen) { return row_units(seen) + kRowCost; }
 
 // T: type of q and out.  fp32 splits q and the weights into two fp16 parts.
-// NT: tiles of 8 query heads per row.  bs: block size.
-template <typename T, int HD, int G, int NT, int bs>
+// NT: tiles of 8 query heads per row.  NC: columns of a tile that a lane looks
+// after; 1 where a row has at most 4 heads, which then take the even columns.
+// bs: block size.
+template <typename T, int HD, int G, int NT, int NC, int bs>
 __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
     decode_q4_kernel(const uint8_t *__restrict__ k_cache, const uint8_t *__restrict__ v_cache, const DecodeParams p,
                      const Q4Split split, uint32_t warps, uint32_t min_share) {
@@ -206,7 +208,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
     constexpr int HALF_BYTES = kUnit * F::ROW_BYTES;   // a stage's K, then its V
     constexpr int STAGE_BYTES = 2 * HALF_BYTES;
     constexpr int WARP_BYTES = NSTAGE * STAGE_BYTES;
-    constexpr int ROWS = 8 * NT;
+    constexpr int ROWS = 4 * NC * NT;
+    static_assert(NC == 2 || NT == 1);
     constexpr int OW = HD / 32;    // code words a lane feeds to one token row's products
     constexpr int MT = HD / 16;    // m-tiles of the output
 
@@ -351,41 +354,37 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
         if (bs == 16) page_b = page_of(v + 16);
         return units;
     };
+    // A stage's copies, one lane each: K's and V's page, and (block size 16) those
+    // of the second half.
+    constexpr int COPIES = bs == 16 ? 4 : 2;
+    const bool of_v = lane & 1, of_b = bs == 16 && (lane & 2);
+    const uint8_t *const from = of_v ? v_cache : k_cache;
+    const uint32_t to = wbuf_s + (of_v ? HALF_BYTES : 0) + (of_b ? page_bytes : 0);
     auto issue = [&](int page_a, int page_b, int k) {
-        const int a = __shfl_sync(kFull, page_a, k), b = __shfl_sync(kFull, page_b, k);
-        if (lane == 0) {
+        const int a = __shfl_sync(kFull, page_a, k), b = bs == 16 ? __shfl_sync(kFull, page_b, k) : -1;
+        if (lane < COPIES) {
             const int s = n_issued % NSTAGE;
-            const uint32_t dst = wbuf_s + s * STAGE_BYTES, bar = bar_s + 8 * s;
+            const uint32_t bar = bar_s + 8 * s;
+            const int page = of_b ? b : a;
             fence_proxy_async_smem();
-            auto copy = [&](int page, uint32_t to) {
-                const long long at = (long long)page * page_bytes;
-                bulk_load_hint(to, k_cache + at, page_bytes, bar, kv_policy);
-                bulk_load_hint(to + HALF_BYTES, v_cache + at, page_bytes, bar, kv_policy);
-            };
-            if ((a | (bs == 16 ? b : 0)) >= 0) {   // a unit's usual case: all its pages
-                mbar_arrive_expect_tx(bar, STAGE_BYTES);
-                copy(a, dst);
-                if (bs == 16) copy(b, dst + page_bytes);
-            } else {
-                mbar_arrive_expect_tx(bar, ((a >= 0) + (b >= 0)) * 2 * page_bytes);
-                if (a >= 0) copy(a, dst);
-                if (b >= 0) copy(b, dst + page_bytes);
-            }
+            if (lane == 0) mbar_arrive_expect_tx(bar, ((a >= 0) + (b >= 0)) * 2 * page_bytes);
+            if (page >= 0)
+                bulk_load_hint(to + s * STAGE_BYTES, from + (long long)page * page_bytes, page_bytes, bar, kv_policy);
         }
         ++n_issued;
     };
 
     // A row's state, carried from block to block.
     uint32_t qf[PARTS][NT][OW][4];
-    float qs[NT][2];            // per column (head): undoes q's scaling, times scale * log2(e)
+    float qs[NT][NC];           // per column (head): undoes q's scaling, times scale * log2(e)
     // Sums of q over a group, times scale * log2(e): by column and group, or
     // (bf16) group t's of head g as the coefficient of m in a B operand whose
     // A operand is a row's (s, m) pairs as they are, in two bf16 parts.
-    float qsum[SPLIT ? NT : 1][2][NG];
+    float qsum[SPLIT ? NT : 1][NC][NG];
     uint32_t qm[NT][2];
     float o[MT][NT][4];         // [row g or g + 8][column]: sums of w * code, see below
-    float om[NT][2][NG];        // this lane's tokens' sum of p * m
-    float less[NT][4], l[NT][2];   // minus the columns' references, as an accumulator; sums of p
+    float om[NT][NC][NG];       // this lane's tokens' sum of p * m
+    float less[NT][4], l[NT][NC];  // minus the columns' references, as an accumulator; sums of p
     float S[NG], inv[NG];       // w = p * s * inv, inv = 4 / S
 
     int slot = 0, page_a, page_b, next_a, next_b;
@@ -407,8 +406,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
         // fp16's 11), and by 16 where a code comes out 16 times too large.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int head = 8 * nt + g;
-            const bool live = head < it.rows;
+            const int head = NC == 2 ? 8 * nt + g : g / 2;   // of column g
+            const bool live = head < it.rows && (NC == 2 || g % 2 == 0);
             const T *qb = static_cast<const T *>(p.q) +
                           ((long long)it.seq * p.num_q_heads + it.qh0 + (live ? head : 0)) * HD;
             float4 lo[OW], hi[OW];
@@ -449,7 +448,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                     }
                 }
             }
-            // To the columns of the accumulators: heads 2 t and 2 t + 1.
+            // To the columns of the accumulators: 2 t and 2 t + 1.
             const float back = p.scale_log2 * (SPLIT ? 1.f : 0x1p24f) * pow2i(e);
             float own = 0.f;
 #pragma unroll
@@ -458,7 +457,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                 if (t == i) own = sum[i];
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < NC; ++c) {
                 qs[nt][c] = __shfl_sync(kFull, back, 4 * (2 * t + c));
                 if constexpr (SPLIT)
 #pragma unroll
@@ -480,8 +479,9 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                less[nt][c] = less[nt][c + 2] = 0.f;
+            for (int c = 0; c < 4; ++c) less[nt][c] = 0.f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
                 l[nt][c] = 0.f;
 #pragma unroll
                 for (int i = 0; i < NG; ++i) om[nt][c][i] = 0.f;
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
             }
 
             // ---- S = K Q^T: rows are tokens, columns heads; one accumulator per group.
-            float sc[2][NT][4];
+            float sc[2][NT][2 * NC];   // of row g + 8 r and column 2 t + c at NC r + c
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const uint8_t *Kc = stage + half * code_half, *Kp = stage + par_0 + half * par_half;
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int col = 0; col < 2; ++col) {
+                        for (int col = 0; col < NC; ++col) {
                             const int c = 2 * r + col;
                             float x = ks[0] * acc[nt][0][c];
                             if constexpr (SPLIT) y[nt][c] = fmaf(km[0], qsum[nt][col][0], y[nt][c]);
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                                 x = fmaf(ks[i], acc[nt][i][c], x);
                                 if constexpr (SPLIT) y[nt][c] = fmaf(km[i], qsum[nt][col][i], y[nt][c]);
                             }
-                            sc[half][nt][c] = fmaf(x, qs[nt][col], y[nt][c]);
+                            sc[half][nt][NC * r + col] = fmaf(x, qs[nt][col], y[nt][c]);
                         }
                 }
             }
@@ -621,8 +621,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if ((hidden >> (2 * half + (c >> 1))) & 1u) sc[half][nt][c] = -INFINITY;
+                        for (int c = 0; c < 2 * NC; ++c)
+                            if ((hidden >> (2 * half + c / NC)) & 1u) sc[half][nt][c] = -INFINITY;
             }
 
             // ---- weights.  w = p s inv in fp16 (inv = 4 / S, S a power of two)
@@ -630,10 +630,10 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
             // as they are.  What would pass fp16's range is seen by sums, which the
             // FMA pipe has room for: while this lane's p sum to at most 2^5 a head and
             // its s inv to at most 2^10, no w passes 2^15.
-            float pr[2][NT][4], sw[2][2][NG];   // p, and s inv of this lane's tokens
-            float sum[NT][2], most = 0.f, wide = 0.f;
+            float pr[2][NT][2 * NC], sw[2][2][NG];   // p, and s inv of this lane's tokens
+            float sum[NT][NC], most = 0.f, wide = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) sum[nt][0] = sum[nt][1] = 0.f;
+            for (int nt = 0; nt < NT; ++nt) sum[nt][0] = sum[nt][NC - 1] = 0.f;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const uint8_t *Vp = stage + HALF_BYTES + par_0 + half * par_half;
@@ -650,24 +650,24 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2 * NC; ++c) {
                         pr[half][nt][c] = ex2(sc[half][nt][c]);
-                        sum[nt][c & 1] += pr[half][nt][c];
+                        sum[nt][c % NC] += pr[half][nt][c];
                     }
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) most = fmaxf(most, fmaxf(sum[nt][0], sum[nt][1]));   // passes NaN over
+            for (int nt = 0; nt < NT; ++nt) most = fmaxf(most, fmaxf(sum[nt][0], sum[nt][NC - 1]));   // passes NaN over
             const bool fresh = first && k == 0;
             if (fresh || __any_sync(kFull, most > 32.f || wide > 1024.f)) {
                 // Raise the references to the running maxima (a row's first unit
                 // sets them), choose S anew above every p s and a sixteenth of every
                 // s, and take p again.  Rare after the first unit.
-                float alpha[NT][2], rise[NT][2], keep = 0.f;
+                float alpha[NT][NC], rise[NT][NC], keep = 0.f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float mx = fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][c + 2]), fmaxf(sc[1][nt][c], sc[1][nt][c + 2]));
+                    for (int c = 0; c < NC; ++c) {
+                        float mx = fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][c + NC]), fmaxf(sc[1][nt][c], sc[1][nt][c + NC]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
                         // by how much; a column of NaN alone stays where it is
@@ -682,13 +682,13 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                     }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    sum[nt][0] = sum[nt][1] = 0.f;
+                    sum[nt][0] = sum[nt][NC - 1] = 0.f;
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            pr[half][nt][c] = ex2(sc[half][nt][c] - rise[nt][c & 1]);
-                            sum[nt][c & 1] += pr[half][nt][c];
+                        for (int c = 0; c < 2 * NC; ++c) {
+                            pr[half][nt][c] = ex2(sc[half][nt][c] - rise[nt][c % NC]);
+                            sum[nt][c % NC] += pr[half][nt][c];
                         }
                 }
                 // (s inv is back to s by 1 / inv = S / 4, exactly)
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                         float most_p = 0.0625f;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            most_p = fmaxf(most_p, fmaxf(pr[half][nt][2 * r], pr[half][nt][2 * r + 1]));
+                            most_p = fmaxf(most_p, fmaxf(pr[half][nt][NC * r], pr[half][nt][NC * r + NC - 1]));
 #pragma unroll
                         for (int i = 0; i < NG; ++i) top[i] = fmaxf(top[i], most_p * sw[half][r][i]);
                     }
@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) o[mt][nt][c] *= alpha[nt][c & 1] * ratio;
+                                for (int c = 0; c < 4; ++c) o[mt][nt][c] *= alpha[nt][c % NC] * ratio;   // (NC 1: column 2 t + 1 is zero)
                 }
             }
 
@@ -740,17 +740,18 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < NC; ++c) {
                         if (half == 0) l[nt][c] += sum[nt][c];
 #pragma unroll
                         for (int i = 0; i < NG; ++i)
-                            om[nt][c][i] = fmaf(pr[half][nt][c], mv[0][i], fmaf(pr[half][nt][c + 2], mv[1][i], om[nt][c][i]));
+                            om[nt][c][i] = fmaf(pr[half][nt][c], mv[0][i], fmaf(pr[half][nt][c + NC], mv[1][i], om[nt][c][i]));
                     }
 #pragma unroll
                     for (int i = 0; i < NG; ++i)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const float x = pr[half][nt][2 * r] * sw[half][r][i], y = pr[half][nt][2 * r + 1] * sw[half][r][i];
+                            const float x = pr[half][nt][NC * r] * sw[half][r][i];
+                            const float y = NC == 2 ? pr[half][nt][NC * r + NC - 1] * sw[half][r][i] : 0.f;
                             const uint32_t h = pack_f16(x, y);
                             pb[0][nt][i][r] = movmatrix_trans(h);
                             if constexpr (SPLIT) {
@@ -819,14 +820,14 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < NC; ++c) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) {
                     l[nt][c] += __shfl_xor_sync(kFull, l[nt][c], d);
 #pragma unroll
                     for (int i = 0; i < NG; ++i) om[nt][c][i] += __shfl_xor_sync(kFull, om[nt][c][i], d);
                 }
-                const int head = 8 * nt + 2 * t + c;
+                const int head = 8 * nt + NC * t + c;
                 if (head >= it.rows) continue;
                 // a row without a token has l = 0 and zero sums; NaN stays NaN
                 const float norm = !whole ? 1.f : l[nt][c] == 0.f ? 0.f : 1.f / l[nt][c];
@@ -962,13 +963,13 @@ struct Q4Launch {
     cudaStream_t stream;
 };
 
-template <typename T, int HD, int G, int NT, int bs>
+template <typename T, int HD, int G, int NT, int NC, int bs>
 int launch_one(const DecodeParams &p, const Q4Launch &c) {
     if (c.phase != PA_PHASE_REDUCE) {
         constexpr int NS = Q4Shape<HD, NT>::NSTAGE;
         constexpr int SMEM = kQ4Warps * NS * (2 * kUnit * Q4Format<HD, G>::ROW_BYTES + 8);
         static KernelSlot slot;
-        auto kernel = decode_q4_kernel<T, HD, G, NT, bs>;
+        auto kernel = decode_q4_kernel<T, HD, G, NT, NC, bs>;
         const int occ = ensure_kernel(kernel, slot, SMEM, c.dev, kQ4Warps * 32);
         if (occ == 0) return pa_fail(PA_ERR_CUDA, "pa_decode_q4: cannot configure the kernel");
         const long long rows = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.head_tiles;
@@ -985,22 +986,27 @@ int launch_one(const DecodeParams &p, const Q4Launch &c) {
     if (c.stretches && c.phase != PA_PHASE_PARTITIONS) {
         const long long ctas = (static_cast<long long>(p.num_seqs) * p.num_q_heads + kJoinWarps - 1) / kJoinWarps;
         const cudaError_t e = launch_dependent(join_q4_kernel<T, HD>, static_cast<int>(ctas), kJoinWarps * 32, 0,
-                                               c.stream, p, c.split, 8 * NT);
+                                               c.stream, p, c.split, 4 * NC * NT);
         if (e != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
     }
     return PA_OK;
 }
 
-template <typename T, int HD, int G>
+template <typename T, int HD, int G, int bs>
 int launch_tile(const DecodeParams &p, const Q4Launch &c) {
-    if (p.block_size == 32) return p.group > 8 ? launch_one<T, HD, G, 2, 32>(p, c) : launch_one<T, HD, G, 1, 32>(p, c);
-    return p.group > 8 ? launch_one<T, HD, G, 2, 16>(p, c) : launch_one<T, HD, G, 1, 16>(p, c);
+    if (p.group > 8) return launch_one<T, HD, G, 2, 2, bs>(p, c);
+    return p.group > 4 ? launch_one<T, HD, G, 1, 2, bs>(p, c) : launch_one<T, HD, G, 1, 1, bs>(p, c);
+}
+
+template <typename T, int HD, int G>
+int launch_block(const DecodeParams &p, const Q4Launch &c) {
+    return p.block_size == 32 ? launch_tile<T, HD, G, 32>(p, c) : launch_tile<T, HD, G, 16>(p, c);
 }
 
 template <typename T>
 int launch_any(const DecodeParams &p, const Q4Launch &c, int head_dim, int group_size) {
-    if (head_dim == 128) return group_size == 64 ? launch_tile<T, 128, 64>(p, c) : launch_tile<T, 128, 32>(p, c);
-    return group_size == 64 ? launch_tile<T, 64, 64>(p, c) : launch_tile<T, 64, 32>(p, c);
+    if (head_dim == 128) return group_size == 64 ? launch_block<T, 128, 64>(p, c) : launch_block<T, 128, 32>(p, c);
+    return group_size == 64 ? launch_block<T, 64, 64>(p, c) : launch_block<T, 64, 32>(p, c);
 }
 
 // Contexts of up to so many tokens are not split, others no finer.  Splitting
@@ -1012,8 +1018,8 @@ int q4_partition(int partition_size, long long rows, int walk_cap) {
     return walk_cap <= 128 ? 128 : rows >= 512 && walk_cap <= 512 ? 512 : 64;
 }
 
-// Query heads per row: a tile of 8, or two for larger groups.
-int q4_tile(int group) { return group > 8 ? 16 : 8; }
+// Query heads per row: half a tile's columns, a tile, or two for larger groups.
+int q4_tile(int group) { return group > 8 ? 16 : group > 4 ? 8 : 4; }
 
 // Workspace: [header: the units per warp at byte 16] [first unit of each
 // sequence] [(max, sum)] [accumulators], two rows of heads per stretch.
