@@ -355,7 +355,9 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
         return units;
     };
     // A stage's copies, one lane each: K's and V's page, and (block size 16) those
-    // of the second half.
+    // of the second half.  (All by one lane: 71.8 us on 64 sequences of GQA 64/4, 69.)
+    // The barrier's count of bytes may go below zero: until lane 0 has arrived, the
+    // phase cannot end.
     constexpr int COPIES = bs == 16 ? 4 : 2;
     const bool of_v = lane & 1, of_b = bs == 16 && (lane & 2);
     const uint8_t *const from = of_v ? v_cache : k_cache;
@@ -868,16 +870,26 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
     }
 }
 
-// Joins the partials of every row that stretches cut: one warp per (sequence,
-// query head).  out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i.
+// Joins the partials of every row that stretches cut.  out = sum_i 2^(m_i - M)
+// acc_i / sum_i 2^(m_i - M) l_i.  PER warps per (sequence, query head).
 constexpr int kJoinWarps = 4;
 
-template <typename T, int HD>
+// A warp takes 8 partials at a time.  Where there are more for a row, four warps
+// share them: the whole call takes 138.4 us rather than 141.6 on 7 sequences of up
+// to 131072 tokens, 50.0 rather than 50.9 on 32 lognormal ones, 8.4 rather than 8.9
+// on one of 777.  Not where there are fewer (64 sequences, GQA 32/8: 134.4 against
+// 132.3) or rows enough to fill the GPU (64 sequences, GQA 64/4: 73.3 against 68.9).
+bool join_by_four(long long stretches, long long rows, long long head_rows, int sms) {
+    return stretches >= 8 * rows && head_rows <= 14ll * sms;
+}
+
+template <typename T, int HD, int PER>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_q4_kernel(const DecodeParams p, const Q4Split split, int rows) {
+    static_assert(PER == 1 || PER == kJoinWarps);
     griddep_launch_dependents();
     griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const long long me = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = PER == 1 ? 0 : warp;
+    const long long me = PER == 1 ? (long long)blockIdx.x * kJoinWarps + warp : blockIdx.x;
     const int seq = static_cast<int>(me / p.num_q_heads), qh = static_cast<int>(me - (long long)seq * p.num_q_heads);
     if (seq >= p.num_seqs) return;
     const uint32_t share = max(1u, *split.share), ru = row_units(seq_view<true>(p, seq).seen);
@@ -897,7 +909,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_q4_kernel(const DecodePa
     constexpr int FETCH = 8;
     float M = -INFINITY, L = 0.f;
     float acc[E] = {};
-    for (int i0 = 0; i0 < parts; i0 += FETCH) {
+    for (int i0 = FETCH * mine; i0 < parts; i0 += FETCH * PER) {
         const int n = min(FETCH, parts - i0);
         const float2 ml = lane < n ? *reinterpret_cast<const float2 *>(split.ml + at(i0 + lane) * 2)
                                    : make_float2(-INFINITY, 0.f);
@@ -929,6 +941,36 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_q4_kernel(const DecodePa
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(kFull, L, o);
+    if constexpr (PER > 1) {   // the warps' sums, in their order (one without a partial has M = -inf and zeros)
+        __shared__ float s_m[PER], s_l[PER];
+        __shared__ Vec s_acc[PER][32];
+        if (lane == 0) {
+            s_m[warp] = M;
+            s_l[warp] = L;
+        }
+        if constexpr (E == 4) s_acc[warp][lane] = make_float4(acc[0], acc[1], acc[E - 2], acc[E - 1]);
+        else s_acc[warp][lane] = make_float2(acc[0], acc[1]);
+        __syncthreads();
+        if (warp != 0) return;
+        float f[PER];
+#pragma unroll
+        for (int w = 1; w < PER; ++w) M = fmaxf(M, s_m[w]);
+        L = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < PER; ++w) {
+            f[w] = exp2f(s_m[w] - M);
+            L = fmaf(f[w], s_l[w], L);
+            const Vec v = s_acc[w][lane];
+            acc[0] = fmaf(f[w], v.x, acc[0]);
+            acc[1] = fmaf(f[w], v.y, acc[1]);
+            if constexpr (E == 4) {
+                acc[E - 2] = fmaf(f[w], v.z, acc[E - 2]);
+                acc[E - 1] = fmaf(f[w], v.w, acc[E - 1]);
+            }
+        }
+    }
     const float norm = L == 0.f ? 0.f : 1.f / L;
     T *to = static_cast<T *>(p.out) + me * HD + lane * E;
     if constexpr (E == 4) {
@@ -965,6 +1007,7 @@ struct Q4Launch {
 
 template <typename T, int HD, int G, int NT, int NC, int bs>
 int launch_one(const DecodeParams &p, const Q4Launch &c) {
+    const long long rows = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.head_tiles;
     if (c.phase != PA_PHASE_REDUCE) {
         constexpr int NS = Q4Shape<HD, NT>::NSTAGE;
         constexpr int SMEM = kQ4Warps * NS * (2 * kUnit * Q4Format<HD, G>::ROW_BYTES + 8);
@@ -972,7 +1015,6 @@ int launch_one(const DecodeParams &p, const Q4Launch &c) {
         auto kernel = decode_q4_kernel<T, HD, G, NT, NC, bs>;
         const int occ = ensure_kernel(kernel, slot, SMEM, c.dev, kQ4Warps * 32);
         if (occ == 0) return pa_fail(PA_ERR_CUDA, "pa_decode_q4: cannot configure the kernel");
-        const long long rows = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.head_tiles;
         long long warps = static_cast<long long>(sm_count(c.dev)) * occ * kQ4Warps;
         if (warps > kMaxStretches) warps = kMaxStretches;
         const long long most = c.stretches ? c.stretches : rows;
@@ -984,9 +1026,12 @@ int launch_one(const DecodeParams &p, const Q4Launch &c) {
         if (e != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
     }
     if (c.stretches && c.phase != PA_PHASE_PARTITIONS) {
-        const long long ctas = (static_cast<long long>(p.num_seqs) * p.num_q_heads + kJoinWarps - 1) / kJoinWarps;
-        const cudaError_t e = launch_dependent(join_q4_kernel<T, HD>, static_cast<int>(ctas), kJoinWarps * 32, 0,
-                                               c.stream, p, c.split, 4 * NC * NT);
+        const long long all = static_cast<long long>(p.num_seqs) * p.num_q_heads;
+        const bool four = join_by_four(c.stretches, rows, all, sm_count(c.dev));
+        const long long ctas = four ? all : (all + kJoinWarps - 1) / kJoinWarps;
+        const cudaError_t e = launch_dependent(four ? join_q4_kernel<T, HD, kJoinWarps> : join_q4_kernel<T, HD, 1>,
+                                               static_cast<int>(ctas), kJoinWarps * 32, 0, c.stream, p, c.split,
+                                               4 * NC * NT);
         if (e != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
     }
     return PA_OK;

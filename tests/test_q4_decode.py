@@ -51,8 +51,8 @@ def test_bad_arguments_are_refused_on_the_host(pa, change, code):
 
 
 def test_workspace_sizes(pa):
-    """A header and a word per sequence, then two rows of heads (a tile of 8, or 16
-    for groups above 8) for each stretch: at most 2432 of them, and at most one
+    """A header and a word per sequence, then two rows of heads (4, 8 or 16 for
+    groups of up to 4, up to 8 and above) for each stretch: at most 2432 of them, and at most one
     per partition_size tokens of what the batch can hold."""
     size = pa.pa_decode_q4_workspace_size
     assert size(4, 8, 2, 128, 512, 512) == 0 and size(4, 8, 2, 128, 0) == 0 and size(0, 8, 2, 128, 4096) == 0
@@ -63,13 +63,14 @@ def test_workspace_sizes(pa):
         n = min(2432, -(-(seqs * rows * -(-tokens // 32)) // (P // 32)))
         return 256 + a256(4 * seqs) + a256(n * 2 * tile * 8) + a256(n * 2 * tile * hd * 4)
 
-    assert size(4, 8, 2, 128, 1025, 512) == want(4, 2, 8, 128, 1025, 512)
+    assert size(4, 8, 2, 128, 1025, 512) == want(4, 2, 4, 128, 1025, 512)
+    assert size(4, 10, 2, 128, 1025, 512) == want(4, 2, 8, 128, 1025, 512)
     assert size(300, 64, 8, 64, 10**6, 512) == want(300, 8, 8, 64, 10**6, 512)
     assert size(4, 40, 2, 128, 1025, 512) == want(4, 4, 16, 128, 1025, 512)
     # a window bounds what is walked: 600 tokens, 5 sinks, and blocks of 32 at their edges
-    assert size(4, 8, 2, 128, 10**6, 512, window=600, num_sinks=5) == want(4, 2, 8, 128, 32 + 600 + 31, 512)
+    assert size(4, 8, 2, 128, 10**6, 512, window=600, num_sinks=5) == want(4, 2, 4, 128, 32 + 600 + 31, 512)
     big = 2**31 - 1
-    assert size(1, 1, 1, 64, big, 1024) == want(1, 1, 8, 64, big, 1024)
+    assert size(1, 1, 1, 64, big, 1024) == want(1, 1, 4, 64, big, 1024)
     assert size(1, 1, 1, 64, big, 1024, window=big, num_sinks=big) == size(1, 1, 1, 64, big, 1024)
 
 
