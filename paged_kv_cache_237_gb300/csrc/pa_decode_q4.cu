@@ -140,6 +140,21 @@ __device__ __forceinline__ void codes_or_bytes_f16(uint32_t x, uint32_t (&r)[4])
     }
 }
 
+// 16 bytes to shared memory, both addresses 16-byte aligned; a group of them; and
+// the wait until at most `left` (up to MOST) of the newest groups are on their way.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int MOST>
+__device__ __forceinline__ void copies_wait(uint32_t left) {
+    if constexpr (MOST > 0) {
+        if (left < MOST) return copies_wait<MOST - 1>(left);
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(MOST) : "memory");
+}
+
 // The smallest power of two above x >= 0, within [2^-100, 2^120].
 __device__ __forceinline__ float pow2_above(float x) {
     const float c = fminf(fmaxf(x, 0x1p-101f), 0x1p119f);
@@ -218,12 +233,6 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
     const int g = lane >> 2, t = lane & 3;
     uint8_t *wbuf = smem + warp * WARP_BYTES;
     const uint32_t wbuf_s = smem_addr(wbuf);
-    const uint32_t bar_s = smem_addr(smem + kQ4Warps * WARP_BYTES) + warp * NSTAGE * 8;
-    if (lane == 0) {
-        for (int s = 0; s < NSTAGE; ++s) mbar_init(bar_s + 8 * s, 1);
-        fence_mbar_init();
-    }
-    __syncwarp();
 
     // Where the 16-token halves of a stage begin: two pages, or one of 32 rows.
     constexpr int bs_shift = bs == 32 ? 5 : 4;
@@ -237,7 +246,6 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
     const int tok_a = (2 * t) ^ (t & 1), tok_b = (2 * t + 1) ^ (t & 1);   // matrix rows 2 t and 2 t + 1
 
     uint32_t n_issued = 0, n_done = 0;
-    bool failed = false;
     const uint64_t kv_policy = l2_evict_first_policy();
     griddep_wait();   // everything above touched only this warp's registers and shared memory
 
@@ -354,25 +362,27 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
         if (bs == 16) page_b = page_of(v + 16);
         return units;
     };
-    // A stage's copies, one lane each: K's and V's page, and (block size 16) those
-    // of the second half.  (All by one lane: 71.8 us on 64 sequences of GQA 64/4, 69.)
-    // The barrier's count of bytes may go below zero: until lane 0 has arrived, the
-    // phase cannot end.
-    constexpr int COPIES = bs == 16 ? 4 : 2;
-    const bool of_v = lane & 1, of_b = bs == 16 && (lane & 2);
-    const uint8_t *const from = of_v ? v_cache : k_cache;
-    const uint32_t to = wbuf_s + (of_v ? HALF_BYTES : 0) + (of_b ? page_bytes : 0);
+    // A stage's copies: 8 lanes (block size 32: 16) take a page each, K's and V's and
+    // with block size 16 those of the second half, 16 bytes a lane at a time.
+    constexpr int LANES = bs == 16 ? 8 : 16, PIECES = page_bytes / 16;
+    const int sub = lane % LANES;
+    const bool of_v = (lane / LANES) & 1, of_b = bs == 16 && lane >= 16;
+    const uint8_t *const from = (of_v ? v_cache : k_cache) + 16 * sub;
+    const uint32_t to = wbuf_s + (of_v ? HALF_BYTES : 0) + (of_b ? page_bytes : 0) + 16 * sub;
     auto issue = [&](int page_a, int page_b, int k) {
-        const int a = __shfl_sync(kFull, page_a, k), b = bs == 16 ? __shfl_sync(kFull, page_b, k) : -1;
-        if (lane < COPIES) {
-            const int s = n_issued % NSTAGE;
-            const uint32_t bar = bar_s + 8 * s;
-            const int page = of_b ? b : a;
-            fence_proxy_async_smem();
-            if (lane == 0) mbar_arrive_expect_tx(bar, ((a >= 0) + (b >= 0)) * 2 * page_bytes);
-            if (page >= 0)
-                bulk_load_hint(to + s * STAGE_BYTES, from + (long long)page * page_bytes, page_bytes, bar, kv_policy);
+        int page = __shfl_sync(kFull, page_a, k);
+        if (bs == 16) {
+            const int b = __shfl_sync(kFull, page_b, k);
+            if (of_b) page = b;
         }
+        if (page >= 0) {
+            const uint8_t *src = from + (long long)page * page_bytes;
+            const uint32_t dst = to + n_issued % NSTAGE * STAGE_BYTES;
+#pragma unroll
+            for (int i = 0; i < PIECES; i += LANES)
+                if (PIECES - i >= LANES || sub < PIECES - i) copy16_async(dst + 16 * i, src + 16 * i, kv_policy);
+        }
+        copies_commit();
         ++n_issued;
     };
 
@@ -392,7 +402,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
     int slot = 0, page_a, page_b, next_a, next_b;
     int units = read_block(s_blocks[warp][0], page_a, page_b);
     int asked = 0, asked_next = 0;        // units of the two blocks that have been issued
-    while (units >= 0 && !failed) {
+    while (units >= 0) {
         const Block &it = s_blocks[warp][slot];
         for (; asked < units && n_issued - n_done < NSTAGE; ++asked) issue(page_a, page_b, asked);
         const int next_units = read_block(s_blocks[warp][slot ^ 1], next_a, next_b);
@@ -494,13 +504,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
 
         for (int k = 0; k < units; ++k) {
             const int s = n_done % NSTAGE;
-            const uint32_t parity = (n_done / NSTAGE) & 1u;
-            if (!__all_sync(kFull, mbar_try_wait(bar_s + 8 * s, parity)) &&
-                !__all_sync(kFull, mbar_wait_bounded(bar_s + 8 * s, parity))) {
-                if (lane == 0) flag_status(p.status, PA_STATUS_WAIT_TIMEOUT);
-                failed = true;
-                break;
-            }
+            copies_wait<NSTAGE - 1>(n_issued - n_done - 1);
+            __syncwarp();   // every lane's copies, for all
             ++n_done;
             uint8_t *stage = wbuf + s * STAGE_BYTES;
             const int v0 = tok_begin + k * kUnit;
@@ -527,7 +532,6 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                         }
                     hidden |= ((~mask >> row_g) & 1u) << (2 * half) | ((~mask >> (row_g + 8)) & 1u) << (2 * half + 1);
                 }
-                fence_proxy_async_smem();
                 __syncwarp();
             }
 
@@ -863,11 +867,6 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
         asked_next = 0;
     }
     griddep_launch_dependents();
-    // A wait gave up: let copies still in flight land before the CTA exits.
-    if (failed && lane == 0) {
-        for (uint32_t gi = n_done; gi < n_issued; ++gi)
-            mbar_wait_bounded(bar_s + 8 * (gi % NSTAGE), (gi / NSTAGE) & 1u);
-    }
 }
 
 // Joins the partials of every row that stretches cut.  out = sum_i 2^(m_i - M)
@@ -896,8 +895,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_q4_kernel(const DecodePa
     const int kvh = qh / p.group, in_group = qh - kvh * p.group, ht = in_group / rows, r = in_group - ht * rows;
     const uint32_t begin = split.bases[seq] + (kvh * p.head_tiles + ht) * (ru + kRowCost) + kRowCost;
     const uint32_t w0 = begin / share, w1 = (begin + ru - 1) / share;
-    // Equal: stored whole.  Past the room, or reversed: a pass that gave up on a
-    // wait, or did not run, left the bases unwritten.
+    // Equal: stored whole.  Past the room, or reversed: no pass has written the bases.
     if (w0 >= w1 || w1 >= split.stretches) return;
     const int parts = static_cast<int>(w1 - w0) + 1;
     // the stretch that begins the row keeps it in its second slot, the others in their first
@@ -1010,7 +1008,7 @@ int launch_one(const DecodeParams &p, const Q4Launch &c) {
     const long long rows = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.head_tiles;
     if (c.phase != PA_PHASE_REDUCE) {
         constexpr int NS = Q4Shape<HD, NT>::NSTAGE;
-        constexpr int SMEM = kQ4Warps * NS * (2 * kUnit * Q4Format<HD, G>::ROW_BYTES + 8);
+        constexpr int SMEM = kQ4Warps * NS * 2 * kUnit * Q4Format<HD, G>::ROW_BYTES;
         static KernelSlot slot;
         auto kernel = decode_q4_kernel<T, HD, G, NT, NC, bs>;
         const int occ = ensure_kernel(kernel, slot, SMEM, c.dev, kQ4Warps * 32);
