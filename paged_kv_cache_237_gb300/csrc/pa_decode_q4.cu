@@ -25,16 +25,19 @@
 // of q and of the weights; and each pair of products in an accumulator of its
 // own, added in fp32.
 //
-// What bounds it: 16 tokens of a head row of 128 are 2304 bytes and about 239
-// warp instructions (half of them on the ALU pipe, which takes two cycles each:
-// 64 ands and 24 permutes and shifts unpack the codes), so instruction issue
-// comes before HBM.  Measured (graph replays): 256 sequences of 16..8192 tokens,
-// GQA 64/8, 1.2 GB: 203 us, 5.9 TB/s, 0.88 of the copy peak (pass 195, join
-// 7); 32 lognormal sequences, 235 MB: 51 us, 0.68 (pass 46, of which about 5
-// are its start and end; join 5); 7 sequences of up to 131072, groups of 32:
-// 141 us, 0.84; head_dim 64 without head groups, window 2000: 88 us, 0.61 (the
-// softmax and the parameters cost as much for half the bytes).  On plain FMAs,
-// one token a warp: 5691, 1231, 3390 and 1508 us.
+// What bounds it: 16 tokens of a head row of 128 are 2304 bytes and over 200 warp
+// instructions (40 % on the ALU pipe, which takes two cycles each: 64 ands and 24
+// permutes and shifts unpack the codes), so their issue comes before HBM, and every
+// instruction taken out of the loop has counted.  Pages come by 16-byte
+// asynchronous copies, 8 or 16 lanes a page: nine instructions for a stage, where a
+// bulk copy per page takes a loop over the lanes that ask, a barrier and a fence
+// (50.2, 138.5 and 81.5 us on the last three cases below).
+// Measured (graph replays): 256 sequences of 16..8192 tokens, GQA 64/8, 1.2 GB:
+// 195.5 us, 6.2 TB/s, 0.92 of the copy peak; 32 lognormal sequences, 235 MB: 46.8 us,
+// 0.75 (about 5 are the pass' start and end, 5 the join); 7 sequences of up to 131072,
+// groups of 32: 129.4 us, 0.91; head_dim 64 without head groups, window 2000: 70.7
+// us, 0.76 (the softmax and the parameters cost as much for half the bytes).  On
+// plain FMAs, one token a warp: 5691, 1231, 3390 and 1508 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -76,6 +79,53 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// The products of N values, a factor with each added to a sum, and a sum: PACKED,
+// two at a time (Blackwell's packed fp32, each half rounded as by itself; 1 to 2 %
+// of the whole for bf16, while fp32's kernels have no registers for the pairs).
+template <bool PACKED, int N>
+__device__ __forceinline__ void times(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += PACKED && N % 2 == 0 ? 2 : 1) {
+        if constexpr (PACKED && N % 2 == 0) {
+            const float2 v = __fmul2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+            d[i] = v.x, d[i + 1] = v.y;
+        } else {
+            d[i] = a[i] * b[i];
+        }
+    }
+}
+template <bool PACKED, int N>
+__device__ __forceinline__ void times(float (&d)[N], float f, const float (&b)[N]) {
+    float a[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = f;
+    times<PACKED>(d, a, b);
+}
+template <bool PACKED, int N>
+__device__ __forceinline__ void add_times(float (&d)[N], float f, const float (&b)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += PACKED && N % 2 == 0 ? 2 : 1) {
+        if constexpr (PACKED && N % 2 == 0) {
+            const float2 v = __ffma2_rn(make_float2(f, f), make_float2(b[i], b[i + 1]), make_float2(d[i], d[i + 1]));
+            d[i] = v.x, d[i + 1] = v.y;
+        } else {
+            d[i] = fmaf(f, b[i], d[i]);
+        }
+    }
+}
+template <bool PACKED, int N>
+__device__ __forceinline__ void add(float (&d)[N], const float (&b)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += PACKED && N % 2 == 0 ? 2 : 1) {
+        if constexpr (PACKED && N % 2 == 0) {
+            const float2 v = __fadd2_rn(make_float2(d[i], d[i + 1]), make_float2(b[i], b[i + 1]));
+            d[i] = v.x, d[i + 1] = v.y;
+        } else {
+            d[i] += b[i];
+        }
+    }
 }
 
 // A token's steps and minima, or (NORMAL: codes less 8) the middles of its ranges.
@@ -164,14 +214,14 @@ __device__ __forceinline__ float pow2_above(float x) {
 constexpr int kQ4Warps = 4;   // per CTA; they are independent
 
 // Launch shape: stages per warp, and the CTAs per SM the kernel is built for.
-// The pass is bound by instruction issue, so it wants registers (161 of 168)
-// before warps: 3 CTAs of 4 warps take 206 us on 256 sequences x 16..8192
-// tokens (GQA 64/8, groups of 64), 4 CTAs at 128 registers 218.  Four warps per
+// The pass is bound by instruction issue, so it wants registers (163 of 168)
+// before warps: 3 CTAs of 4 warps take 198 us on 256 sequences x 16..8192
+// tokens (GQA 64/8, groups of 64), 4 CTAs at 128 registers 204.  Four warps per
 // CTA keep the SM's four schedulers evenly loaded, which equal stretches need:
 // 12 or 14 CTAs of one warp take 10 to 15 % longer.
 template <int HD, int NT>
 struct Q4Shape {
-    static constexpr int NSTAGE = HD == 128 ? 2 : 3;
+    static constexpr int NSTAGE = 2;   // 3 and 4 change nothing, or cost 2 % (head_dim 128)
     static constexpr int CPS = NT == 2 ? 2 : 3;
 };
 
@@ -204,12 +254,14 @@ __device__ __forceinline__ uint32_t row_units(int seen) { return seen > kUnit ? 
 
 // A row takes kRowCost more places on the axis than it has units, before them:
 // what beginning and ending a row costs a warp, in units.
-constexpr uint32_t kRowCost = 3;   // 256 sequences x 16..8192 tokens: 0 takes 244 us, 3 211, 5 212, 8 216
+constexpr uint32_t kRowCost = 3;   // 256 sequences x 16..8192 tokens: 2 takes 200 us, 3 198, 4 198.5
 __device__ __forceinline__ uint32_t row_places(int seen) { return row_units(seen) + kRowCost; }
 
 // T: type of q and out.  fp32 splits q and the weights into two fp16 parts.
 // NT: tiles of 8 query heads per row.  NC: columns of a tile that a lane looks
-// after; 1 where a row has at most 4 heads, which then take the even columns.
+// after; 1 where a row has at most 4 heads, which then take the even columns and
+// leave the lanes half the softmax (64 sequences, GQA 32/8: 132 us for 141; MHA of
+// head_dim 64: 82 for 92).
 // bs: block size.
 template <typename T, int HD, int G, int NT, int NC, int bs>
 __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
@@ -637,7 +689,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
             // FMA pipe has room for: while this lane's p sum to at most 2^5 a head and
             // its s inv to at most 2^10, no w passes 2^15.
             float pr[2][NT][2 * NC], sw[2][2][NG];   // p, and s inv of this lane's tokens
-            float sum[NT][NC], most = 0.f, wide = 0.f;
+            float sum[NT][NC], most = 0.f, wides[NG] = {}, wide = 0.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) sum[nt][0] = sum[nt][NC - 1] = 0.f;
 #pragma unroll
@@ -647,11 +699,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                 for (int r = 0; r < 2; ++r) {
                     float sv[NG], mv[NG];
                     load_pairs<NG, SPLIT>(Vp + (row_g + 8 * r) * F::PARAM_BYTES, sv, mv);
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) {
-                        sw[half][r][i] = sv[i] * inv[i];
-                        wide += sw[half][r][i];
-                    }
+                    times<!SPLIT>(sw[half][r], sv, inv);
+                    add<!SPLIT>(wides, sw[half][r]);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -663,6 +712,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) most = fmaxf(most, fmaxf(sum[nt][0], sum[nt][NC - 1]));   // passes NaN over
+#pragma unroll
+            for (int i = 0; i < NG; ++i) wide += wides[i];
             const bool fresh = first && k == 0;
             if (fresh || __any_sync(kFull, most > 32.f || wide > 1024.f)) {
                 // Raise the references to the running maxima (a row's first unit
@@ -748,16 +799,17 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         if (half == 0) l[nt][c] += sum[nt][c];
-#pragma unroll
-                        for (int i = 0; i < NG; ++i)
-                            om[nt][c][i] = fmaf(pr[half][nt][c], mv[0][i], fmaf(pr[half][nt][c + NC], mv[1][i], om[nt][c][i]));
+                        add_times<!SPLIT>(om[nt][c], pr[half][nt][c + NC], mv[1]);
+                        add_times<!SPLIT>(om[nt][c], pr[half][nt][c], mv[0]);
                     }
 #pragma unroll
-                    for (int i = 0; i < NG; ++i)
+                    for (int r = 0; r < 2; ++r) {
+                        float wx[NG], wy[NG] = {};
+                        times<!SPLIT>(wx, pr[half][nt][NC * r], sw[half][r]);
+                        if (NC == 2) times<!SPLIT>(wy, pr[half][nt][NC * r + NC - 1], sw[half][r]);
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float x = pr[half][nt][NC * r] * sw[half][r][i];
-                            const float y = NC == 2 ? pr[half][nt][NC * r + NC - 1] * sw[half][r][i] : 0.f;
+                        for (int i = 0; i < NG; ++i) {
+                            const float x = wx[i], y = wy[i];
                             const uint32_t h = pack_f16(x, y);
                             pb[0][nt][i][r] = movmatrix_trans(h);
                             if constexpr (SPLIT) {
@@ -765,6 +817,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
                                 pb[PARTS - 1][nt][i][r] = movmatrix_trans(pack_f16(x - b.x, y - b.y));
                             }
                         }
+                    }
                 }
 
                 // ---- O += V^T W: rows are values, k is the tokens.

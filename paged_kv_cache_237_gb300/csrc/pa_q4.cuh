@@ -57,17 +57,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     return y;
 }
 
-// Untiled bulk copy of `bytes` (a multiple of 16, both addresses 16-byte
-// aligned) into shared memory, completing on `bar`.
-__device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar,
-                                               uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
-        ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
-        : "memory");
-}
-
 inline bool q4_sizes_ok(int head_dim, int block_size, int group_size) {
     return (head_dim == 64 || head_dim == 128) && (block_size == 16 || block_size == 32) &&
            (group_size == 32 || group_size == 64);
