@@ -11,14 +11,14 @@
 //
 // The write has about as many instructions to issue as bytes to move, so each
 // group's parameters (a division and a reciprocal) are worked out by one lane
-// (lane i K's group i, lane 4 + i V's) and handed round, and a code costs four
-// instructions: subtract, multiply, add 1.5 * 2^23 (which rounds half to even
-// and leaves the code in the low mantissa bits), and a multiply-add that packs
-// it.  Measured on 30011 tokens x 8 heads of 128 bf16 values in groups of 32 (161
-// MB either way, 24 us at the copy peak): write 33.8 us (82.6 with sixteen lanes
-// a row, every lane at the parameters and 64-bit divisions; 37 with 256 threads
-// per CTA), read 28.4 us (50.6; two or four rows a lane change nothing).  32
-// tokens: 1.9 and 1.7 us, the launch.
+// (lane i K's group i, lane 4 + i V's) and handed round, and a code costs three
+// instructions: subtract and multiply two at a time, add 1.5 * 2^23 (which rounds
+// half to even and leaves the code in the low mantissa bits), and a multiply-add
+// that packs it.  Measured on 30011 tokens x 8 heads of 128 bf16 values in groups
+// of 32 (161 MB either way, 24 us at the copy peak): write 32.0 us (82.6 with
+// sixteen lanes a row, every lane at the parameters and 64-bit divisions; 37 with
+// 256 threads per CTA; 33.6 without packed fp32), read 28.4 us (50.6; packed fp32 and
+// two or four rows a lane change nothing).  32 tokens: 1.9 and 1.7 us, the launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -183,11 +183,14 @@ __device__ __forceinline__ Group group_of(float low, float high) {
 // Codes of four values in the low 16 bits.  Each sum's bits are 0x4b400000 plus
 // the code; the constant's low 22 bits are zero and stay so when multiplied.
 __device__ __forceinline__ uint32_t encode4(const float (&x)[4], float m, float inv) {
-    uint32_t u = 0;
-#pragma unroll
-    for (int j = 3; j >= 0; --j)
-        u = u * 16u + __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(x[j], m), inv), 12582912.f));
-    return u;
+    const float2 less = make_float2(-m, -m), by = make_float2(inv, inv);
+    const float2 a = __fmul2_rn(__fadd2_rn(make_float2(x[0], x[1]), less), by);
+    const float2 b = __fmul2_rn(__fadd2_rn(make_float2(x[2], x[3]), less), by);
+    constexpr float up = 12582912.f;   // added one at a time: a packed sum would be contracted with the product
+    uint32_t u = __float_as_uint(__fadd_rn(b.y, up));
+    u = u * 16u + __float_as_uint(__fadd_rn(b.x, up));
+    u = u * 16u + __float_as_uint(__fadd_rn(a.y, up));
+    return u * 16u + __float_as_uint(__fadd_rn(a.x, up));
 }
 
 // Eight lanes take the K and the V row of one (token, head).
