@@ -941,18 +941,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_q4_kernel(const DecodePa
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = PER == 1 ? 0 : warp;
-    const long long me = PER == 1 ? (long long)blockIdx.x * kJoinWarps + warp : blockIdx.x;
-    const int seq = static_cast<int>(me / p.num_q_heads), qh = static_cast<int>(me - (long long)seq * p.num_q_heads);
-    if (seq >= p.num_seqs) return;
+    // (rows are counted in 31 bits, and partials' values too: kMaxStretches of them)
+    const uint32_t me = PER == 1 ? blockIdx.x * kJoinWarps + warp : blockIdx.x;
+    const uint32_t seq = me / static_cast<uint32_t>(p.num_q_heads), qh = me - seq * p.num_q_heads;
+    if (seq >= static_cast<uint32_t>(p.num_seqs)) return;
     const uint32_t share = max(1u, *split.share), ru = row_units(seq_view<true>(p, seq).seen);
-    const int kvh = qh / p.group, in_group = qh - kvh * p.group, ht = in_group / rows, r = in_group - ht * rows;
+    const uint32_t kvh = qh / static_cast<uint32_t>(p.group), in_group = qh - kvh * p.group;
+    const uint32_t ht = in_group / static_cast<uint32_t>(rows), r = in_group - ht * rows;
     const uint32_t begin = split.bases[seq] + (kvh * p.head_tiles + ht) * (ru + kRowCost) + kRowCost;
     const uint32_t w0 = begin / share, w1 = (begin + ru - 1) / share;
     // Equal: stored whole.  Past the room, or reversed: no pass has written the bases.
     if (w0 >= w1 || w1 >= split.stretches) return;
     const int parts = static_cast<int>(w1 - w0) + 1;
     // the stretch that begins the row keeps it in its second slot, the others in their first
-    auto at = [&](int i) { return ((long long)(w0 + i) * 2 + (i == 0)) * rows + r; };
+    auto at = [&](int i) { return ((w0 + i) * 2 + (i == 0)) * rows + r; };
     constexpr int E = HD / 32;   // values per lane
     using Vec = typename std::conditional<E == 4, float4, float2>::type;
     // Partials on their way at a time (registers for 16 halve the warps per SM:
@@ -1023,7 +1025,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_q4_kernel(const DecodePa
         }
     }
     const float norm = L == 0.f ? 0.f : 1.f / L;
-    T *to = static_cast<T *>(p.out) + me * HD + lane * E;
+    T *to = static_cast<T *>(p.out) + static_cast<size_t>(me) * HD + lane * E;
     if constexpr (E == 4) {
         store4(to, make_float4(acc[0] * norm, acc[1] * norm, acc[E - 2] * norm, acc[E - 1] * norm));
     } else if constexpr (sizeof(T) == 4) {
