@@ -27,16 +27,16 @@
 //
 // What bounds it: 16 tokens of a head row of 128 are 2304 bytes and over 200 warp
 // instructions (40 % on the ALU pipe, which takes two cycles each: 64 ands and 24
-// permutes and shifts unpack the codes), so their issue comes before HBM, and every
+// permutes and shifts unpack the codes), so their issue and HBM are close, and every
 // instruction taken out of the loop has counted.  Pages come by 16-byte
 // asynchronous copies, 8 or 16 lanes a page: nine instructions for a stage, where a
 // bulk copy per page takes a loop over the lanes that ask, a barrier and a fence
 // (50.2, 138.5 and 81.5 us on the last three cases below).
 // Measured (graph replays): 256 sequences of 16..8192 tokens, GQA 64/8, 1.2 GB:
-// 195.5 us, 6.2 TB/s, 0.92 of the copy peak; 32 lognormal sequences, 235 MB: 46.8 us,
-// 0.75 (about 5 are the pass' start and end, 5 the join); 7 sequences of up to 131072,
-// groups of 32: 129.4 us, 0.91; head_dim 64 without head groups, window 2000: 70.7
-// us, 0.76 (the softmax and the parameters cost as much for half the bytes).  On
+// 195 us, 0.92 of the copy peak (pass 187, 0.96; join 8); 32 lognormal sequences, 235
+// MB: 46.5 us, 0.75 (about 5 are the pass' start and end, 4.5 the join); 7 sequences of
+// up to 131072, groups of 32: 129.3 us, 0.91; head_dim 64 without head groups, window
+// 2000: 70.3 us, 0.77 (the softmax and the parameters cost as much for half the bytes).  On
 // plain FMAs, one token a warp: 5691, 1231, 3390 and 1508 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
