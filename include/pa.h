@@ -484,7 +484,8 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_hea
                                    int max_context_len, int partition_size, int window, int num_sinks);
 
 /* ---- self-test of the bounded wait ----------------------------------------
- * Every wait of the decode kernels for staged data gives up after about two
+ * Every wait of the decode kernels on a barrier for staged data (pa_decode and
+ * pa_decode_window; pa_decode_q4's copies need none) gives up after about two
  * seconds, sets PA_STATUS_WAIT_TIMEOUT and lets the kernel finish, so a copy
  * that never lands cannot hang the GPU.  This call runs that same wait in a
  * one-thread kernel on a barrier that nothing completes, with a limit of
