@@ -218,11 +218,13 @@ constexpr int kQ4Warps = 4;   // per CTA; they are independent
 // before warps: 3 CTAs of 4 warps take 198 us on 256 sequences x 16..8192
 // tokens (GQA 64/8, groups of 64), 4 CTAs at 128 registers 204.  Four warps per
 // CTA keep the SM's four schedulers evenly loaded, which equal stretches need:
-// 12 or 14 CTAs of one warp take 10 to 15 % longer.
-template <int HD, int NT>
+// 12 or 14 CTAs of one warp take 10 to 15 % longer.  fp32's kernels for head_dim 128
+// (SPLIT) would spill at 168 registers: 2 CTAs, 53.7 us against 59.3 on 32 sequences,
+// GQA 64/8, groups of 32.
+template <int HD, int NT, bool SPLIT>
 struct Q4Shape {
     static constexpr int NSTAGE = 2;   // 3 and 4 change nothing, or cost 2 % (head_dim 128)
-    static constexpr int CPS = NT == 2 ? 2 : 3;
+    static constexpr int CPS = NT == 2 || (SPLIT && HD == 128) ? 2 : 3;
 };
 
 constexpr int kUnit = 32;   // tokens per stage: one block of 32 or two of 16
@@ -264,13 +266,13 @@ __device__ __forceinline__ uint32_t row_places(int seen) { return row_units(seen
 // head_dim 64: 82 for 92).
 // bs: block size.
 template <typename T, int HD, int G, int NT, int NC, int bs>
-__global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT>::CPS)
+__global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>::CPS)
     decode_q4_kernel(const uint8_t *__restrict__ k_cache, const uint8_t *__restrict__ v_cache, const DecodeParams p,
                      const Q4Split split, uint32_t warps, uint32_t min_share) {
     using F = Q4Format<HD, G>;
     constexpr bool SPLIT = sizeof(T) == 4;
     constexpr int PARTS = SPLIT ? 2 : 1;
-    constexpr int NSTAGE = Q4Shape<HD, NT>::NSTAGE;
+    constexpr int NSTAGE = Q4Shape<HD, NT, sizeof(T) == 4>::NSTAGE;
     constexpr int W = F::W, NG = F::GROUPS;
     constexpr int HALF_BYTES = kUnit * F::ROW_BYTES;   // a stage's K, then its V
     constexpr int STAGE_BYTES = 2 * HALF_BYTES;
@@ -1062,7 +1064,7 @@ template <typename T, int HD, int G, int NT, int NC, int bs>
 int launch_one(const DecodeParams &p, const Q4Launch &c) {
     const long long rows = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.head_tiles;
     if (c.phase != PA_PHASE_REDUCE) {
-        constexpr int NS = Q4Shape<HD, NT>::NSTAGE;
+        constexpr int NS = Q4Shape<HD, NT, sizeof(T) == 4>::NSTAGE;
         constexpr int SMEM = kQ4Warps * NS * 2 * kUnit * Q4Format<HD, G>::ROW_BYTES;
         static KernelSlot slot;
         auto kernel = decode_q4_kernel<T, HD, G, NT, NC, bs>;
