@@ -374,7 +374,10 @@ def _workspace(workspace, need, skip_counter_reset, dev, stream):
         if stream is None:
             return torch.zeros(need, dtype=torch.uint8, device=dev), True
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
+            handle = int(getattr(stream, "cuda_stream", stream))
+            # handle 0 is the default stream, but torch takes it for "no handle given"
+            # and wraps a stream of its own pool, which nothing orders with the call
+            stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
         with torch.cuda.stream(stream):
             return torch.zeros(need, dtype=torch.uint8, device=dev), True
     if workspace is not None:
