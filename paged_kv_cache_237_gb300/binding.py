@@ -304,6 +304,11 @@ class _PreparedCall:
         self._operands = [ctypes.c_void_p(t.data_ptr()) for t in (out, *operands)]
         self._sizes, self._ref = sizes, ctypes.byref(args)
 
+    def owns_workspace(self, workspace) -> bool:
+        """Whether the call runs on this workspace or none, so that it may be kept:
+        one that had a workspace made for it serves the stream it was made on."""
+        return not self._args.workspace or workspace is not None
+
     def __call__(self, stream=None, phase=None) -> torch.Tensor:
         a = self._args
         a.stream = _stream_ptr(stream, self._device)

@@ -16,7 +16,20 @@ from . import binding
 from .workloads import WORKLOADS, prefix_share_layout, randn
 
 
-class DecodeStep:
+class _KeptCall:
+    """A step that keeps a checked call, ``_call``, until one of its attributes
+    is assigned: the next call is then checked anew.  A tensor resized or moved
+    in place (``set_``, ``.data``) is not noticed; assign it."""
+
+    _call = None
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name != "_call":
+            object.__setattr__(self, "_call", None)
+
+
+class DecodeStep(_KeptCall):
     """Holds the device buffers a repeated decode step needs (output,
     split-K workspace, status word) so that the timed calls allocate nothing.
 
@@ -27,8 +40,9 @@ class DecodeStep:
 
     With ``window`` (and ``num_sinks``) the step attends to each sequence's
     last ``window`` tokens and its first ``num_sinks`` (``pa_decode_window``).
-    A windowed call without a fused write is checked once, so the tensors given
-    are that step's for its life: update them in place."""
+    A windowed call without a fused write is checked once and kept until an
+    attribute of the step is assigned (a tensor resized or moved in place, with
+    ``set_`` or ``.data``, is not noticed: assign it)."""
 
     def __init__(self, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
@@ -55,7 +69,6 @@ class DecodeStep:
             ws = binding.pa_decode_workspace_size(S, Hq, hd, max_context_len, partition_size)
         self.workspace = _own_workspace(workspace, ws, q.device)
         self.status = status if status is not None else binding.DeviceStatus(q.device)
-        self._plain = None      # the windowed call without a fused write, checked once
 
     def decode(self, stream=None, phase: int = binding.PA_PHASE_ALL, k_new=None, v_new=None,
                slot_mapping=None) -> torch.Tensor:
@@ -70,14 +83,14 @@ class DecodeStep:
 
     def _decode_window(self, stream, phase, k_new, v_new, slot_mapping) -> torch.Tensor:
         fused = k_new is not None or v_new is not None or slot_mapping is not None
-        call = None if fused else self._plain
+        call = None if fused else self._call
         if call is None:
             call = binding._decode_call(self.out, self.q, self.k_cache, self.v_cache, self.block_tables,
                                         self.context_lens, self.scale, self.max_context_len, self.partition_size,
                                         self.workspace, self.status, phase, k_new, v_new, slot_mapping, False, True,
-                                        self.window, self.num_sinks)
-            if not fused:
-                self._plain = call
+                                        self.window, self.num_sinks, stream)
+            if not fused and call.owns_workspace(self.workspace):
+                self._call = call
         return call(stream, phase)
 
     def run_fused(self, k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
@@ -114,10 +127,11 @@ def _own_workspace(workspace: torch.Tensor | None, need: int, device, zeroed: in
     return workspace if need else None
 
 
-class Q4DecodeStep:
+class Q4DecodeStep(_KeptCall):
     """``DecodeStep`` over a 4-bit cache: holds the output, workspace and
-    status word of a repeated step, and its call, checked once.  The tensors
-    given are the step's for its life (update them in place).
+    status word of a repeated step, and its call, checked once and kept until
+    an attribute of the step is assigned (a tensor resized or moved in place,
+    with ``set_`` or ``.data``, is not noticed: assign it).
 
     k_cache, v_cache are uint8 [num_blocks, Hkv, page_bytes]; q may be bf16 or
     fp32.  ``window`` 0 attends to every token."""
@@ -128,29 +142,41 @@ class Q4DecodeStep:
                  workspace: torch.Tensor | None = None, status: binding.DeviceStatus | None = None):
         self.q, self.k_cache, self.v_cache = q, k_cache, v_cache
         self.block_tables, self.context_lens = block_tables, context_lens
-        self.group_size = group_size
+        self.scale, self.max_context_len, self.partition_size = scale, max_context_len, partition_size
+        self.group_size, self.window, self.num_sinks = group_size, window, num_sinks
         self.out = torch.empty_like(q)
         self.status = status if status is not None else binding.DeviceStatus(q.device)
         S, Hq, hd = q.shape
-        _, Hkv, self.block_size = binding._q4_geometry(k_cache, v_cache, hd, group_size, q.device)
+        _, Hkv, _ = binding._q4_geometry(k_cache, v_cache, hd, group_size, q.device)
         ws = binding.pa_decode_q4_workspace_size(S, Hq, Hkv, hd, max_context_len, partition_size, window=window,
                                                  num_sinks=num_sinks)
         # only the header has to be zero, for a pa_decode call that may use it later
         self.workspace = _own_workspace(workspace, ws, q.device, zeroed=256)
-        self._call = binding._decode_q4_call(self.out, q, k_cache, v_cache, block_tables, context_lens, scale,
-                                             max_context_len, group_size, window, num_sinks, partition_size,
-                                             self.workspace, self.status, binding.PA_PHASE_ALL, True)
+        self._checked(None)
+
+    @property
+    def block_size(self) -> int:
+        return binding._q4_geometry(self.k_cache, self.v_cache, self.q.shape[2], self.group_size, self.q.device)[2]
+
+    def _checked(self, stream):
+        call = binding._decode_q4_call(self.out, self.q, self.k_cache, self.v_cache, self.block_tables,
+                                       self.context_lens, self.scale, self.max_context_len, self.group_size,
+                                       self.window, self.num_sinks, self.partition_size, self.workspace, self.status,
+                                       binding.PA_PHASE_ALL, True, stream)
+        if call.owns_workspace(self.workspace):
+            self._call = call
+        return call
 
     def decode(self, stream=None, phase: int = binding.PA_PHASE_ALL) -> torch.Tensor:
-        return self._call(stream, phase)
+        return (self._call or self._checked(stream))(stream, phase)
 
     def write_tokens(self, k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
                      cow_pairs: torch.Tensor | None = None, stream=None) -> None:
         """The step's cache updates: copy-on-write copies, then the new rows, quantised."""
         if cow_pairs is not None and cow_pairs.numel():
-            binding.pa_copy_blocks(binding.q4_block_rows(self.k_cache, self.block_size),
-                                   binding.q4_block_rows(self.v_cache, self.block_size), cow_pairs,
-                                   status=self.status, stream=stream)
+            bs = self.block_size
+            binding.pa_copy_blocks(binding.q4_block_rows(self.k_cache, bs), binding.q4_block_rows(self.v_cache, bs),
+                                   cow_pairs, status=self.status, stream=stream)
         if slot_mapping.numel():
             binding.pa_reshape_and_cache_q4(k_new, v_new, self.k_cache, self.v_cache, slot_mapping,
                                             group_size=self.group_size, status=self.status, stream=stream)
