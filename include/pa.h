@@ -432,7 +432,7 @@ int pa_build_tables(int32_t *block_tables, int64_t *slot_mapping, int32_t *posit
  *
  * Quantisation of a group, every operation rounded to fp32 unless stated, so
  * that every writer gives the same bits:
- *   m = min(x) rounded down to bf16;  far = max(x) - m;
+ *   m = min(x) rounded down to bf16, +0 where that is zero;  far = max(x) - m;
  *   s = 0 if far = 0, else max(far / 15 rounded up to bf16, 2^-126);
  *   c = round_half_even((x - m) * (1 / s)), 0 where s = 0.
  * Then |s c + m - x| <= s / 2 (up to fp32 rounding).  A group that holds a NaN,

@@ -165,7 +165,7 @@ constexpr uint32_t kBad = 0x7fc00000u;   // step 0, minimum NaN
 __device__ __forceinline__ Group group_of(float low, float high) {
     Group g{0.f, 0.f, kBad};
     if (!(low > -0x1p126f && high < 0x1p126f)) return g;   // NaN compares false
-    const uint32_t lo = __float_as_uint(low);
+    const uint32_t lo = __float_as_uint(__fadd_rn(low, 0.f));   // -0 becomes +0
     uint32_t m = lo & 0xffff0000u;
     if ((lo >> 31) && (lo & 0xffffu)) m += 0x10000u;   // negative: towards the larger magnitude
     g.m = __uint_as_float(m);
