@@ -19,8 +19,13 @@
 // ands, and the powers of two are undone where they cost nothing, in q and in
 // the output.  The tensor core aligns a subnormal's products by its nominal
 // exponent, which leaves sums about 17 bits: plenty for a bf16 result (8), not
-// for fp32.  fp32 q and out take codes as the normal values c - 8 and the
-// middle of the range for the minimum, s c + m = s (c - 8) + (m + 8 s), so that
+// for fp32.  It also cuts sums off towards zero, so V's codes are taken as c for
+// the first eight tokens of a product's sixteen and as -(15 - c), with the sign in the
+// weight and the maximum m + 15 s for the minimum, for the others: sums of both signs stay small, and what
+// is cut off, or rounded off weights that are alike, does not add up (flat
+// scores over values of mean zero are the worst case: the output is a small
+// difference of large sums).  fp32 q and out take codes as the normal values c - 7.5 and the
+// middle of the range for the minimum, s c + m = s (c - 7.5) + (m + 7.5 s), so that
 // long flat sums do not cancel what a code's offset brought in; two fp16 parts
 // of q and of the weights; and each pair of products in an accumulator of its
 // own, added in fp32.
@@ -116,6 +121,18 @@ __device__ __forceinline__ void add_times(float (&d)[N], float f, const float (&
     }
 }
 template <bool PACKED, int N>
+__device__ __forceinline__ void add_times(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += PACKED && N % 2 == 0 ? 2 : 1) {
+        if constexpr (PACKED && N % 2 == 0) {
+            const float2 v = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), make_float2(d[i], d[i + 1]));
+            d[i] = v.x, d[i + 1] = v.y;
+        } else {
+            d[i] = fmaf(a[i], b[i], d[i]);
+        }
+    }
+}
+template <bool PACKED, int N>
 __device__ __forceinline__ void add(float (&d)[N], const float (&b)[N]) {
 #pragma unroll
     for (int i = 0; i < N; i += PACKED && N % 2 == 0 ? 2 : 1) {
@@ -128,7 +145,7 @@ __device__ __forceinline__ void add(float (&d)[N], const float (&b)[N]) {
     }
 }
 
-// A token's steps and minima, or (NORMAL: codes less 8) the middles of its ranges.
+// A token's steps and minima, or (NORMAL: codes less 7.5) the middles of its ranges.
 template <int NG, bool NORMAL>
 __device__ __forceinline__ void load_pairs(const uint8_t *at, float (&s)[NG], float (&m)[NG]) {
     uint32_t pair[NG];
@@ -144,7 +161,7 @@ __device__ __forceinline__ void load_pairs(const uint8_t *at, float (&s)[NG], fl
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
         s[i] = q4_step(pair[i]);
-        m[i] = NORMAL ? fmaf(8.f, s[i], q4_min(pair[i])) : q4_min(pair[i]);
+        m[i] = NORMAL ? fmaf(7.5f, s[i], q4_min(pair[i])) : q4_min(pair[i]);
     }
 }
 
@@ -152,7 +169,7 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_ca
 
 // The two nibble pairs (a nibble of each half-word) at a time that make the
 // codes of two units fp16 operands: values 0, 1, 2, 3 of both units.  NORMAL:
-// code - 8, exactly, by way of 16 + code (whose mantissa holds the code in its
+// code - 7.5, exactly, by way of 16 + code (whose mantissa holds the code in its
 // upper bits).  Otherwise code * 2^-24, and code * 2^-20 for values 1 and 3.
 template <bool NORMAL>
 __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&r)[4]) {
@@ -164,7 +181,7 @@ __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&r)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             r[i] = (r[i] & 0x03c003c0u) | 0x4c004c00u;
-            asm("sub.f16x2 %0, %0, %1;" : "+r"(r[i]) : "r"(0x4e004e00u));   // 24
+            asm("sub.f16x2 %0, %0, %1;" : "+r"(r[i]) : "r"(0x4de04de0u));   // 23.5
         }
     } else {
         r[0] = x & 0x000f000fu;
@@ -177,11 +194,17 @@ __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t (&r)[4]) {
 
 // The same for V, whose products can be untangled in the output: not NORMAL,
 // values 1 and 3 come as whole bytes, lower code * 2^-24 + code * 2^-20, which
-// saves an and each.
-template <bool NORMAL>
+// saves an and each.  UPPER: 15 - code in place of code.
+template <bool NORMAL, bool UPPER>
 __device__ __forceinline__ void codes_or_bytes_f16(uint32_t x, uint32_t (&r)[4]) {
     if constexpr (NORMAL) {
         codes_f16<true>(x, r);
+    } else if constexpr (UPPER) {
+        r[1] = ~x & 0x00ff00ffu;
+        r[0] = ~x & 0x000f000fu;
+        // 255 - byte as an fp16 subtraction (exact), which the FMA pipe takes
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(r[3]) : "r"(0x00ff00ffu), "r"(__byte_perm(x, 0u, 0x4341)));
+        r[2] = r[3] & 0x000f000fu;
     } else {
         r[1] = x & 0x00ff00ffu;
         r[0] = x & 0x000f000fu;
@@ -227,13 +250,25 @@ struct Q4Shape {
     static constexpr int CPS = NT == 2 || (SPLIT && HD == 128) ? 2 : 3;
 };
 
+// Every kHoldBlocks blocks of 32 units (4096 tokens) a lane adds its running sums
+// to a second set, in shared memory, and starts anew: whatever a row's length, no
+// accumulator adds up more.  (An fp32 sum of n equal terms may be n 2^-25 off, a
+// tensor core's more.)  q4_held: the sums of a lane, and q4_held_all: with the
+// references and scales that they go by.
+constexpr int kHoldBlocks = 4;
+
+template <int HD, int G, int NT, int NC>
+__host__ __device__ constexpr int q4_held() { return NT * (HD / 16 * 4 + NC * (HD / G) + NC); }
+template <int HD, int G, int NT, int NC>
+__host__ __device__ constexpr int q4_held_all() { return q4_held<HD, G, NT, NC>() + NT * NC + HD / G; }
+
 constexpr int kUnit = 32;   // tokens per stage: one block of 32 or two of 16
 
 // Where a warp stands on the axis, kept in shared memory.
 struct Walk {
     uint32_t pos, begin, end;    // next place, and the warp's stretch
     uint32_t base, places;       // first place of sequence seq, places of each of its rows
-    int seq, n, seen, skip, begins;
+    int seq, n, seen, skip, begins, index;
 };
 
 // Up to 32 units of one row, kept in shared memory.
@@ -241,6 +276,7 @@ struct Block {
     int seq, qh0, rows, n, skip, tok_begin, tok_end;
     int first, last;             // of the row's units in this stretch
     int begins, whole;           // the stretch holds the row's beginning; the whole row
+    int index;                   // of the block in the row's part of this stretch
 };
 
 // The split-K state of a call, in its workspace.
@@ -286,6 +322,9 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     uint8_t *wbuf = smem + warp * WARP_BYTES;
+    // (volatile: one after the other, or the batch of them takes 15 registers that the loop needs)
+    volatile float *const held = reinterpret_cast<float *>(smem + kQ4Warps * WARP_BYTES) + warp * 32 * q4_held_all<HD, G, NT, NC>() + lane;
+    constexpr int HELD = q4_held<HD, G, NT, NC>();
     const uint32_t wbuf_s = smem_addr(wbuf);
 
     // Where the 16-token halves of a stage begin: two pages, or one of 32 rows.
@@ -346,7 +385,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
         }
         if (lane == 0) {
             const SeqView view = begin < end ? seq_view<true>(p, seq) : SeqView{0, 0, 0};
-            walk = Walk{begin, begin, end, base, cut ? row_places(view.seen) : 1u, seq, view.n, view.seen, view.skip, 0};
+            walk = Walk{begin, begin, end, base, cut ? row_places(view.seen) : 1u, seq, view.n, view.seen, view.skip, 0, 0};
         }
         __syncwarp();
     }
@@ -382,10 +421,11 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
         const bool begins = first ? u == 0 : walk.begins != 0;
         const int kvh = h / p.head_tiles, ht = h - kvh * p.head_tiles;
         const int begin = static_cast<int>(u) * kUnit, end = min(view.seen, begin + units * kUnit);
+        const int index = first ? 0 : walk.index + 1;
         __syncwarp();   // the slot's last readers, and the walk's, are done
         if (lane == 0) {
             to = Block{seq, kvh * p.group + ht * ROWS, min(ROWS, p.group - ht * ROWS), view.n, view.skip, begin, end,
-                       first, last, begins, begins && (!cut || u + units + kRowCost == rp)};
+                       first, last, begins, begins && (!cut || u + units + kRowCost == rp), index};
             walk.pos = pos + (cut ? units : 1);
             walk.base = base;
             walk.places = rp;
@@ -394,6 +434,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
             walk.seen = view.seen;
             walk.skip = view.skip;
             walk.begins = begins;
+            walk.index = index;
             if (h == 0 && u == 0) {
                 if (cut) split.bases[seq] = base;
                 const int raw = p.context_lens[seq];
@@ -451,7 +492,27 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
     float o[MT][NT][4];         // [row g or g + 8][column]: sums of w * code, see below
     float om[NT][NC][NG];       // this lane's tokens' sum of p * m
     float less[NT][4], l[NT][NC];  // minus the columns' references, as an accumulator; sums of p
-    float S[NG], inv[NG];       // w = p * s * inv, inv = 4 / S
+    // w = p * s * inv with inv = 4 / S, S a power of two; bf16: 15 steps are fifteen
+    // times s inv
+    float inv[NG], fifteen[NG];
+    auto S = [&](int i) { return __uint_as_float(0x80000000u - __float_as_uint(inv[i])); };
+    // f(sum, its place among the held, its tile and column, and of o its group)
+    auto each_sum = [&](auto &&f) {
+        int j = 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                f(l[nt][c], j++, nt, c, -1);
+#pragma unroll
+                for (int i = 0; i < NG; ++i) f(om[nt][c][i], j++, nt, c, -1);
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) f(o[mt][nt][c], j++, nt, c % NC, G == 64 ? mt / 4 : mt / 2);
+        }
+    };
 
     int slot = 0, page_a, page_b, next_a, next_b;
     int units = read_block(s_blocks[warp][0], page_a, page_b);
@@ -537,8 +598,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
 
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-            S[i] = 1.f;
             inv[i] = 4.f;
+            fifteen[i] = 3.75f;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -770,9 +831,9 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
                     float mx = top[i];
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
-                    const float now = pow2_above(mx * (0.25f * S[i])), ratio = S[i] / now;
-                    S[i] = now;
+                    const float now = pow2_above(mx * (0.25f * S(i))), ratio = S(i) / now;
                     inv[i] = 4.f / now;
+                    fifteen[i] = 3.75f * now;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         sw[half][0][i] *= ratio;
@@ -796,6 +857,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
                 for (int r = 0; r < 2; ++r)
                     load_pairs<NG, SPLIT>(stage + HALF_BYTES + par_0 + half * par_half +
                                               (row_g + 8 * r) * F::PARAM_BYTES, sv[r], mv[r]);
+                if constexpr (!SPLIT) add_times<true>(mv[1], fifteen, sw[half][1]);   // rows 8 to 15 count codes from 15
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -811,7 +873,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
                         if (NC == 2) times<!SPLIT>(wy, pr[half][nt][NC * r + NC - 1], sw[half][r]);
 #pragma unroll
                         for (int i = 0; i < NG; ++i) {
-                            const float x = wx[i], y = wy[i];
+                            const float x = !SPLIT && r == 1 ? -wx[i] : wx[i], y = !SPLIT && r == 1 ? -wy[i] : wy[i];
                             const uint32_t h = pack_f16(x, y);
                             pb[0][nt][i][r] = movmatrix_trans(h);
                             if constexpr (SPLIT) {
@@ -842,8 +904,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
                     for (int hf = 0; hf < 2; ++hf) {
                         const uint32_t sel = hf ? 0x7632 : 0x5410;
                         uint32_t y[4], z[4];
-                        codes_or_bytes_f16<SPLIT>(__byte_perm(x[0][wd], x[1][wd], sel), y);
-                        codes_or_bytes_f16<SPLIT>(__byte_perm(x[2][wd], x[3][wd], sel), z);
+                        codes_or_bytes_f16<SPLIT, false>(__byte_perm(x[0][wd], x[1][wd], sel), y);
+                        codes_or_bytes_f16<SPLIT, true>(__byte_perm(x[2][wd], x[3][wd], sel), z);
                         const int i = G == 64 ? wd : 2 * wd + hf;
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
@@ -870,6 +932,35 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
                 issue(page_a, page_b, asked++);
             else if (asked_next < next_units)
                 issue(next_a, next_b, asked_next++);
+        }
+
+        const bool hold = !it.last && it.index % kHoldBlocks == kHoldBlocks - 1;
+        if (it.index >= kHoldBlocks && (hold || it.last)) {
+            // what the held sums' references and scales were then, against now
+            float f[NT][NC], ratio[NG];
+            int j = HELD;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) f[nt][c] = ex2(less[nt][c] - held[32 * j++]);
+#pragma unroll
+            for (int i = 0; i < NG; ++i) ratio[i] = fminf(held[32 * j++] / S(i), 0x1p126f);   // (finite: f may be 0)
+            each_sum([&](float &sum, int j, int nt, int c, int i) {
+                sum = fmaf(held[32 * j], i < 0 ? f[nt][c] : f[nt][c] * ratio[i], sum);
+            });
+        }
+        if (hold) {
+            int j = HELD;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) held[32 * j++] = less[nt][c];
+#pragma unroll
+            for (int i = 0; i < NG; ++i) held[32 * j++] = S(i);
+            each_sum([&](float &sum, int j, int, int, int) {
+                held[32 * j] = sum;
+                sum = 0.f;
+            });
         }
 
         // Undo the scalings, add the minima's part, and store: the final rows,
@@ -900,9 +991,9 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float *acc = o[2 * m2 + e][nt];
-                        y[2 * e] = fmaf(acc[c] * (SPLIT ? 0x1p-2f : 0x1p22f), S[i], om[nt][c][i]) * norm;
+                        y[2 * e] = fmaf(acc[c] * (SPLIT ? 0x1p-2f : 0x1p22f), S(i), om[nt][c][i]) * norm;
                         const float odd = SPLIT ? acc[c + 2] * 0x1p-2f : (acc[c + 2] - acc[c]) * 0x1p18f;
-                        y[2 * e + 1] = fmaf(odd, S[i], om[nt][c][i]) * norm;
+                        y[2 * e + 1] = fmaf(odd, S(i), om[nt][c][i]) * norm;
                     }
                     const float4 v = make_float4(y[0], y[1], y[2], y[3]);
                     if (whole)
@@ -1065,7 +1156,7 @@ int launch_one(const DecodeParams &p, const Q4Launch &c) {
     const long long rows = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.head_tiles;
     if (c.phase != PA_PHASE_REDUCE) {
         constexpr int NS = Q4Shape<HD, NT, sizeof(T) == 4>::NSTAGE;
-        constexpr int SMEM = kQ4Warps * NS * 2 * kUnit * Q4Format<HD, G>::ROW_BYTES;
+        constexpr int SMEM = kQ4Warps * (NS * 2 * kUnit * Q4Format<HD, G>::ROW_BYTES + 128 * q4_held_all<HD, G, NT, NC>());
         static KernelSlot slot;
         auto kernel = decode_q4_kernel<T, HD, G, NT, NC, bs>;
         const int occ = ensure_kernel(kernel, slot, SMEM, c.dev, kQ4Warps * 32);
