@@ -464,15 +464,29 @@ int pa_gather_q4(void *k, void *v, const void *k_cache, const void *v_cache, con
 
 /* Decode attention over the 4-bit cache: pa_decode (window == 0) or
  * pa_decode_window (window >= 1) with K_i[t], V_i[t] the values s * c + m that
- * the cache holds.  args->dtype is the type of q and out; products and sums
- * are in fp32 or more.  A block id out of range reads as zeros (flagged).
+ * the cache holds.  args->dtype is the type of q and out.  A block id out of
+ * range reads as zeros (flagged).
+ * Arithmetic: scores, exponentials, maxima and sums are fp32, a row's sums in
+ * two levels, 4096 tokens at a time.  The products with the codes run on tensor
+ * cores, whose operands are rounded first:
+ *  - PA_BF16: q enters exactly, no finer than 2^-35 of its row's largest magnitude;
+ *    sums of q over a group, which meet K's minima, as two bf16 parts (16 bits); a
+ *    weight times its value's step as one fp16 number (2^-11 relative); a sum of 16
+ *    tokens' codes or of a group's is cut off at about 17 bits of its largest term.
+ *  - PA_F32: q enters as two fp16 parts (2^-22 relative, no finer than 2^-40 of its
+ *    row's largest magnitude), a weight times its step as two as well.
+ * A weight times its step is held relative to M, the largest such product so far
+ * among its group of values and the query heads of one KV head that are worked
+ * on together (4, 8 or 16): no finer than 2^-32 M (PA_BF16) or 2^-43 M (PA_F32), for
+ * each token.  Finite results need |scale * q| below 2^115.
  * args->partition_size is 0 (the library picks) or a multiple of 32 in
  * [32, 1024]: contexts of up to so many tokens are never split, longer ones are
  * cut wherever that makes the GPU's warps' shares equal, no finer than that.
  * Results are deterministic for given inputs, sizes and GPU.  No counter is
  * used, so skip_counter_reset says nothing, and a workspace may be shared with
- * pa_decode under the same rule of one call at a time; args->simt must be 0 and k_new, v_new and slot_mapping NULL
- * (PA_ERR_UNSUPPORTED): pa_reshape_and_cache_q4 writes the step's tokens. */
+ * pa_decode under the same rule of one call at a time; args->simt must be 0 and
+ * k_new, v_new and slot_mapping NULL (PA_ERR_UNSUPPORTED):
+ * pa_reshape_and_cache_q4 writes the step's tokens. */
 int pa_decode_q4(void *out, const void *q, const void *k_cache, const void *v_cache,
                  const int32_t *block_tables, const int32_t *context_lens, int num_q_heads, int num_kv_heads,
                  int head_dim, int block_size, int group_size, float scale, int window, int num_sinks,

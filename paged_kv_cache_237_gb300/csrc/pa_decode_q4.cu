@@ -20,15 +20,15 @@
 // the output.  The tensor core aligns a subnormal's products by its nominal
 // exponent, which leaves sums about 17 bits: plenty for a bf16 result (8), not
 // for fp32.  It also cuts sums off towards zero, so V's codes are taken as c for
-// the first eight tokens of a product's sixteen and as -(15 - c), with the sign in the
-// weight and the maximum m + 15 s for the minimum, for the others: sums of both signs stay small, and what
-// is cut off, or rounded off weights that are alike, does not add up (flat
-// scores over values of mean zero are the worst case: the output is a small
-// difference of large sums).  fp32 q and out take codes as the normal values c - 7.5 and the
-// middle of the range for the minimum, s c + m = s (c - 7.5) + (m + 7.5 s), so that
-// long flat sums do not cancel what a code's offset brought in; two fp16 parts
-// of q and of the weights; and each pair of products in an accumulator of its
-// own, added in fp32.
+// the first eight tokens of a product's sixteen and as -(15 - c), with the sign in
+// the weight and the maximum m + 15 s for the minimum, for the others: sums of both
+// signs stay small, and what is cut off, or rounded off weights that are alike,
+// does not add up (flat scores over values of mean zero are the worst case: the
+// output is a small difference of large sums).  fp32 q and out take codes as the
+// normal values c - 7.5 and the middle of the range for the minimum, s c + m =
+// s (c - 7.5) + (m + 7.5 s), to the same end; two fp16 parts of q and of the
+// weights, the second scaled up, since a small weight's second part would be
+// subnormal; and each part's products in an accumulator of its own, added in fp32.
 //
 // What bounds it: 16 tokens of a head row of 128 are 2304 bytes and over 200 warp
 // instructions (40 % on the ALU pipe, which takes two cycles each: 64 ands and 24
@@ -86,7 +86,7 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// The products of N values, a factor with each added to a sum, and a sum: PACKED,
+// The products of N values, and of a factor with each, or added to sums: PACKED,
 // two at a time (Blackwell's packed fp32, each half rounded as by itself; 1 to 2 %
 // of the whole for bf16, while fp32's kernels have no registers for the pairs).
 template <bool PACKED, int N>
@@ -129,18 +129,6 @@ __device__ __forceinline__ void add_times(float (&d)[N], const float (&a)[N], co
             d[i] = v.x, d[i + 1] = v.y;
         } else {
             d[i] = fmaf(a[i], b[i], d[i]);
-        }
-    }
-}
-template <bool PACKED, int N>
-__device__ __forceinline__ void add(float (&d)[N], const float (&b)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; i += PACKED && N % 2 == 0 ? 2 : 1) {
-        if constexpr (PACKED && N % 2 == 0) {
-            const float2 v = __fadd2_rn(make_float2(d[i], d[i + 1]), make_float2(b[i], b[i + 1]));
-            d[i] = v.x, d[i + 1] = v.y;
-        } else {
-            d[i] += b[i];
         }
     }
 }
@@ -234,6 +222,11 @@ __device__ __forceinline__ float pow2_above(float x) {
     return __uint_as_float((__float_as_uint(c) + 0x800000u) & 0x7f800000u);
 }
 
+// The largest weight when its scale is chosen, from below; and what the second
+// fp16 part of a weight (fp32) is multiplied by, so that it has as many bits as
+// the first down to the first's subnormals (their sum's steps end at 2^-36).
+constexpr float kLift = 256.f, kPart = 2048.f;
+
 constexpr int kQ4Warps = 4;   // per CTA; they are independent
 
 // Launch shape: stages per warp, and the CTAs per SM the kernel is built for.
@@ -243,11 +236,12 @@ constexpr int kQ4Warps = 4;   // per CTA; they are independent
 // CTA keep the SM's four schedulers evenly loaded, which equal stretches need:
 // 12 or 14 CTAs of one warp take 10 to 15 % longer.  fp32's kernels for head_dim 128
 // (SPLIT) would spill at 168 registers: 2 CTAs, 53.7 us against 59.3 on 32 sequences,
-// GQA 64/8, groups of 32.
+// GQA 64/8, groups of 32.  Two tiles of heads (NT) fit 168 for bf16 and head_dim 64
+// only: 27.7 us against 28.5 with 2 CTAs (64 sequences of 1000..6000, GQA 64/4).
 template <int HD, int NT, bool SPLIT>
 struct Q4Shape {
     static constexpr int NSTAGE = 2;   // 3 and 4 change nothing, or cost 2 % (head_dim 128)
-    static constexpr int CPS = NT == 2 || (SPLIT && HD == 128) ? 2 : 3;
+    static constexpr int CPS = (NT == 2) + SPLIT + (HD == 128) >= 2 ? 2 : 3;
 };
 
 // Every kHoldBlocks blocks of 32 units (4096 tokens) a lane adds its running sums
@@ -492,10 +486,10 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
     float o[MT][NT][4];         // [row g or g + 8][column]: sums of w * code, see below
     float om[NT][NC][NG];       // this lane's tokens' sum of p * m
     float less[NT][4], l[NT][NC];  // minus the columns' references, as an accumulator; sums of p
-    // w = p * s * inv with inv = 4 / S, S a power of two; bf16: 15 steps are fifteen
-    // times s inv
+    // w = p * s * inv with inv = kLift / S, S a power of two; bf16: 15 steps are
+    // fifteen times s inv
     float inv[NG], fifteen[NG];
-    auto S = [&](int i) { return __uint_as_float(0x80000000u - __float_as_uint(inv[i])); };
+    auto S = [&](int i) { return __uint_as_float(0x83000000u - __float_as_uint(inv[i])); };
     // f(sum, its place among the held, its tile and column, and of o its group)
     auto each_sum = [&](auto &&f) {
         int j = 0;
@@ -598,15 +592,16 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
 
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-            inv[i] = 4.f;
-            fifteen[i] = 3.75f;
+            inv[i] = kLift;
+            fifteen[i] = 15.f / kLift;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) less[nt][c] = 0.f;
+            for (int c = 0; c < 4; ++c)   // (a column without a head has no weights)
+                less[nt][c] = 8 * nt + NC * t + (NC == 2 ? c % 2 : 0) < it.rows ? 0.f : -INFINITY;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 l[nt][c] = 0.f;
@@ -746,25 +741,20 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
                             if ((hidden >> (2 * half + c / NC)) & 1u) sc[half][nt][c] = -INFINITY;
             }
 
-            // ---- weights.  w = p s inv in fp16 (inv = 4 / S, S a power of two)
+            // ---- weights.  w = p s inv in fp16 (inv = kLift / S, S a power of two)
             // carries the value's step, so that the codes enter the second product
-            // as they are.  What would pass fp16's range is seen by sums, which the
-            // FMA pipe has room for: while this lane's p sum to at most 2^5 a head and
-            // its s inv to at most 2^10, no w passes 2^15.
+            // as they are.  S is the power of two above the largest p s when it was
+            // chosen: from 2^7, weights may grow to 2^15 before it is chosen anew, and
+            // fall by 2^21 before fp16's subnormals cost them bits.  What would pass
+            // that is seen by sums, which the FMA pipe has room for: this lane's p,
+            // and its w.  (Not by s alone: a token without weight may have any step.)
             float pr[2][NT][2 * NC], sw[2][2][NG];   // p, and s inv of this lane's tokens
-            float sum[NT][NC], most = 0.f, wides[NG] = {}, wide = 0.f;
+            float sum[NT][NC], most = 0.f, ws[NG] = {}, w_sum = 0.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) sum[nt][0] = sum[nt][NC - 1] = 0.f;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const uint8_t *Vp = stage + HALF_BYTES + par_0 + half * par_half;
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float sv[NG], mv[NG];
-                    load_pairs<NG, SPLIT>(Vp + (row_g + 8 * r) * F::PARAM_BYTES, sv, mv);
-                    times<!SPLIT>(sw[half][r], sv, inv);
-                    add<!SPLIT>(wides, sw[half][r]);
-                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -772,16 +762,27 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
                         pr[half][nt][c] = ex2(sc[half][nt][c]);
                         sum[nt][c % NC] += pr[half][nt][c];
                     }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float sv[NG], mv[NG], p_all = 0.f;
+                    load_pairs<NG, SPLIT>(Vp + (row_g + 8 * r) * F::PARAM_BYTES, sv, mv);
+                    times<!SPLIT>(sw[half][r], sv, inv);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) p_all += pr[half][nt][NC * r + c];
+                    add_times<!SPLIT>(ws, p_all, sw[half][r]);
+                }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) most = fmaxf(most, fmaxf(sum[nt][0], sum[nt][NC - 1]));   // passes NaN over
 #pragma unroll
-            for (int i = 0; i < NG; ++i) wide += wides[i];
+            for (int i = 0; i < NG; ++i) w_sum += ws[i];
             const bool fresh = first && k == 0;
-            if (fresh || __any_sync(kFull, most > 32.f || wide > 1024.f)) {
+            if (fresh || __any_sync(kFull, most > 32.f || !(w_sum <= 0x1p15f))) {   // (or NaN: 0 times infinity)
                 // Raise the references to the running maxima (a row's first unit
-                // sets them), choose S anew above every p s and a sixteenth of every
-                // s, and take p again.  Rare after the first unit.
+                // sets them), choose S anew above every p s, and take p again.  Rare
+                // after the first unit.
                 float alpha[NT][NC], rise[NT][NC], keep = 0.f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -792,7 +793,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
                         for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
                         // by how much; a column of NaN alone stays where it is
                         rise[nt][c] = !fresh ? fmaxf(mx, 0.f) : mx == -INFINITY ? 0.f : mx;
-                        alpha[nt][c] = !fresh ? ex2(-rise[nt][c]) : 0.f;
+                        alpha[nt][c] = !fresh && less[nt][c] != -INFINITY ? ex2(-rise[nt][c]) : 0.f;
                         less[nt][c] -= rise[nt][c];
                         less[nt][c + 2] = less[nt][c];
                         l[nt][c] *= alpha[nt][c];
@@ -811,18 +812,20 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
                             sum[nt][c % NC] += pr[half][nt][c];
                         }
                 }
-                // (s inv is back to s by 1 / inv = S / 4, exactly)
+                // (the steps once more: s inv may have overflowed)
                 float top[NG];
 #pragma unroll
-                for (int i = 0; i < NG; ++i) top[i] = keep * 4.f;
+                for (int i = 0; i < NG; ++i) top[i] = 0.5f * keep * S(i);   // S is above what it was chosen for
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        float most_p = 0.0625f;
+                        float most_p = 0x1p-100f, mv[NG];   // (s inv stays below 2^109)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             most_p = fmaxf(most_p, fmaxf(pr[half][nt][NC * r], pr[half][nt][NC * r + NC - 1]));
+                        load_pairs<NG, SPLIT>(stage + HALF_BYTES + par_0 + half * par_half +
+                                                  (row_g + 8 * r) * F::PARAM_BYTES, sw[half][r], mv);
 #pragma unroll
                         for (int i = 0; i < NG; ++i) top[i] = fmaxf(top[i], most_p * sw[half][r][i]);
                     }
@@ -831,13 +834,13 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
                     float mx = top[i];
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
-                    const float now = pow2_above(mx * (0.25f * S(i))), ratio = S(i) / now;
-                    inv[i] = 4.f / now;
-                    fifteen[i] = 3.75f * now;
+                    const float now = pow2_above(mx), ratio = fminf(S(i) / now, 0x1p126f);   // (finite: alpha may be 0)
+                    inv[i] = kLift / now;
+                    fifteen[i] = 15.f / kLift * now;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        sw[half][0][i] *= ratio;
-                        sw[half][1][i] *= ratio;
+                        sw[half][0][i] *= inv[i];
+                        sw[half][1][i] *= inv[i];
                     }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
@@ -878,7 +881,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
                             pb[0][nt][i][r] = movmatrix_trans(h);
                             if constexpr (SPLIT) {
                                 const float2 b = unpack_f16(h);
-                                pb[PARTS - 1][nt][i][r] = movmatrix_trans(pack_f16(x - b.x, y - b.y));
+                                pb[PARTS - 1][nt][i][r] = movmatrix_trans(pack_f16((x - b.x) * kPart, (y - b.y) * kPart));
                             }
                         }
                     }
@@ -915,11 +918,11 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
                             for (int nt = 0; nt < NT; ++nt)
 {
                                     if constexpr (SPLIT) {
-                                        float d[4];
+                                        float d[4], rest[4];
                                         mma_f16_16816(d, a, pb[0][nt][i][0], pb[0][nt][i][1], 0.f);
-                                        mma_f16_16816(d, a, pb[PARTS - 1][nt][i][0], pb[PARTS - 1][nt][i][1]);
+                                        mma_f16_16816(rest, a, pb[PARTS - 1][nt][i][0], pb[PARTS - 1][nt][i][1], 0.f);
 #pragma unroll
-                                        for (int c = 0; c < 4; ++c) o[mt][nt][c] += d[c];
+                                        for (int c = 0; c < 4; ++c) o[mt][nt][c] += fmaf(rest[c], 1.f / kPart, d[c]);
                                     } else {
                                         mma_f16_16816(o[mt][nt], a, pb[0][nt][i][0], pb[0][nt][i][1]);
                                     }
@@ -991,8 +994,8 @@ __global__ void __launch_bounds__(kQ4Warps * 32, Q4Shape<HD, NT, sizeof(T) == 4>
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float *acc = o[2 * m2 + e][nt];
-                        y[2 * e] = fmaf(acc[c] * (SPLIT ? 0x1p-2f : 0x1p22f), S(i), om[nt][c][i]) * norm;
-                        const float odd = SPLIT ? acc[c + 2] * 0x1p-2f : (acc[c + 2] - acc[c]) * 0x1p18f;
+                        y[2 * e] = fmaf(acc[c] * ((SPLIT ? 1.f : 0x1p24f) / kLift), S(i), om[nt][c][i]) * norm;
+                        const float odd = SPLIT ? acc[c + 2] / kLift : (acc[c + 2] - acc[c]) * (0x1p20f / kLift);
                         y[2 * e + 1] = fmaf(odd, S(i), om[nt][c][i]) * norm;
                     }
                     const float4 v = make_float4(y[0], y[1], y[2], y[3]);
