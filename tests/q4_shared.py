@@ -52,13 +52,15 @@ class Shared:
         self.step, self.low = rounded(step), rounded(low)
         self.values = codes * np.repeat(self.step, group, 1) + np.repeat(self.low, group, 1)
 
-    def reference(self):
-        """fp64 [heads, hd] and the weights' sums relative to the largest [heads]."""
+    def reference(self, window=0, sinks=0):
+        """fp64 [heads, hd]."""
+        t = np.arange(self.n)
+        seen = (t >= self.n - window) | (t < sinks) if window else t >= 0
         out = []
         for a in self.heads.tolist():
-            x = self.scores * a
+            x = self.scores[seen] * a
             p = np.exp(x - x.max())
-            out.append((p / p.sum()) @ self.values)
+            out.append((p / p.sum()) @ self.values[seen])
         return np.array(out)
 
     def run(self, pa, dtype, seqs=SEQS, **kw):

@@ -66,3 +66,21 @@ def test_the_same_value_all_along(pa, dtype, code, n):
     steps = 2.0 ** -11 + 2.0 ** -12.9 if dtype == torch.bfloat16 else 2.0 ** -22 + 2 * 2.0 ** -16
     tol = steps * 15 * 0.3125 + (2.0 ** -8 * np.abs(ref) if dtype == torch.bfloat16 else 0)
     assert (off <= tol).all(), (off / tol).max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bs", [16, 32])
+@pytest.mark.parametrize("window,sinks", [(9000, 5), (12345, 4500), (4096, 0)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_long_window_in_one_warp(pa, dtype, window, sinks, bs):
+    """Sums put by on both sides of what the window leaves out: the tolerances of the flat scores above, with
+    scores and values of ordinary spread (the output is larger against its parts, so they hold all the more)."""
+    rng = np.random.default_rng(window)
+    n, hd, group = 20011, 128, 64
+    scores = q4_ref.bf16_toward(rng.uniform(-2, 2, n), True)
+    step = rng.uniform(0.1, 0.4, (n, hd // group))
+    batch = Shared(scores, rng.integers(0, 16, (n, hd)), step, -7.5 * step, group, bs, heads=(1.0, 0.5, -1.0))
+    ref = batch.reference(window, sinks)
+    out = batch.run(pa, dtype, window=window, num_sinks=sinks)
+    rel = np.sqrt(((out - ref) ** 2).sum((1, 2)) / (ref ** 2).sum())
+    assert rel.max() <= (2.0 ** -18 if dtype == torch.float32 else (2.0 ** -8 + 6 * 2.0 ** -11) / 3 ** 0.5), rel
