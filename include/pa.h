@@ -185,7 +185,9 @@ size_t pa_decode_workspace_size(int num_seqs, int num_q_heads, int head_dim,
  *
  * Only blocks that hold a visible position are looked up and read, so the
  * blocks between the sinks and the window may have been given back: their
- * table entries may hold anything.  The fused cache write works as in
+ * table entries may hold anything.  (To the caller's own pool and tables: a
+ * pa_bm sequence keeps its blocks until it is freed, and pa_build_tables takes
+ * a sequence's whole list and flags ids that are not blocks.)  The fused cache write works as in
  * pa_decode.  args->simt must be 0 for PA_BF16 (PA_ERR_UNSUPPORTED).
  * args->partition_size 0 picks by the batch's sizes (equal partitions of what
  * the window shows).  Everything else, types, layouts, checks, determinism, as

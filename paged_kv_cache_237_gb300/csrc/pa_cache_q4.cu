@@ -15,7 +15,7 @@
 // instructions: subtract and multiply two at a time, add 1.5 * 2^23 (which rounds
 // half to even and leaves the code in the low mantissa bits), and a multiply-add
 // that packs it.  Measured on 30011 tokens x 8 heads of 128 bf16 values in groups
-// of 32 (161 MB either way, 24 us at the copy peak): write 32.0 us (82.6 with
+// of 32 (161 MB either way, 24 us at the copy peak): write 32.2 us (82.6 with
 // sixteen lanes a row, every lane at the parameters and 64-bit divisions; 37 with
 // 256 threads per CTA; 33.6 without packed fp32), read 28.4 us (50.6; packed fp32 and
 // two or four rows a lane change nothing).  32 tokens: 1.9 and 1.7 us, the launch.

@@ -583,7 +583,8 @@ int effective_partition(int partition_size) { return partition_size == 0 ? 512 :
 // is a CTA's time per token with the memory to itself and a t2 its share of the
 // bandwidth; items come in waves, each costing `start` more, and n > 1 adds the
 // merge launch and its partials.  Constants measured at head_dim 128 (bf16 12.2
-// ns, fp32 30 ns per token alone; 6.6 TB/s), window 512 to 4096, 8 to 1024 rows;
+// ns, fp32 30 ns per token alone; 6.6 TB/s), window 512 to 4096, 8 to 1024 rows
+// (for head_dim 64 they are scaled by the bytes, not measured);
 // e.g. 8 rows x 531 tokens: n = 9 takes 7.5 us, n = 1 10.6; 256 x 1043: n = 1
 // 25.0, n = 2 39.5; 512 x 4115: n = 4 166, n = 9 172, n = 33 212.
 int window_partition(int num_seqs, int num_kv_heads, int group, int head_dim, bool f32, int walk) {

@@ -36,13 +36,18 @@
 // instruction taken out of the loop has counted.  Pages come by 16-byte
 // asynchronous copies, 8 or 16 lanes a page: nine instructions for a stage, where a
 // bulk copy per page takes a loop over the lanes that ask, a barrier and a fence
-// (50.2, 138.5 and 81.5 us on the last three cases below).
+// (50.2 for 47.3 us on the lognormal batch below, 138.5 for 130.9 on the long one, 81.5
+// for 72.6 with head_dim 64, when it was taken).
 // Measured (graph replays): 256 sequences of 16..8192 tokens, GQA 64/8, 1.2 GB:
-// 195 us, 0.92 of the copy peak (pass 187, 0.96; join 8); 32 lognormal sequences, 235
-// MB: 46.5 us, 0.75 (about 5 are the pass' start and end, 4.5 the join); 7 sequences of
-// up to 131072, groups of 32: 129.3 us, 0.91; head_dim 64 without head groups, window
-// 2000: 70.3 us, 0.77 (the softmax and the parameters cost as much for half the bytes).  On
-// plain FMAs, one token a warp: 5691, 1231, 3390 and 1508 us.
+// 197.7 us, 0.91 of the copy peak (pass 190, 0.95; join 8); 32 lognormal sequences, 235
+// MB: 47.6 us, 0.74 (about 5 are the pass' start and end, 4.6 the join); 7 sequences of
+// up to 131072, groups of 32: 133.7 us, 0.88; head_dim 64 without head groups, window
+// 2000: 72.1 us, 0.75 (the softmax and the parameters cost as much for half the bytes);
+// fp32 q and out, 32 sequences of 1000..6000, GQA 64/8: 55.9 us with groups of 32, 50.0
+// with 64, 0.39 (issue: 65 % of slots, and 8 warps per SM to hide latency with).  Of
+// this the two signs of V's codes cost 0.5 to 3 %, the second set of sums 0.5 %, weights
+// that keep their bits 0 to 4 % (fp32: 3; with 16 heads a group 8).  On plain FMAs, one
+// token a warp: 5691, 1231, 3390 and 1508 us for the first four.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -1206,7 +1211,8 @@ int launch_any(const DecodeParams &p, const Q4Launch &c, int head_dim, int group
 // Contexts of up to so many tokens are not split, others no finer.  Splitting
 // costs the join (about 2 us) and is worth it where rows alone do not fill the
 // GPU: of 8 x 300 tokens P = 64 takes 8.9 us, unsplit 12.1; of 512 x 300, 16.2
-// and 12.7; of 8 x 100, 9.4 and 7.2; of 512 x 1000, 25 and 31.
+// and 12.7; of 8 x 100, 9.4 and 7.2; of 512 x 1000, 25 and 31.  (Between 8 and 512
+// rows nothing was measured: where in between they cross is not known.)
 int q4_partition(int partition_size, long long rows, int walk_cap) {
     if (partition_size != 0) return partition_size;
     return walk_cap <= 128 ? 128 : rows >= 512 && walk_cap <= 512 ? 512 : 64;
