@@ -72,6 +72,8 @@ extern "C" {
 #define PA_STATUS_BAD_PAIR 8        /* copy pair out of range, or its dst is another pair's src/dst */
 #define PA_STATUS_WAIT_TIMEOUT 16   /* a bounded wait for staged data gave up */
 #define PA_STATUS_SHORT_LIST 32     /* pa_build_tables: fewer block ids or token rows than the lengths need */
+#define PA_STATUS_BAD_TREE 64       /* query_start not increasing or outside the rows, a parent that is not an earlier
+                                       node, or a tree of more nodes than its mask or PA_TREE_MAX_NODES holds */
 
 /* ---- decode attention --------------------------------------------------
  * [P3] "Jak dziala" / "Komponenty": the attention kernel reads the K/V cache
@@ -315,6 +317,12 @@ int pa_bm_append_slot(pa_bm *bm, int seq_id, int64_t *slot, int32_t *cow_src, in
  * the pool at zero. */
 int pa_bm_free_seq(pa_bm *bm, int seq_id);
 
+/* Keep the sequence's first num_tokens tokens (at most what it holds): blocks past
+ * them lose one reference, the last first, as in pa_bm_free_seq.  For drafted tokens
+ * that were not accepted.  A keyed block that is then only partly the sequence's keeps
+ * its key until pa_bm_append_slot writes into it (or, shared, copies it first). */
+int pa_bm_trim_seq(pa_bm *bm, int seq_id, int num_tokens);
+
 /* Copy the sequence's physical block ids into out[0..cap).  Returns the
  * number of blocks (>= 0), or PA_ERR_INVALID_ARG if cap is too small. */
 int pa_bm_block_table(const pa_bm *bm, int seq_id, int32_t *out, int cap);
@@ -498,6 +506,102 @@ int pa_decode_q4(void *out, const void *q, const void *k_cache, const void *v_ca
  * one partition). */
 size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                    int max_context_len, int partition_size, int window, int num_sinks);
+
+/* ---- several queries per sequence ------------------------------------------
+ * The queries of all sequences lie end to end: q and out are
+ * [num_tokens][num_q_heads][head_dim] and sequence i owns rows query_start[i] ..
+ * query_start[i + 1] - 1 (int32 [num_seqs + 1], as pa_build_tables makes it), c_i
+ * of them, none included.  Rows that belong to no sequence (padding behind the
+ * last one) are not read and left as they were.  No counterpart in the pages.
+ *
+ * pa_decode_tree: verification of drafted tokens.  The queries are the last c_i of
+ * the n_i = context_lens[i] tokens, whose K/V the cache already holds: query r is
+ * position n_i - c_i + r.  It sees every position below n_i - c_i, and position
+ * n_i - c_i + j if bit j of its row of tree_mask is set (uint64
+ * [num_tokens][mask_words], bit j % 64 of word j / 64; positions past the words
+ * are not seen).  A row may see anything, itself left out; pa_build_tree makes the
+ * rows of a tree.  With tree_mask NULL (mask_words 0) the drafted tokens are a
+ * chain: query r sees position n_i - c_i + j for j <= r, as a prompt's chunk does.
+ *
+ * pa_decode_cross: the queries (any number, of a decoder step or prompt, or the
+ * beams of one request) see all n_i = context_lens[i] tokens of a cache that holds
+ * another sequence: an encoder's states.
+ *
+ * out = softmax over the seen t of scale * (q . K[t]), times V[t]; a row that sees
+ * nothing (n_i = 0, an empty mask) is zero.  What a row does not see has weight
+ * zero, whatever its cache slots hold (NaN included).
+ *
+ * args as for pa_decode: num_seqs, max_blocks_per_seq, num_blocks, dtype,
+ * max_context_len (longer entries are clamped and flagged), dev_status, stream, and
+ * a workspace of pa_decode_tree_workspace_size bytes (both calls), which needs no
+ * zeros and follows the rule of one call at a time.  phase, simt, partition_size
+ * and the fused write's pointers must be 0 (PA_ERR_UNSUPPORTED).  A sequence whose
+ * rows of query_start run backwards or leave [0, num_tokens] has no queries
+ * (flagged PA_STATUS_BAD_TREE); one with c_i > n_i in pa_decode_tree gets zero rows
+ * (PA_STATUS_BAD_CONTEXT_LEN); a block id out of range reads as zeros (flagged).
+ * Rows of two sequences must not overlap.
+ * Results are deterministic for given inputs, sizes and GPU. */
+#define PA_TREE_MAX_NODES 1024 /* nodes of one tree; mask_words is at most 16 */
+
+int pa_decode_tree(void *out, const void *q, const void *k_cache, const void *v_cache,
+                   const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
+                   const uint64_t *tree_mask, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                   float scale, int num_tokens, int mask_words, const pa_decode_args *args);
+
+int pa_decode_cross(void *out, const void *q, const void *k_cache, const void *v_cache,
+                    const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
+                    int num_q_heads, int num_kv_heads, int head_dim, int block_size, float scale, int num_tokens,
+                    const pa_decode_args *args);
+
+/* Bytes of workspace that both calls need for up to num_tokens rows; it does not
+ * grow with the contexts. */
+size_t pa_decode_tree_workspace_size(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim);
+
+/* ---- trees of drafted tokens ------------------------------------------------
+ * Sequence i's tree has nodes 0 .. c_i - 1, its rows of the batch as above.
+ * parents [num_tokens] holds each node's parent within its tree: an earlier node,
+ * or -1 for none.
+ *
+ * pa_build_tree: tree_mask row of node r = bit r and its parent's row; positions
+ * [num_tokens] (may be NULL) = n_i - c_i + depth, depth counted from 0.  Trees of
+ * more than 64 * mask_words nodes are flagged (PA_STATUS_BAD_TREE): the nodes past
+ * that see nothing.  A parent that is not an earlier node counts as none (flagged).
+ * Rows of no sequence are left as they were. */
+int pa_build_tree(uint64_t *tree_mask, int32_t *positions, const int32_t *parents, const int32_t *query_start,
+                  const int32_t *context_lens, int num_seqs, int num_tokens, int mask_words, int32_t *dev_status,
+                  void *stream);
+
+/* pa_accept_tree: the path that the target model agrees with.  Node 0 holds the
+ * sequence's newest token, the others are drafted; draft_tokens [num_tokens] are the
+ * nodes' tokens and target_tokens [num_tokens] the target model's choice behind
+ * each.  a_0 = 0, and a_(j+1) is the lowest child of a_j whose token is
+ * target_tokens[a_j], as long as there is one and j + 1 < max_accepted.  With the
+ * path's L nodes (0 for a sequence that drafted nothing):
+ *   accepted_lens[i] = L;   accepted_nodes[i][j] = a_j, -1 from L on;
+ *   next_tokens[i] = target_tokens[a_(L-1)], -1 if L = 0;
+ *   new_lens[i] = n_i - c_i + L, the sequence's length once its path has moved;
+ *   slot_pairs[i][j] = (slot of position n_i - c_i + a_j, slot of n_i - c_i + j)
+ *   where a_j != j and j < L, else (-1, -1): the pairs of pa_move_rows
+ * ([num_seqs][max_accepted], int32; slot_pairs int64 [num_seqs][max_accepted][2]).
+ * parents NULL is a chain.  max_accepted is 1 to PA_TREE_MAX_NODES; nodes past
+ * PA_TREE_MAX_NODES are not accepted (flagged).  c_i > n_i, or n_i beyond the
+ * table: flagged, L = 0 and new_lens[i] = n_i. */
+int pa_accept_tree(int32_t *accepted_lens, int32_t *accepted_nodes, int32_t *next_tokens, int32_t *new_lens,
+                   int64_t *slot_pairs, const int32_t *draft_tokens, const int32_t *target_tokens,
+                   const int32_t *parents, const int32_t *query_start, const int32_t *context_lens,
+                   const int32_t *block_tables, int num_seqs, int num_tokens, int max_accepted,
+                   int max_blocks_per_seq, int block_size, int num_blocks, int32_t *dev_status, void *stream);
+
+/* pa_move_rows: K/V rows from slot to slot of one cache, every KV head.
+ * slot_pairs [num_groups][pairs_per_group][2] are (source, destination); pairs with
+ * a negative slot are skipped, and ones past the pool too (PA_STATUS_BAD_SLOT).
+ * Within a group every source is read before any destination is written, so a row
+ * may be both.  Destinations must be distinct, and no slot of one group may be a
+ * destination of another.  A group's rows of one head must fit in 48 KB (96 rows of
+ * 128 fp32 values; PA_ERR_UNSUPPORTED). */
+int pa_move_rows(void *k_cache, void *v_cache, const int64_t *slot_pairs, int num_groups, int pairs_per_group,
+                 int num_kv_heads, int head_dim, int block_size, int num_blocks, int dtype, int32_t *dev_status,
+                 void *stream);
 
 /* ---- self-test of the bounded wait ----------------------------------------
  * Every wait of the decode kernels on a barrier for staged data (pa_decode and

@@ -37,6 +37,7 @@ STATUS_BAD_SLOT = 4
 STATUS_BAD_PAIR = 8
 STATUS_WAIT_TIMEOUT = 16
 STATUS_SHORT_LIST = 32
+STATUS_BAD_TREE = 64
 
 
 class PAError(RuntimeError):
@@ -140,6 +141,22 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.pa_reshape_and_cache_q4.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp]
     lib.pa_gather_q4.restype = i32
     lib.pa_gather_q4.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.pa_decode_tree.restype = i32
+    lib.pa_decode_tree.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, i32, i32,
+                                   ctypes.POINTER(_DecodeArgs)]
+    lib.pa_decode_cross.restype = i32
+    lib.pa_decode_cross.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, i32,
+                                    ctypes.POINTER(_DecodeArgs)]
+    lib.pa_decode_tree_workspace_size.restype = sz
+    lib.pa_decode_tree_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.pa_build_tree.restype = i32
+    lib.pa_build_tree.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp, vp]
+    lib.pa_accept_tree.restype = i32
+    lib.pa_accept_tree.argtypes = [vp] * 11 + [i32] * 6 + [vp, vp]
+    lib.pa_move_rows.restype = i32
+    lib.pa_move_rows.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.pa_bm_trim_seq.restype = i32
+    lib.pa_bm_trim_seq.argtypes = [vp, i32, i32]
     lib.pa_last_error_string.restype = ctypes.c_char_p
     lib.pa_last_error_string.argtypes = []
     lib.pa_version.restype = i32
@@ -623,6 +640,159 @@ def _q4_rows_call(fn, k, v, k_cache, v_cache, slot_mapping, group_size, status, 
           _stream_ptr(stream, dev))
 
 
+def pa_decode_tree_workspace_size(num_tokens: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(_lib.pa_decode_tree_workspace_size(num_tokens, num_q_heads, num_kv_heads, head_dim))
+
+
+def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor, scale: float, *,
+                   max_context_len: int, tree_mask: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   status: DeviceStatus | None = None, stream=None) -> torch.Tensor:
+    """Attention of drafted tokens over the paged cache; writes ``out``
+    [T, Hq, hd] and returns it.
+
+    The rows of q [T, Hq, hd] from query_start[i] (int32 [S + 1]) on are the last
+    tokens of sequence i, whose K/V the cache holds already.  Each sees every
+    position before the sequence's drafted tokens, and of those the ones whose
+    bits are set in its row of tree_mask (int64 [T, W], bit j % 64 of word j // 64;
+    ``pa_build_tree`` makes it), or without one those up to itself.  Rows behind
+    the last sequence's are left as they were.  The workspace takes
+    ``pa_decode_tree_workspace_size`` bytes, whatever the contexts; the other
+    arguments are those of ``pa_decode``.
+    """
+    return _multi_call(True, out, q, k_cache, v_cache, block_tables, context_lens, query_start, tree_mask, scale,
+                       max_context_len, workspace, status, stream)(stream)
+
+
+def pa_decode_cross(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor, scale: float,
+                    *, max_context_len: int, workspace: torch.Tensor | None = None,
+                    status: DeviceStatus | None = None, stream=None) -> torch.Tensor:
+    """Attention of any number of queries per request over the paged states of
+    another sequence (an encoder's): every row of q [T, Hq, hd] from
+    query_start[i] on sees all context_lens[i] tokens of block_tables[i].  The
+    arguments are those of ``pa_decode_tree``."""
+    return _multi_call(False, out, q, k_cache, v_cache, block_tables, context_lens, query_start, None, scale,
+                       max_context_len, workspace, status, stream)(stream)
+
+
+def _multi_call(tree, out, q, k_cache, v_cache, block_tables, context_lens, query_start, tree_mask, scale,
+                max_context_len, workspace, status, stream=None) -> _PreparedCall:
+    """The checks and arguments of pa_decode_tree and pa_decode_cross."""
+    _check_cuda(q, "q", (torch.float32, torch.bfloat16))
+    dev = q.device
+    for name, t in (("out", out), ("k_cache", k_cache), ("v_cache", v_cache)):
+        _check_cuda(t, name, (q.dtype,), dev)
+    for name, t in (("block_tables", block_tables), ("context_lens", context_lens), ("query_start", query_start)):
+        _check_cuda(t, name, (torch.int32,), dev)
+    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
+        raise ValueError("q must be [T, Hq, hd], caches [num_blocks, Hkv, bs, hd], tables [S, max_blocks]")
+    T, Hq, hd = q.shape
+    nb, Hkv, bs, hd2 = k_cache.shape
+    S = block_tables.shape[0]
+    if (hd2 != hd or v_cache.shape != k_cache.shape or out.shape != q.shape or context_lens.shape != (S,)
+            or query_start.shape != (S + 1,)):
+        raise ValueError("inconsistent shapes")
+    words = 0
+    if tree_mask is not None:
+        _check_cuda(tree_mask, "tree_mask", (torch.int64,), dev)
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != T:
+            raise ValueError("tree_mask must be [T, words]")
+        words = tree_mask.shape[1]
+    workspace, _ = _workspace(workspace, pa_decode_tree_workspace_size(T, Hq, Hkv, hd), False, dev, stream)
+    args = _DecodeArgs(S, block_tables.shape[1], nb, _dtype_code(q.dtype), 0, max_context_len, _ptr(workspace),
+                       workspace.numel() if workspace is not None else 0, status.ptr() if status is not None else None)
+    operands = (q, k_cache, v_cache, block_tables, context_lens, query_start)
+    sizes = [Hq, Hkv, hd, bs, float(scale), T]
+    keep = (workspace, status, tree_mask, *operands)
+    if not tree:
+        return _PreparedCall(_lib.pa_decode_cross, out, operands, sizes, args, dev, keep)
+    return _PreparedCall(_lib.pa_decode_tree, out, operands, [_ptr(tree_mask), *sizes, words], args, dev, keep)
+
+
+def pa_build_tree(tree_mask: torch.Tensor, positions: torch.Tensor | None, parents: torch.Tensor,
+                  query_start: torch.Tensor, context_lens: torch.Tensor, *, status: DeviceStatus | None = None,
+                  stream=None) -> None:
+    """Ancestor bits and positions of the batch's trees of drafted tokens.
+
+    parents int32 [T]: each node's parent within its tree, an earlier node or -1;
+    query_start int32 [S + 1] and context_lens int32 [S] as for ``pa_decode_tree``.
+    Writes tree_mask int64 [T, W] (trees of up to 64 W nodes, W <= 16) and
+    positions int32 [T] (or None): the sequence's length before its tree plus the
+    node's depth.
+    """
+    _check_cuda(tree_mask, "tree_mask", (torch.int64,))
+    dev = tree_mask.device
+    for name, t in (("parents", parents), ("query_start", query_start), ("context_lens", context_lens)):
+        _check_cuda(t, name, (torch.int32,), dev)
+    if positions is not None:
+        _check_cuda(positions, "positions", (torch.int32,), dev)
+    T, S = parents.shape[0], context_lens.shape[0]
+    if (tree_mask.dim() != 2 or tree_mask.shape[0] != T or parents.shape != (T,) or context_lens.shape != (S,)
+            or query_start.shape != (S + 1,) or (positions is not None and positions.shape != (T,))):
+        raise ValueError("tree_mask must be [T, words], parents and positions [T], context_lens [S], "
+                         "query_start [S + 1]")
+    _call(dev, _lib.pa_build_tree, tree_mask.data_ptr(), _ptr(positions), parents.data_ptr(), query_start.data_ptr(),
+          context_lens.data_ptr(), S, T, tree_mask.shape[1], status.ptr() if status is not None else None,
+          _stream_ptr(stream, dev))
+
+
+def pa_accept_tree(accepted_lens: torch.Tensor, accepted_nodes: torch.Tensor, next_tokens: torch.Tensor,
+                   new_lens: torch.Tensor, slot_pairs: torch.Tensor, draft_tokens: torch.Tensor,
+                   target_tokens: torch.Tensor, parents: torch.Tensor | None, query_start: torch.Tensor,
+                   context_lens: torch.Tensor, block_tables: torch.Tensor, *, block_size: int, num_blocks: int,
+                   status: DeviceStatus | None = None, stream=None) -> None:
+    """The path of each tree that the target model agrees with.
+
+    draft_tokens int32 [T]: the nodes' tokens; target_tokens int32 [T]: the target
+    model's choice behind each node; parents as for ``pa_build_tree``, None for
+    chains.  Node 0 is always accepted, then the lowest child whose token is the
+    target's choice, up to M = accepted_nodes.shape[1] nodes.  Writes, int32 and
+    per sequence, accepted_lens [S], accepted_nodes [S, M] (-1 behind the path),
+    next_tokens [S] (the target's choice at the path's end) and new_lens [S], and
+    slot_pairs int64 [S, M, 2], the (source, destination) slots by which
+    ``pa_move_rows`` puts the path's rows where the sequence goes on.
+    """
+    _check_cuda(accepted_nodes, "accepted_nodes", (torch.int32,))
+    dev = accepted_nodes.device
+    for name, t in (("accepted_lens", accepted_lens), ("next_tokens", next_tokens), ("new_lens", new_lens),
+                    ("draft_tokens", draft_tokens), ("target_tokens", target_tokens), ("query_start", query_start),
+                    ("context_lens", context_lens), ("block_tables", block_tables)):
+        _check_cuda(t, name, (torch.int32,), dev)
+    _check_cuda(slot_pairs, "slot_pairs", (torch.int64,), dev)
+    if parents is not None:
+        _check_cuda(parents, "parents", (torch.int32,), dev)
+    if accepted_nodes.dim() != 2 or block_tables.dim() != 2 or draft_tokens.dim() != 1:
+        raise ValueError("accepted_nodes must be [S, M], block_tables [S, max_blocks], draft_tokens [T]")
+    (S, M), T = accepted_nodes.shape, draft_tokens.shape[0]
+    if (any(t.shape != (S,) for t in (accepted_lens, next_tokens, new_lens, context_lens))
+            or slot_pairs.shape != (S, M, 2) or target_tokens.shape != (T,) or query_start.shape != (S + 1,)
+            or block_tables.shape[0] != S or (parents is not None and parents.shape != (T,))):
+        raise ValueError("inconsistent shapes")
+    _call(dev, _lib.pa_accept_tree, accepted_lens.data_ptr(), accepted_nodes.data_ptr(), next_tokens.data_ptr(),
+          new_lens.data_ptr(), slot_pairs.data_ptr(), draft_tokens.data_ptr(), target_tokens.data_ptr(),
+          _ptr(parents), query_start.data_ptr(), context_lens.data_ptr(), block_tables.data_ptr(), S, T, M,
+          block_tables.shape[1], block_size, num_blocks, status.ptr() if status is not None else None,
+          _stream_ptr(stream, dev))
+
+
+def pa_move_rows(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_pairs: torch.Tensor, *,
+                 status: DeviceStatus | None = None, stream=None) -> None:
+    """Move K/V rows from slot to slot, every KV head: slot_pairs int64
+    [groups, pairs, 2] (source, destination), negative ones skipped.  Within a
+    group every source is read before any destination is written."""
+    _check_cuda(k_cache, "k_cache", (torch.float32, torch.bfloat16))
+    dev = k_cache.device
+    _check_cuda(v_cache, "v_cache", (k_cache.dtype,), dev)
+    _check_cuda(slot_pairs, "slot_pairs", (torch.int64,), dev)
+    if slot_pairs.dim() != 3 or slot_pairs.shape[2] != 2 or k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("slot_pairs must be [groups, pairs, 2], caches [num_blocks, Hkv, bs, hd]")
+    nb, Hkv, bs, hd = k_cache.shape
+    _call(dev, _lib.pa_move_rows, k_cache.data_ptr(), v_cache.data_ptr(), slot_pairs.data_ptr(), slot_pairs.shape[0],
+          slot_pairs.shape[1], Hkv, hd, bs, nb, _dtype_code(k_cache.dtype),
+          status.ptr() if status is not None else None, _stream_ptr(stream, dev))
+
+
 class BlockManager:
     """Host block manager (``pa_bm_*``): free pool, refcounts, copy-on-write."""
 
@@ -704,6 +874,10 @@ class BlockManager:
 
     def free_seq(self, seq_id: int) -> None:
         _raise(_lib.pa_bm_free_seq(self._h, seq_id))
+
+    def trim_seq(self, seq_id: int, num_tokens: int) -> None:
+        """Keep the sequence's first tokens only; blocks past them are released."""
+        _raise(_lib.pa_bm_trim_seq(self._h, seq_id, num_tokens))
 
     def block_table(self, seq_id: int) -> list[int]:
         cap = max(1, self.num_blocks)

@@ -208,6 +208,10 @@ extern "C" int pa_bm_append_slot(pa_bm *bm, int seq_id, int64_t *slot, int32_t *
             s.blocks.back() = fresh;
             src = last;
             dst = fresh;
+        } else if (bm->keyed[last]) {
+            // A trimmed sequence goes on inside a block that was full: its
+            // contents are about to differ from what its key says.
+            bm->unkey(last);
         }
     }
     s.num_tokens += 1;
@@ -226,6 +230,23 @@ extern "C" int pa_bm_free_seq(pa_bm *bm, int seq_id) {
         if (--bm->refcount[*b] == 0) bm->release(*b);
     }
     bm->seqs.erase(it);
+    return PA_OK;
+}
+
+extern "C" int pa_bm_trim_seq(pa_bm *bm, int seq_id, int num_tokens) {
+    if (!bm || num_tokens < 0) return pa_fail(PA_ERR_INVALID_ARG, "pa_bm_trim_seq: bad manager or length");
+    auto it = bm->seqs.find(seq_id);
+    if (it == bm->seqs.end()) return pa_fail(PA_ERR_REFCOUNT, "pa_bm_trim_seq: unknown sequence");
+    PaSeq &s = it->second;
+    if (num_tokens > s.num_tokens)
+        return pa_fail(PA_ERR_INVALID_ARG, "pa_bm_trim_seq: the sequence holds fewer tokens");
+    const size_t keep = static_cast<size_t>((static_cast<int64_t>(num_tokens) + bm->block_size - 1) / bm->block_size);
+    while (s.blocks.size() > keep) {
+        const int32_t b = s.blocks.back();
+        s.blocks.pop_back();
+        if (--bm->refcount[b] == 0) bm->release(b);
+    }
+    s.num_tokens = num_tokens;
     return PA_OK;
 }
 

@@ -1,0 +1,122 @@
+// pa_decode_tree and pa_decode_cross: checks, workspace and dispatch.
+#include <climits>
+
+#include "pa_multi.cuh"
+
+namespace {
+
+using namespace pa::host;
+
+struct MultiLayout {
+    size_t acc, bytes;   // where the rows' sums start, and the workspace's size
+    int rows;            // rows per partial
+};
+
+MultiLayout multi_layout(int num_tokens, int group, int head_dim) {
+    const long long need = static_cast<long long>(num_tokens) * group;
+    MultiLayout l;
+    l.rows = static_cast<int>(need < pa::kMultiSimtRows ? need : pa::kMultiSimtRows);
+    const size_t slots = 2ull * pa::kMultiSimtCtas * l.rows;
+    l.acc = align256(slots * 2 * sizeof(float));
+    l.bytes = l.acc + align256(slots * head_dim * sizeof(float));
+    return l;
+}
+
+int decode_multi(void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                 const int32_t *context_lens, const int32_t *query_start, const uint64_t *mask, int see,
+                 int num_q_heads, int num_kv_heads, int head_dim, int block_size, float scale, int num_tokens,
+                 int mask_words, const pa_decode_args *a) {
+    if (!a) return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_tree/cross: args is NULL");
+    if (a->num_seqs < 0 || num_tokens < 0) return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_tree/cross: negative sizes");
+    if (a->dtype != PA_F32 && a->dtype != PA_BF16)
+        return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_tree/cross: bad dtype");
+    if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0)
+        return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_tree/cross: num_q_heads must be a positive multiple of num_kv_heads");
+    if (head_dim != 64 && head_dim != 128)
+        return pa_fail(PA_ERR_UNSUPPORTED, "pa_decode_tree/cross: head_dim must be 64 or 128");
+    if (block_size != 16 && block_size != 32)
+        return pa_fail(PA_ERR_UNSUPPORTED, "pa_decode_tree/cross: block_size must be 16 or 32");
+    if (a->phase != PA_PHASE_ALL || a->simt || a->k_new || a->v_new || a->slot_mapping || a->partition_size)
+        return pa_fail(PA_ERR_UNSUPPORTED,
+                       "pa_decode_tree/cross: phase, simt, k_new, v_new, slot_mapping and partition_size must be 0");
+    if (a->num_blocks <= 0 || a->max_blocks_per_seq <= 0 || a->max_context_len < 0)
+        return pa_fail(PA_ERR_INVALID_ARG,
+                       "pa_decode_tree/cross: bad num_blocks, max_blocks_per_seq or max_context_len");
+    if (a->num_seqs == 0 || num_tokens == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start)
+        return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_tree/cross: null tensor pointer");
+    if (mask ? mask_words < 1 || mask_words > PA_TREE_MAX_NODES / 64 : mask_words != 0)
+        return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_tree: mask_words must be 1 to 16, and 0 without a mask");
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+        return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_tree/cross: out, q and caches must be 16-byte aligned");
+    const uintptr_t words = reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
+                            reinterpret_cast<uintptr_t>(query_start) | reinterpret_cast<uintptr_t>(a->dev_status);
+    if ((words & 3u) || (reinterpret_cast<uintptr_t>(mask) & 7u))
+        return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_tree/cross: misaligned pointer");
+    const long long total_rows = static_cast<long long>(a->num_blocks) * num_kv_heads * block_size;
+    if (total_rows >= INT_MAX || static_cast<long long>(num_tokens) * num_q_heads >= INT_MAX / 2)
+        return pa_fail(PA_ERR_UNSUPPORTED, "pa_decode_tree/cross: 2^31 or more cache rows, or 2^30 or more query rows");
+    const MultiLayout lay = multi_layout(num_tokens, num_q_heads / num_kv_heads, head_dim);
+    if (!a->workspace || a->workspace_bytes < lay.bytes || !aligned16(a->workspace))
+        return pa_fail(PA_ERR_WORKSPACE,
+                       "pa_decode_tree/cross: workspace missing, unaligned or smaller than pa_decode_tree_workspace_size()");
+    pa::MultiParams p{};
+    p.out = out;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_start = query_start;
+    p.mask = reinterpret_cast<const unsigned long long *>(mask);
+    p.part_ml = static_cast<float *>(a->workspace);
+    p.part_acc = reinterpret_cast<float *>(static_cast<char *>(a->workspace) + lay.acc);
+    p.status = a->dev_status;
+    p.num_seqs = a->num_seqs;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_q_heads / num_kv_heads;
+    p.block_size = block_size;
+    p.num_blocks = a->num_blocks;
+    p.width = a->max_blocks_per_seq;
+    const long long table_cap = static_cast<long long>(a->max_blocks_per_seq) * block_size;
+    p.ctx_cap = static_cast<int>(a->max_context_len < table_cap ? a->max_context_len : table_cap);
+    p.words = mask_words;
+    p.see = see;
+    p.slot_rows = lay.rows;
+    p.total_rows = static_cast<int>(total_rows);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return pa_fail(PA_ERR_CUDA, "pa_decode_tree/cross: no CUDA device");
+    if (sm_count(dev) <= 0) return pa_fail(PA_ERR_CUDA, "pa_decode_tree/cross: cannot query the SM count");
+    return pa::launch_multi_simt(p, a->dtype == PA_F32, head_dim, dev, static_cast<cudaStream_t>(a->stream));
+}
+
+}  // namespace
+
+extern "C" size_t pa_decode_tree_workspace_size(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim) {
+    if (num_tokens <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || head_dim <= 0)
+        return 0;
+    return multi_layout(num_tokens, num_q_heads / num_kv_heads, head_dim).bytes;
+}
+
+extern "C" int pa_decode_tree(void *out, const void *q, const void *k_cache, const void *v_cache,
+                              const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
+                              const uint64_t *tree_mask, int num_q_heads, int num_kv_heads, int head_dim,
+                              int block_size, float scale, int num_tokens, int mask_words,
+                              const pa_decode_args *args) {
+    PaTraceRange trace("pa_decode_tree");
+    return decode_multi(out, q, k_cache, v_cache, block_tables, context_lens, query_start, tree_mask,
+                        tree_mask ? pa::kSeeMask : pa::kSeeChain, num_q_heads, num_kv_heads, head_dim, block_size,
+                        scale, num_tokens, mask_words, args);
+}
+
+extern "C" int pa_decode_cross(void *out, const void *q, const void *k_cache, const void *v_cache,
+                               const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
+                               int num_q_heads, int num_kv_heads, int head_dim, int block_size, float scale,
+                               int num_tokens, const pa_decode_args *args) {
+    PaTraceRange trace("pa_decode_cross");
+    return decode_multi(out, q, k_cache, v_cache, block_tables, context_lens, query_start, nullptr, pa::kSeeAll,
+                        num_q_heads, num_kv_heads, head_dim, block_size, scale, num_tokens, 0, args);
+}

@@ -187,6 +187,81 @@ class Q4DecodeStep(_KeptCall):
         return self.decode(stream)
 
 
+class _MultiStep(_KeptCall):
+    """Holds the output, workspace and status word of a repeated step with
+    several queries per sequence, and its call, checked once and kept until an
+    attribute of the step is assigned (a tensor resized or moved in place, with
+    ``set_`` or ``.data``, is not noticed: assign it)."""
+
+    tree_mask = None
+
+    def __init__(self, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                 context_lens: torch.Tensor, query_start: torch.Tensor, scale: float, max_context_len: int,
+                 workspace: torch.Tensor | None = None, status: binding.DeviceStatus | None = None):
+        self.q, self.k_cache, self.v_cache = q, k_cache, v_cache
+        self.block_tables, self.context_lens, self.query_start = block_tables, context_lens, query_start
+        self.scale, self.max_context_len = scale, max_context_len
+        self.out = torch.empty_like(q)
+        self.status = status if status is not None else binding.DeviceStatus(q.device)
+        T, Hq, hd = q.shape
+        # only the header has to be zero, for a pa_decode call that may use it later
+        self.workspace = _own_workspace(workspace, binding.pa_decode_tree_workspace_size(T, Hq, k_cache.shape[1], hd),
+                                        q.device, zeroed=256)
+
+    def decode(self, stream=None) -> torch.Tensor:
+        call = self._call
+        if call is None:
+            call = binding._multi_call(self._tree, self.out, self.q, self.k_cache, self.v_cache, self.block_tables,
+                                       self.context_lens, self.query_start, self.tree_mask, self.scale,
+                                       self.max_context_len, self.workspace, self.status, stream)
+            if call.owns_workspace(self.workspace):
+                self._call = call
+        return call(stream)
+
+
+class TreeDecodeStep(_MultiStep):
+    """The step that verifies drafted tokens: their rows are written to the
+    cache, each attends to the context and to its ancestors
+    (``pa_decode_tree``), and ``commit`` moves the rows of the path that was
+    kept.  q is [T, Hq, hd], every sequence's drafted tokens end to end;
+    tree_mask int64 [T, W] from ``pa_build_tree``, or None for chains."""
+
+    _tree = True
+
+    def __init__(self, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                 context_lens: torch.Tensor, query_start: torch.Tensor, scale: float, max_context_len: int,
+                 tree_mask: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 status: binding.DeviceStatus | None = None):
+        super().__init__(q, k_cache, v_cache, block_tables, context_lens, query_start, scale, max_context_len,
+                         workspace, status)
+        self.tree_mask = tree_mask
+
+    def write_tokens(self, k_new, v_new, slot_mapping, cow_pairs=None, stream=None) -> None:
+        """The step's cache updates: copy-on-write copies, then the drafted tokens' rows."""
+        if cow_pairs is not None and cow_pairs.numel():
+            binding.pa_copy_blocks(self.k_cache, self.v_cache, cow_pairs, status=self.status, stream=stream)
+        if slot_mapping.numel():
+            binding.pa_reshape_and_cache(k_new, v_new, self.k_cache, self.v_cache, slot_mapping,
+                                         status=self.status, stream=stream)
+
+    def run(self, k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
+            cow_pairs: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        self.write_tokens(k_new, v_new, slot_mapping, cow_pairs, stream)
+        return self.decode(stream)
+
+    def commit(self, slot_pairs: torch.Tensor, stream=None) -> None:
+        """Move the kept path's rows (``pa_accept_tree``'s slot_pairs) to where the sequences go on."""
+        binding.pa_move_rows(self.k_cache, self.v_cache, slot_pairs, status=self.status, stream=stream)
+
+
+class CrossDecodeStep(_MultiStep):
+    """Attention of a decoder's queries, any number per request, over the
+    paged states of its encoder (``pa_decode_cross``).  The caches, tables and
+    lengths are the encoder's; q is [T, Hq, hd], request by request."""
+
+    _tree = False
+
+
 def prefix_share_state(device="cuda", seed: int | None = None) -> dict:
     """The prefix-sharing workload driven through the host block manager.
 
@@ -231,4 +306,4 @@ def prefix_share_state(device="cuda", seed: int | None = None) -> dict:
     )
 
 
-__all__ = ["DecodeStep", "Q4DecodeStep", "prefix_share_state", "WORKLOADS"]
+__all__ = ["DecodeStep", "Q4DecodeStep", "TreeDecodeStep", "CrossDecodeStep", "prefix_share_state", "WORKLOADS"]
