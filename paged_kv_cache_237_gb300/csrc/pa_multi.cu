@@ -12,11 +12,13 @@ struct MultiLayout {
     int rows;            // rows per partial
 };
 
-MultiLayout multi_layout(int num_tokens, int group, int head_dim) {
+// num_tokens rows of `group` heads: an item has no more rows than that.
+MultiLayout multi_layout(int num_tokens, int group, int head_dim, bool f32) {
     const long long need = static_cast<long long>(num_tokens) * group;
+    const int most = f32 ? pa::kMultiSimtRows : pa::kMultiMmaRows;
     MultiLayout l;
-    l.rows = static_cast<int>(need < pa::kMultiSimtRows ? need : pa::kMultiSimtRows);
-    const size_t slots = 2ull * pa::kMultiSimtCtas * l.rows;
+    l.rows = static_cast<int>(need < most ? need : most);
+    const size_t slots = 2ull * (f32 ? pa::kMultiSimtCtas : pa::kMultiMmaCtas) * l.rows;
     l.acc = align256(slots * 2 * sizeof(float));
     l.bytes = l.acc + align256(slots * head_dim * sizeof(float));
     return l;
@@ -56,7 +58,7 @@ int decode_multi(void *out, const void *q, const void *k_cache, const void *v_ca
     const long long total_rows = static_cast<long long>(a->num_blocks) * num_kv_heads * block_size;
     if (total_rows >= INT_MAX || static_cast<long long>(num_tokens) * num_q_heads >= INT_MAX / 2)
         return pa_fail(PA_ERR_UNSUPPORTED, "pa_decode_tree/cross: 2^31 or more cache rows, or 2^30 or more query rows");
-    const MultiLayout lay = multi_layout(num_tokens, num_q_heads / num_kv_heads, head_dim);
+    const MultiLayout lay = multi_layout(num_tokens, num_q_heads / num_kv_heads, head_dim, a->dtype == PA_F32);
     if (!a->workspace || a->workspace_bytes < lay.bytes || !aligned16(a->workspace))
         return pa_fail(PA_ERR_WORKSPACE,
                        "pa_decode_tree/cross: workspace missing, unaligned or smaller than pa_decode_tree_workspace_size()");
@@ -90,7 +92,8 @@ int decode_multi(void *out, const void *q, const void *k_cache, const void *v_ca
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return pa_fail(PA_ERR_CUDA, "pa_decode_tree/cross: no CUDA device");
     if (sm_count(dev) <= 0) return pa_fail(PA_ERR_CUDA, "pa_decode_tree/cross: cannot query the SM count");
-    return pa::launch_multi_simt(p, a->dtype == PA_F32, head_dim, dev, static_cast<cudaStream_t>(a->stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(a->stream);
+    return a->dtype == PA_F32 ? pa::launch_multi_simt(p, head_dim, dev, st) : pa::launch_multi_mma(p, head_dim, dev, st);
 }
 
 }  // namespace
@@ -98,7 +101,10 @@ int decode_multi(void *out, const void *q, const void *k_cache, const void *v_ca
 extern "C" size_t pa_decode_tree_workspace_size(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim) {
     if (num_tokens <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || head_dim <= 0)
         return 0;
-    return multi_layout(num_tokens, num_q_heads / num_kv_heads, head_dim).bytes;
+    const int group = num_q_heads / num_kv_heads;
+    const size_t bf16 = multi_layout(num_tokens, group, head_dim, false).bytes;
+    const size_t f32 = multi_layout(num_tokens, group, head_dim, true).bytes;
+    return bf16 > f32 ? bf16 : f32;
 }
 
 extern "C" int pa_decode_tree(void *out, const void *q, const void *k_cache, const void *v_cache,

@@ -288,7 +288,9 @@ int launch_join(const MultiParams &p, int pass_grid, cudaStream_t st) {
 // CTAs of a pass at most (a workspace has two partials for each), and the rows
 // of its items.
 constexpr int kMultiSimtCtas = 608, kMultiSimtRows = 32;
+constexpr int kMultiMmaCtas = 152, kMultiMmaRows = 256;
 
-int launch_multi_simt(const MultiParams &p, bool f32, int head_dim, int dev, cudaStream_t st);
+int launch_multi_simt(const MultiParams &p, int head_dim, int dev, cudaStream_t st);   // fp32
+int launch_multi_mma(const MultiParams &p, int head_dim, int dev, cudaStream_t st);    // bf16
 
 }  // namespace pa

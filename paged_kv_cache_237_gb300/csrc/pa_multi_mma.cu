@@ -1,0 +1,638 @@
+// pa_decode_tree and pa_decode_cross over bf16 caches, on tcgen05.
+//
+// An item is up to 256 rows (query tokens x the heads of one KV head) against a
+// stretch of the sequence's cache in tiles of 128 tokens.  One CTA per SM runs
+// two streams, each with its own 128 rows of scores S, its own sums O (both in
+// tensor memory), running maximum and sum:
+//   more than 128 rows: stream s has rows 128 s.. and both use every tile;
+//   at most 128 rows: both have the same rows, stream s takes every second tile,
+//   and the two are joined at the end of the item.
+// So while one stream's softmax runs, the tensor core works for the other, and a
+// decode step's few rows keep as many copies in flight as a prompt's many.
+//
+// Roles (warps): 0-3 and 4-7 the streams' softmax, a thread per row; 8 the
+// copies; 9 the matrix instructions; 10 and 11 nothing (registers move between
+// whole groups of four warps: 12 x 168 at launch, 8 x 216 + 4 x 72 then).
+//   S = Q K^T      128 x 128 x head_dim, Q and K in shared memory (128-byte swizzle)
+//   O += P V       128 x head_dim x 128, P in tensor memory over S, V in shared
+//                  memory as it is cached (tokens x head_dim, the MN-major form)
+// p enters as the sum of two bf16 parts (about 16 significant bits), as in
+// pa_decode, so two products per tile of V.  Row maxima are references that only
+// move when a tile's maximum is more than 2^8 above: then the row's O and sum are
+// rescaled (p stays below 2^8, and fp32 sums lose nothing by it).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "pa_multi.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kTile = 128;                 // tokens per tile, and rows per stream
+constexpr int kMmaThreads = 384;
+using Axis = MultiAxis<kMultiMmaRows, kTile, 2>;
+
+// ---------------------------------------------------------------- tcgen05 ---
+__device__ __forceinline__ void tm_alloc(uint32_t dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tm_dealloc(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of this thread's lane.  The values are there after tm_wait_ld().
+__device__ __forceinline__ void tm_ld32(uint32_t addr, float *r) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+          "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+          "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t *u) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(u[0]),
+        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
+        "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]),
+        "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]),
+        "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t *u) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(u[0]),
+        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
+        "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+// Arrives at `bar` once every matrix instruction issued so far is done.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Shared-memory operand in 128-byte swizzled rows; 8-row groups follow each other.
+// K-major (Q, K): the row is along head_dim.  MN-major (V): the row is along
+// head_dim too, but that is N, so the next 64 columns are `next` bytes away.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t next) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>((next >> 4) & 0x3fffu) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// bf16 x bf16 -> fp32, 128 rows, n columns.
+constexpr __host__ __device__ uint32_t mma_idesc(int n, bool b_mn_major) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n / 8) << 17) |
+           (static_cast<uint32_t>(128 / 16) << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint64_t l2_normal_policy() {
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+
+// Shared memory: Q (two tiles), rings of K and V tiles, then the small things.
+template <int HD>
+struct Smem {
+    static constexpr int TILE = kTile * HD * 2, SLAB = kTile * 128;   // a slab: 64 columns of a tile
+    static constexpr int NK = HD == 128 ? 3 : 6, NV = HD == 128 ? 2 : 6;
+    static constexpr int K = 2 * TILE, V = K + NK * TILE, END = V + NV * TILE;
+    static constexpr int BYTES = END + 1024;   // and room to align
+};
+
+struct Control {
+    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], s_full[2], p_full[2], o_full[2], q_full, e_full;
+    int dirty[2];          // number of the item whose drafted tokens have values that are not finite, by its parity
+    int failed;
+    uint32_t tmem;
+    MultiSpot spot;
+};
+
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    template <int N>
+    __device__ __forceinline__ void advance() {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// Waits give up after about two seconds, or when another role has; every role
+// then leaves its loop.
+__device__ __forceinline__ bool await(Control &c, uint64_t *bar, uint32_t parity) {
+    const uint32_t b = smem_addr(bar);
+    if (mbar_try_wait(b, parity)) return true;
+    const uint64_t start = global_timer_ns();
+    for (uint32_t spin = 1;; ++spin) {
+        if (mbar_try_wait(b, parity)) return true;
+        if ((spin & 63u) == 0) {
+            if (*static_cast<volatile int *>(&c.failed)) return false;
+            if (global_timer_ns() - start > kWaitLimitNs) {
+                *static_cast<volatile int *>(&c.failed) = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// The same for a whole warp: all lanes go on, or none.
+__device__ __forceinline__ bool await_warp(Control &c, uint64_t *bar, uint32_t parity) {
+    return __all_sync(kFull, await(c, bar, parity));
+}
+
+// Which of the 32 positions from u on a row sees, as bits.
+__device__ __forceinline__ uint32_t seen_bits(const MultiParams &p, const MultiSeq &s, int tok, int u) {
+    const auto below = [](int count) { return count <= 0 ? 0u : (count >= 32 ? ~0u : (1u << count) - 1u); };
+    const int base = s.n - s.c;
+    if (p.see == kSeeAll) return below(s.n - u);
+    if (p.see == kSeeChain) return below(min(s.n, base + tok + 1) - u);
+    uint32_t bits = below(base - u);
+    const int j = u - base;   // first position's node, negative before the tree
+    if (j > -32 && u < s.n) {
+        const unsigned long long *row = p.mask + static_cast<long long>(s.start + tok) * p.words;
+        const int w = j >> 6;
+        const unsigned long long a = w >= 0 && w < p.words ? row[w] : 0ull;
+        const unsigned long long b = w + 1 >= 0 && w + 1 < p.words ? row[w + 1] : 0ull;
+        const int sh = j & 63;
+        bits |= static_cast<uint32_t>(sh ? (a >> sh) | (b << (64 - sh)) : a);
+    }
+    return bits & below(s.n - u);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+    multi_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const MultiParams p) {
+    using M = Smem<HD>;
+    constexpr uint32_t kIdescS = mma_idesc(kTile, false), kIdescO = mma_idesc(HD, true);
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Control ctl;
+    const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t *smem_p = smem_raw + (smem - smem_addr(smem_raw));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(smem_addr(&ctl.k_full[i]), 1);
+            mbar_init(smem_addr(&ctl.k_empty[i]), 1);
+            mbar_init(smem_addr(&ctl.v_full[i]), 1);
+            mbar_init(smem_addr(&ctl.v_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&ctl.s_full[i]), 1);
+            mbar_init(smem_addr(&ctl.p_full[i]), kTile);
+            mbar_init(smem_addr(&ctl.o_full[i]), 1);
+            ctl.dirty[i] = 0;
+        }
+        mbar_init(smem_addr(&ctl.q_full), 2 * kTile);
+        mbar_init(smem_addr(&ctl.e_full), 2 * kTile);
+        ctl.failed = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    if (warp == 9) tm_alloc(smem_addr(&ctl.tmem), 512);
+    griddep_wait();
+    int flags = 0;
+    const MultiLocator<Axis, kMmaThreads> loc(p, flags);
+    if (flags && blockIdx.x == 0) flag_status(p.status, flags);
+    const long long ctas = multi_ctas(loc.total, gridDim.x);
+    const bool idle = blockIdx.x >= ctas;
+    const long long unit = idle ? 0 : multi_start(loc.total, ctas, blockIdx.x);
+    long long left = idle ? 0 : multi_start(loc.total, ctas, blockIdx.x + 1) - unit;
+    if (!idle) loc.find(p, unit, &ctl.spot);
+    tm_fence_before();
+    __syncthreads();
+    tm_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    MultiSpot spot = ctl.spot;
+    MultiItem it;
+
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8) {
+        // ------------------------------------------------------- copies ---
+        const int pages = kTile / p.block_size, box_bytes = p.block_size * 128;
+        const uint64_t once = l2_evict_first_policy(), again = l2_normal_policy();
+        Ring k, v;
+        bool ok = true;
+        while (ok && Axis::next(p, spot, left, it)) {
+            const int seen = Axis::seen(p, it.s, it.m), rows = it.s.c * p.group - it.m * kMultiMmaRows;
+            const int lag = rows > kTile ? 0 : 1;   // a V tile is needed after the next tile's K if the streams alternate
+            const uint64_t policy = Axis::row_blocks(p, it.s) > 1 ? again : once;
+            const int32_t *table = p.block_tables + static_cast<long long>(it.seq) * p.width;
+            // Lane l holds page l of a window of 32 pages, as a row of the cache view.
+            const auto page_row = [&](int page) {
+                const long long u = static_cast<long long>(page) * p.block_size;
+                if (u >= seen || page >= it.tile1 * pages) return p.total_rows;
+                const int b = table[page];
+                if (b < 0 || b >= p.num_blocks) {
+                    flag_status(p.status, PA_STATUS_BAD_BLOCK_ID);
+                    return p.total_rows;
+                }
+                return static_cast<int>((static_cast<long long>(b) * p.num_kv_heads + it.kvh) * p.block_size);
+            };
+            int window = it.tile0 * pages, now = page_row(window + lane), ahead = page_row(window + 32 + lane);
+            int row = p.total_rows, row_v = p.total_rows;
+            const auto issue = [&](const CUtensorMap *map, int r, uint32_t dst, uint64_t *full) {
+                if (lane == 0) mbar_arrive_expect_tx(smem_addr(full), M::TILE);
+                __syncwarp();
+                if (lane < pages)
+#pragma unroll
+                    for (int h = 0; h < HD / 64; ++h)
+                        tma_load_2d_hint(dst + h * M::SLAB + lane * box_bytes, map, h * 64, r, smem_addr(full), policy);
+            };
+            for (int t = it.tile0; t < it.tile1 + lag; ++t) {
+                if (lag) row_v = row;
+                if (t < it.tile1) {
+                    if (t * pages >= window + 32) {
+                        window += 32;
+                        now = ahead;
+                        ahead = page_row(window + 32 + lane);
+                    }
+                    row = __shfl_sync(kFull, now, (t * pages - window + lane) & 31);
+                    if (!(ok = await_warp(ctl, &ctl.k_empty[k.slot], k.phase ^ 1))) break;
+                    issue(&tmK, row, smem + M::K + k.slot * M::TILE, &ctl.k_full[k.slot]);
+                    k.advance<M::NK>();
+                }
+                if (!lag) row_v = row;
+                if (t >= it.tile0 + lag) {
+                    if (!(ok = await_warp(ctl, &ctl.v_empty[v.slot], v.phase ^ 1))) break;
+                    issue(&tmV, row_v, smem + M::V + v.slot * M::TILE, &ctl.v_full[v.slot]);
+                    v.advance<M::NV>();
+                }
+            }
+        }
+    } else if (warp == 9) {
+        // --------------------------------------------- matrix instructions ---
+        if (lane == 0) {
+            Ring k, v;
+            uint32_t items = 0, steps[2] = {0, 0};
+            bool ok = true;
+            while (ok && Axis::next(p, spot, left, it)) {
+                const bool both = it.s.c * p.group - it.m * kMultiMmaRows > kTile;
+                const int tiles = it.tile1 - it.tile0, count = both ? 2 * tiles : tiles;
+                if (!(ok = await(ctl, &ctl.q_full, items++ & 1))) break;
+                tm_fence_after();
+                const auto scores = [&](int j) {
+                    const int s = j & 1;
+                    if ((!both || s == 0) && !await(ctl, &ctl.k_full[k.slot], k.phase)) return false;
+                    const uint64_t a = smem_desc(smem + (both ? s * M::TILE : 0), 16);
+                    const uint64_t b = smem_desc(smem + M::K + k.slot * M::TILE, 16);
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk) {
+                        const uint32_t at = ((kk / 4) * M::SLAB + (kk % 4) * 32) >> 4;
+                        mma_ss(tmem + s * kTile, a + at, b + at, kIdescS, kk > 0);
+                    }
+                    mma_commit(smem_addr(&ctl.s_full[s]));
+                    if (!both || s == 1) {
+                        mma_commit(smem_addr(&ctl.k_empty[k.slot]));
+                        k.advance<M::NK>();
+                    }
+                    return true;
+                };
+                ok = scores(0) && (count < 2 || scores(1));
+                for (int j = 0; ok && j < count; ++j) {
+                    const int s = j & 1;
+                    if ((!both || s == 0) && !(ok = await(ctl, &ctl.v_full[v.slot], v.phase))) break;
+                    if (!(ok = await(ctl, &ctl.p_full[s], steps[s]++ & 1))) break;
+                    tm_fence_after();
+                    const uint32_t pt = tmem + s * kTile, o = tmem + 256 + s * kTile;
+                    const uint64_t b = smem_desc(smem + M::V + v.slot * M::TILE, M::SLAB);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            mma_ts(o, pt + part * 64 + kk * 8, b + ((kk * 16 * 128) >> 4), kIdescO,
+                                   j >= 2 || part > 0 || kk > 0);
+                    if (j + 2 >= count) mma_commit(smem_addr(&ctl.o_full[s]));
+                    if (!both || s == 1) {
+                        mma_commit(smem_addr(&ctl.v_empty[v.slot]));
+                        v.advance<M::NV>();
+                    }
+                    if (j + 2 < count) ok = scores(j + 2);
+                }
+            }
+        }
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // ------------------------------------------------------- softmax ---
+        const int s = warp >> 2, r = tid & (kTile - 1);   // stream, and row of its tile
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // first lane of this warp's quarter, in bits 16..
+        const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 256 + s * kTile;
+        const float scale = fmaxf(fabsf(p.scale_log2), 1.2e-38f);   // the sign goes into Q; zero stays finite on -inf
+        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+        uint32_t step = 0, ends = 0;
+        int item_no = 0;
+        float2 *const ml = reinterpret_cast<float2 *>(smem_p + M::TILE);   // one tile of rows leaves the second unused
+        Ring v;
+        bool ok = true;
+        while (ok && Axis::next(p, spot, left, it)) {
+            ++item_no;
+            const int R0 = it.m * kMultiMmaRows, total = it.s.c * p.group - R0;
+            const bool both = total > kTile;
+            const int rows = both ? min(kTile, total - s * kTile) : total;   // of this stream's tile
+            const int row0 = R0 + (both ? s * kTile : 0);
+            const int tok = min(row0 + r, it.s.c * p.group - 1) / p.group;
+            const int seen = Axis::seen(p, it.s, it.m), base = it.s.n - it.s.c;
+            const int clear = p.see == kSeeAll ? it.s.n : base;   // every row sees every position before
+            {
+                // Q, zero behind the last row: its tile per stream, or half of the one tile.
+                constexpr int C = HD / 8;
+                uint8_t *tile = smem_p + (both ? s * M::TILE : 0);
+                const int first = both ? 0 : s * (kTile / 2), span = both ? kTile : kTile / 2;
+                for (int i = r; i < span * C; i += kTile) {
+                    const int qr = first + i / C, c = i % C;
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (qr < rows) {
+                        x = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
+                                                             multi_row(p, it.s, it.kvh, row0 + qr, HD) + c * 8);
+                        x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
+                    }
+                    *reinterpret_cast<uint4 *>(tile + (c / 8) * M::SLAB + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) = x;
+                }
+                fence_proxy_async_smem();
+                tm_fence_before();
+                mbar_arrive(smem_addr(&ctl.q_full));
+            }
+            const bool live = (warp & 3) * 32 < rows;   // this warp has rows
+            float ref = -INFINITY, sum = 0.f;
+            const int tiles = it.tile1 - it.tile0;
+            int mine = 0;   // steps of this stream
+            for (int t = 0; t < tiles; ++t) {
+                const bool take = both || (t & 1) == s;
+                if (take) {
+                    const int u0 = (it.tile0 + t) * kTile;
+                    // First the scores: they were issued behind the products of this stream's tile before, so the
+                    // V ring's barrier is in the phase before the awaited one at least.
+                    if (!(ok = await_warp(ctl, &ctl.s_full[s], step & 1))) break;
+                    tm_fence_after();
+                    if (u0 + kTile > clear || u0 + kTile > seen) {
+                        // Values that some row does not see: what lies behind the last seen token becomes zero, and
+                        // so do values of drafted tokens that are not finite (added again where they are seen).
+                        if (!(ok = await_warp(ctl, &ctl.v_full[v.slot], v.phase))) break;
+                        uint8_t *vt = smem_p + M::V + v.slot * M::TILE;
+                        const int from = max(0, min(kTile, clear - u0));
+                        for (int i = from * (HD / 8) + r; i < kTile * (HD / 8); i += kTile) {
+                            const int j = i / (HD / 8), c = i % (HD / 8);
+                            uint4 *at = reinterpret_cast<uint4 *>(vt + (c / 8) * M::SLAB + j * 128 + (c & 7) * 16);
+                            if (u0 + j >= seen) {
+                                *at = make_uint4(0u, 0u, 0u, 0u);
+                            } else {
+                                uint4 x = *at;
+                                uint32_t *w = &x.x;
+                                bool bad = false;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if ((w[e] & 0x7f80u) == 0x7f80u) bad = true, w[e] &= 0xffff0000u;
+                                    if ((w[e] & 0x7f800000u) == 0x7f800000u) bad = true, w[e] &= 0xffffu;
+                                }
+                                if (bad) {
+                                    *at = x;
+                                    ctl.dirty[item_no & 1] = item_no;
+                                }
+                            }
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    if (live) {
+                        float x[kTile];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) tm_ld32(ts + g * 32, x + g * 32);
+                        tm_wait_ld();
+                        if (u0 + kTile > clear) {
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const uint32_t bits = seen_bits(p, it.s, tok, u0 + g * 32);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    if (!((bits >> c) & 1u)) x[g * 32 + c] = -INFINITY;
+                            }
+                        }
+                        float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                        for (int c = 4; c < kTile; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
+                        const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+                        if (mine == 0) {
+                            ref = best;
+                        } else if (__any_sync(kFull, best > ref + 8.f)) {
+                            const float now = fmaxf(ref, best);
+                            const float f = now == ref ? 1.f : ex2(ref - now);
+                            // O holds the products of the step before: these scores were issued behind them, and
+                            // their barrier waits for every matrix instruction issued so far
+#pragma unroll
+                            for (int g = 0; g < HD / 32; ++g) {
+                                float o[32];
+                                tm_ld32(to + g * 32, o);
+                                tm_wait_ld();
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) o[c] *= f;
+                                tm_st32(to + g * 32, reinterpret_cast<uint32_t *>(o));
+                            }
+                            sum *= f;
+                            ref = now;
+                        }
+                        const float shift = ref == -INFINITY ? 0.f : -ref;
+                        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            uint32_t hi[16], lo[16];
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                const float a = ex2(fmaf(x[g * 32 + 2 * c], scale, shift));
+                                const float b = ex2(fmaf(x[g * 32 + 2 * c + 1], scale, shift));
+                                part[(2 * c) & 3] += a;
+                                part[(2 * c + 1) & 3] += b;
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                                memcpy(&hi[c], &h, 4);
+                                const __nv_bfloat162 l = __floats2bfloat162_rn(a - __uint_as_float(hi[c] << 16),
+                                                                               b - __uint_as_float(hi[c] & 0xffff0000u));
+                                memcpy(&lo[c], &l, 4);
+                            }
+                            tm_st16(ts + g * 16, hi);
+                            tm_st16(ts + 64 + g * 16, lo);
+                        }
+                        sum += (part[0] + part[1]) + (part[2] + part[3]);
+                        tm_wait_st();
+                    }
+                    tm_fence_before();
+                    mbar_arrive(smem_addr(&ctl.p_full[s]));
+                    ++step;
+                    ++mine;
+                }
+                v.advance<M::NV>();
+            }
+            if (!ok) break;
+            // The item's end: all products are in, and both streams say what they have.
+            if (mine > 0 && !(ok = await_warp(ctl, &ctl.o_full[s], ends++ & 1))) break;
+            tm_fence_after();
+            if (!both) ml[s * kTile + r] = make_float2(ref, sum);
+            tm_fence_before();
+            mbar_arrive(smem_addr(&ctl.e_full));
+            if (!(ok = await_warp(ctl, &ctl.e_full, (item_no - 1) & 1))) break;
+            tm_fence_after();
+            if (live) {
+                const bool dirty = ctl.dirty[item_no & 1] == item_no;
+                float f[2], top = ref, all = sum;
+                if (both) {
+                    f[0] = f[1] = 1.f;
+                } else {
+                    const float2 a = ml[r], b = ml[kTile + r];
+                    top = fmaxf(a.x, b.x);
+                    const float at = top == -INFINITY ? 0.f : top;
+                    f[0] = ex2(a.x - at);
+                    f[1] = ex2(b.x - at);
+                    all = f[0] * a.y + f[1] * b.y;
+                }
+                const bool second = !both && tiles > 1;
+                const float inv = all == 0.f ? 0.f : 1.f / all;
+                const bool whole = it.whole();
+                const long long at = static_cast<long long>(it.slot(blockIdx.x)) * p.slot_rows + (both ? s * kTile : 0) + r;
+                // one tile: each stream's threads write half of the columns
+                const int g0 = both ? 0 : s * (HD / 64), g1 = both ? HD / 32 : g0 + HD / 64;
+                for (int g = g0; g < g1; ++g) {
+                    float o[32];
+                    tm_ld32((both ? to : tmem + lanes + 256) + g * 32, o);
+                    tm_wait_ld();
+                    if (!both) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] *= f[0];
+                    }
+                    if (second) {
+                        float o1[32];
+                        tm_ld32(tmem + lanes + 256 + kTile + g * 32, o1);
+                        tm_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] = fmaf(o1[c], f[1], o[c]);
+                    }
+                    if (dirty && r < rows)
+                        for (int u = max(max(base, 0), it.tile0 * kTile); u < min(seen, it.tile1 * kTile); ++u) {
+                            if (!(seen_bits(p, it.s, tok, u) & 1u)) continue;
+                            const int b = p.block_tables[static_cast<long long>(it.seq) * p.width + u / p.block_size];
+                            if (b < 0 || b >= p.num_blocks) continue;
+                            const __nv_bfloat16 *vr =
+                                static_cast<const __nv_bfloat16 *>(p.v_cache) +
+                                ((static_cast<long long>(b) * p.num_kv_heads + it.kvh) * p.block_size + u % p.block_size) * HD;
+                            for (int c = 0; c < 32; ++c) {
+                                const float x = __bfloat162float(vr[g * 32 + c]);
+                                if (!isfinite(x)) o[c] += x;
+                            }
+                        }
+                    if (r < rows && whole) {
+                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) +
+                                             multi_row(p, it.s, it.kvh, row0 + r, HD) + g * 32;
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8) {
+                            uint4 x;
+                            uint32_t *w = &x.x;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 h =
+                                    __floats2bfloat162_rn(o[c + 2 * e] * inv, o[c + 2 * e + 1] * inv);
+                                memcpy(&w[e], &h, 4);
+                            }
+                            *reinterpret_cast<uint4 *>(out + c) = x;
+                        }
+                    } else if (r < rows) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            store4(p.part_acc + at * HD + g * 32 + c, make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
+                    }
+                }
+                if (!whole && r < rows && (both || s == 0))
+                    *reinterpret_cast<float2 *>(p.part_ml + 2 * at) = make_float2(top, all);
+            }
+        }
+    }
+
+    griddep_launch_dependents();
+    __syncwarp();
+    tm_fence_before();
+    __syncthreads();
+    tm_fence_after();
+    if (ctl.failed) {
+        // A wait gave up: copies and products in flight get a millisecond to land.
+        if (tid == 0) flag_status(p.status, PA_STATUS_WAIT_TIMEOUT);
+        for (const uint64_t start = global_timer_ns(); global_timer_ns() - start < 1000000ull;) {
+        }
+        __syncthreads();
+    }
+    if (warp == 9) tm_dealloc(tmem, 512);
+}
+
+// A cache seen as [rows][HD], boxes of one block's rows x 64 columns with the
+// 128-byte swizzle; rows past the end read as zeros.
+bool block_map(CUtensorMap *map, const void *base, long long rows, int hd, int block_size) {
+    const host::EncodeTiledFn enc = host::encode_tiled();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(hd) * 2};
+    cuuint32_t box[2] = {64, static_cast<cuuint32_t>(block_size)}, estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int HD>
+int multi_mma(const MultiParams &p, int dev, cudaStream_t st) {
+    static host::KernelSlot slot;
+    auto kernel = multi_mma_kernel<HD>;
+    if (host::ensure_kernel(kernel, slot, Smem<HD>::BYTES, dev, kMmaThreads) == 0)
+        return pa_fail(PA_ERR_CUDA, "pa_decode_tree/cross: cannot configure the bf16 kernel");
+    CUtensorMap mk, mv;
+    if (!block_map(&mk, p.k_cache, p.total_rows, HD, p.block_size) ||
+        !block_map(&mv, p.v_cache, p.total_rows, HD, p.block_size))
+        return pa_fail(PA_ERR_CUDA, "pa_decode_tree/cross: cuTensorMapEncodeTiled failed");
+    const int grid = min(host::sm_count(dev), kMultiMmaCtas);
+    const cudaError_t e = host::launch_dependent(kernel, grid, kMmaThreads, Smem<HD>::BYTES, st, mk, mv, p);
+    if (e != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
+    return launch_join<__nv_bfloat16, HD, Axis>(p, grid, st);
+}
+
+}  // namespace
+
+int launch_multi_mma(const MultiParams &p, int head_dim, int dev, cudaStream_t st) {
+    return head_dim == 128 ? multi_mma<128>(p, dev, st) : multi_mma<64>(p, dev, st);
+}
+
+}  // namespace pa

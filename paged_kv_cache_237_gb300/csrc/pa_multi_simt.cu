@@ -183,9 +183,8 @@ int multi_simt(const MultiParams &p, int dev, cudaStream_t st) {
     return launch_join<T, HD, Axis>(p, grid, st);
 }
 
-int launch_multi_simt(const MultiParams &p, bool f32, int head_dim, int dev, cudaStream_t st) {
-    if (f32) return head_dim == 128 ? multi_simt<float, 128>(p, dev, st) : multi_simt<float, 64>(p, dev, st);
-    return head_dim == 128 ? multi_simt<__nv_bfloat16, 128>(p, dev, st) : multi_simt<__nv_bfloat16, 64>(p, dev, st);
+int launch_multi_simt(const MultiParams &p, int head_dim, int dev, cudaStream_t st) {
+    return head_dim == 128 ? multi_simt<float, 128>(p, dev, st) : multi_simt<float, 64>(p, dev, st);
 }
 
 }  // namespace pa
