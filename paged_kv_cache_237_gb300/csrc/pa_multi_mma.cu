@@ -12,7 +12,7 @@
 //
 // Roles (warps): 0-3 and 4-7 the streams' softmax, a thread per row; 8 the
 // copies; 9 the matrix instructions; 10 and 11 nothing (registers move between
-// whole groups of four warps: 12 x 168 at launch, 8 x 216 + 4 x 72 then).
+// whole groups of four warps: 12 x 168 at launch, 8 x 224 + 4 x 56 then).
 //   S = Q K^T      128 x 128 x head_dim, Q and K in shared memory (128-byte swizzle)
 //   O += P V       128 x head_dim x 128, P in tensor memory over S, V in shared
 //                  memory as it is cached (tokens x head_dim, the MN-major form)
@@ -49,29 +49,16 @@ __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sy
 
 // 32 columns of this thread's lane.  The values are there after tm_wait_ld().
 __device__ __forceinline__ void tm_ld32(uint32_t addr, float *r) {
-    uint32_t *u = reinterpret_cast<uint32_t *>(r);
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
-          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
-          "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
-          "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(addr));
 }
-__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t *u) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(u[0]),
-        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
-        "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]),
-        "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]),
-        "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(addr)
-        : "memory");
-}
-
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t *u) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -79,6 +66,21 @@ __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t *u) {
         "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
         "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(addr)
         : "memory");
+}
+
+__device__ __forceinline__ void tm_ld16(uint32_t addr, float *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tm_ld2(uint32_t addr, float *r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=f"(r[0]), "=f"(r[1]) : "r"(addr));
+}
+__device__ __forceinline__ void tm_st2(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%2], {%0, %1};" ::"r"(a), "r"(b), "r"(addr) : "memory");
 }
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -93,6 +95,14 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+// The same for the lanes (rows) whose bits in `off` are clear.
+__device__ __forceinline__ void mma_ts_lanes(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, const uint32_t (&off)[4]) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
         : "memory");
 }
 // Arrives at `bar` once every matrix instruction issued so far is done.
@@ -118,6 +128,29 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    uint32_t u;
+    memcpy(&u, &h, 4);
+    return u;
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -137,7 +170,12 @@ struct Smem {
 };
 
 struct Control {
-    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], s_full[2], p_full[2], o_full[2], q_full, e_full;
+    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], s_full[2], p_full[2][2], o_full[2], q_full, e_full;
+    uint32_t one_part[2][4];   // by stream and quarter of its rows: all ones if this step's p is one bf16 part
+    struct {
+        MultiSpot spot;
+        long long left;
+    } walk[8];                 // of the softmax warps, out of their registers
     int dirty[2];          // number of the item whose drafted tokens have values that are not finite, by its parity
     int failed;
     uint32_t tmem;
@@ -219,7 +257,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&ctl.s_full[i]), 1);
-            mbar_init(smem_addr(&ctl.p_full[i]), kTile);
+            mbar_init(smem_addr(&ctl.p_full[i][0]), kTile);
+            mbar_init(smem_addr(&ctl.p_full[i][1]), kTile);
             mbar_init(smem_addr(&ctl.o_full[i]), 1);
             ctl.dirty[i] = 0;
         }
@@ -248,7 +287,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     MultiItem it;
 
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 8) {
         // ------------------------------------------------------- copies ---
         const int pages = kTile / p.block_size, box_bytes = p.block_size * 128;
@@ -334,16 +373,29 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 for (int j = 0; ok && j < count; ++j) {
                     const int s = j & 1;
                     if ((!both || s == 0) && !(ok = await(ctl, &ctl.v_full[v.slot], v.phase))) break;
-                    if (!(ok = await(ctl, &ctl.p_full[s], steps[s]++ & 1))) break;
-                    tm_fence_after();
                     const uint32_t pt = tmem + s * kTile, o = tmem + 256 + s * kTile;
                     const uint64_t b = smem_desc(smem + M::V + v.slot * M::TILE, M::SLAB);
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                    for (int half = 0; half < 2; ++half) {
+                        if (!(ok = await(ctl, &ctl.p_full[s][half], steps[s] & 1))) break;
+                        tm_fence_after();
+                        uint32_t off[4];
+                        bool two = false;
 #pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            mma_ts(o, pt + part * 64 + kk * 8, b + ((kk * 16 * 128) >> 4), kIdescO,
-                                   j >= 2 || part > 0 || kk > 0);
+                        for (int w = 0; w < 4; ++w) {
+                            off[w] = ctl.one_part[s][w];
+                            two |= off[w] == 0u;
+                        }
+#pragma unroll
+                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                            mma_ts(o, pt + kk * 8, b + ((kk * 16 * 128) >> 4), kIdescO, j >= 2 || kk > 0);
+                        if (two)
+#pragma unroll
+                            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                                mma_ts_lanes(o, pt + 64 + kk * 8, b + ((kk * 16 * 128) >> 4), kIdescO, off);
+                    }
+                    if (!ok) break;
+                    ++steps[s];
                     if (j + 2 >= count) mma_commit(smem_addr(&ctl.o_full[s]));
                     if (!both || s == 1) {
                         mma_commit(smem_addr(&ctl.v_empty[v.slot]));
@@ -355,19 +407,27 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
     }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // ------------------------------------------------------- softmax ---
         const int s = warp >> 2, r = tid & (kTile - 1);   // stream, and row of its tile
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // first lane of this warp's quarter, in bits 16..
         const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + 256 + s * kTile;
         const float scale = fmaxf(fabsf(p.scale_log2), 1.2e-38f);   // the sign goes into Q; zero stays finite on -inf
-        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         uint32_t step = 0, ends = 0;
         int item_no = 0;
-        float2 *const ml = reinterpret_cast<float2 *>(smem_p + M::TILE);   // one tile of rows leaves the second unused
         Ring v;
         bool ok = true;
-        while (ok && Axis::next(p, spot, left, it)) {
+        // 16 bytes c of this thread's row in its stream's tile of Q, where its results are staged too.
+        const auto staged = [&](int row, int c) {
+            return reinterpret_cast<uint4 *>(smem_p + s * M::TILE + (c / 8) * M::SLAB + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+        };
+        while (ok) {
+            if (!Axis::next(p, spot, left, it)) break;
+            __syncwarp();
+            if (lane == 0) {
+                ctl.walk[warp].spot = spot;
+                ctl.walk[warp].left = left;
+            }
             ++item_no;
             const int R0 = it.m * kMultiMmaRows, total = it.s.c * p.group - R0;
             const bool both = total > kTile;
@@ -376,175 +436,196 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const int tok = min(row0 + r, it.s.c * p.group - 1) / p.group;
             const int seen = Axis::seen(p, it.s, it.m), base = it.s.n - it.s.c;
             const int clear = p.see == kSeeAll ? it.s.n : base;   // every row sees every position before
-            {
-                // Q, zero behind the last row: its tile per stream, or half of the one tile.
-                constexpr int C = HD / 8;
-                uint8_t *tile = smem_p + (both ? s * M::TILE : 0);
-                const int first = both ? 0 : s * (kTile / 2), span = both ? kTile : kTile / 2;
-                for (int i = r; i < span * C; i += kTile) {
-                    const int qr = first + i / C, c = i % C;
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (qr < rows) {
-                        x = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
-                                                             multi_row(p, it.s, it.kvh, row0 + qr, HD) + c * 8);
-                        x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-                    }
-                    *reinterpret_cast<uint4 *>(tile + (c / 8) * M::SLAB + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) = x;
+            // Where this row lies in q and out.
+            const long long row_at = multi_row(p, it.s, it.kvh, min(row0 + r, it.s.c * p.group - 1), HD);
+            if (both || s == 0) {
+                // Q, a row per thread, zero behind the last one.
+                const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+                const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + row_at);
+                uint4 x[HD / 8];
+#pragma unroll
+                for (int c = 0; c < HD / 8; ++c) x[c] = r < rows ? q[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int c = 0; c < HD / 8; ++c) {
+                    x[c].x ^= flip, x[c].y ^= flip, x[c].z ^= flip, x[c].w ^= flip;
+                    *staged(r, c) = x[c];
                 }
                 fence_proxy_async_smem();
-                tm_fence_before();
-                mbar_arrive(smem_addr(&ctl.q_full));
             }
+            tm_fence_before();
+            mbar_arrive(smem_addr(&ctl.q_full));
             const bool live = (warp & 3) * 32 < rows;   // this warp has rows
             float ref = -INFINITY, sum = 0.f;
             const int tiles = it.tile1 - it.tile0;
             int mine = 0;   // steps of this stream
-            for (int t = 0; t < tiles; ++t) {
-                const bool take = both || (t & 1) == s;
-                if (take) {
-                    const int u0 = (it.tile0 + t) * kTile;
-                    // First the scores: they were issued behind the products of this stream's tile before, so the
-                    // V ring's barrier is in the phase before the awaited one at least.
-                    if (!(ok = await_warp(ctl, &ctl.s_full[s], step & 1))) break;
-                    tm_fence_after();
-                    if (u0 + kTile > clear || u0 + kTile > seen) {
-                        // Values that some row does not see: what lies behind the last seen token becomes zero, and
-                        // so do values of drafted tokens that are not finite (added again where they are seen).
-                        if (!(ok = await_warp(ctl, &ctl.v_full[v.slot], v.phase))) break;
-                        uint8_t *vt = smem_p + M::V + v.slot * M::TILE;
-                        const int from = max(0, min(kTile, clear - u0));
-                        for (int i = from * (HD / 8) + r; i < kTile * (HD / 8); i += kTile) {
-                            const int j = i / (HD / 8), c = i % (HD / 8);
-                            uint4 *at = reinterpret_cast<uint4 *>(vt + (c / 8) * M::SLAB + j * 128 + (c & 7) * 16);
-                            if (u0 + j >= seen) {
-                                *at = make_uint4(0u, 0u, 0u, 0u);
-                            } else {
-                                uint4 x = *at;
-                                uint32_t *w = &x.x;
-                                bool bad = false;
+            for (int t = 0; t < tiles; ++t, v.advance<M::NV>()) {
+                if (!both && (t & 1) != s) continue;
+                const int u0 = (it.tile0 + t) * kTile;
+                // First the scores: they were issued behind the products of this stream's tile before, so the
+                // V ring's barrier is in the phase before the awaited one at least.
+                if (!(ok = await_warp(ctl, &ctl.s_full[s], step & 1))) break;
+                tm_fence_after();
+                if (u0 + kTile > clear || u0 + kTile > seen) {
+                    // Values that some row does not see: what lies behind the last seen token becomes zero, and
+                    // so do values of drafted tokens that are not finite (added again where they are seen).
+                    if (!(ok = await_warp(ctl, &ctl.v_full[v.slot], v.phase))) break;
+                    uint8_t *vt = smem_p + M::V + v.slot * M::TILE;
+                    const int from = max(0, min(kTile, clear - u0));
+                    for (int i = from * (HD / 8) + r; i < kTile * (HD / 8); i += kTile) {
+                        const int j = i / (HD / 8), c = i % (HD / 8);
+                        uint4 *at = reinterpret_cast<uint4 *>(vt + (c / 8) * M::SLAB + j * 128 + (c & 7) * 16);
+                        if (u0 + j >= seen) {
+                            *at = make_uint4(0u, 0u, 0u, 0u);
+                        } else {
+                            uint4 x = *at;
+                            uint32_t *w = &x.x;
+                            bool bad = false;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if ((w[e] & 0x7f80u) == 0x7f80u) bad = true, w[e] &= 0xffff0000u;
-                                    if ((w[e] & 0x7f800000u) == 0x7f800000u) bad = true, w[e] &= 0xffffu;
-                                }
-                                if (bad) {
-                                    *at = x;
-                                    ctl.dirty[item_no & 1] = item_no;
-                                }
+                            for (int e = 0; e < 4; ++e) {
+                                if ((w[e] & 0x7f80u) == 0x7f80u) bad = true, w[e] &= 0xffff0000u;
+                                if ((w[e] & 0x7f800000u) == 0x7f800000u) bad = true, w[e] &= 0xffffu;
+                            }
+                            if (bad) {
+                                *at = x;
+                                ctl.dirty[item_no & 1] = item_no;
                             }
                         }
-                        fence_proxy_async_smem();
                     }
-                    if (live) {
-                        float x[kTile];
+                    fence_proxy_async_smem();
+                }
+                if (live) {
+                    float x[kTile];
+                    // the second half arrives while the first one's maximum is taken
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) tm_ld32(ts + g * 32, x + g * 32);
-                        tm_wait_ld();
-                        if (u0 + kTile > clear) {
+                    for (int g = 0; g < 2; ++g) tm_ld32(ts + g * 32, x + g * 32);
+                    tm_wait_ld();
 #pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const uint32_t bits = seen_bits(p, it.s, tok, u0 + g * 32);
+                    for (int g = 2; g < 4; ++g) tm_ld32(ts + g * 32, x + g * 32);
+                    const bool masked = u0 + kTile > clear;
+                    const auto hide = [&](int g) {
+                        const uint32_t bits = seen_bits(p, it.s, tok, u0 + g * 32);
 #pragma unroll
-                                for (int c = 0; c < 32; ++c)
-                                    if (!((bits >> c) & 1u)) x[g * 32 + c] = -INFINITY;
-                            }
+                        for (int c = 0; c < 32; ++c)
+                            if (!((bits >> c) & 1u)) x[g * 32 + c] = -INFINITY;
+                    };
+                    if (masked) hide(0), hide(1);
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < kTile / 2; c += 2) top[c / 2 & 3] = fmaxf(top[c / 2 & 3], fmaxf(x[c], x[c + 1]));
+                    tm_wait_ld();
+                    if (masked) hide(2), hide(3);
+#pragma unroll
+                    for (int c = kTile / 2; c < kTile; c += 2)
+                        top[c / 2 & 3] = fmaxf(top[c / 2 & 3], fmaxf(x[c], x[c + 1]));
+                    const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+                    if (mine == 0) {
+                        ref = best;
+                    } else if (__any_sync(kFull, best > ref + 8.f)) {
+                        const float now = fmaxf(ref, best);
+                        const float f = now == ref ? 1.f : ex2(ref - now);
+                        // O holds the products of the step before: these scores were issued behind them, and
+                        // their barrier waits for every matrix instruction issued so far
+#pragma unroll 1
+                        for (int g = 0; g < HD / 16; ++g) {
+                            float o[16];
+                            uint32_t u[16];
+                            tm_ld16(to + g * 16, o);
+                            tm_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(o[c] * f);
+                            tm_st16(to + g * 16, u);
                         }
-                        float top[4] = {x[0], x[1], x[2], x[3]};
+                        sum *= f;
+                        ref = now;
+                    }
+                    const float shift = ref == -INFINITY ? 0.f : -ref;
+                    // One part is enough where no weight of the warp's rows is above 1/32 of its row's sum so far.
+                    const bool two = __any_sync(kFull, r < rows && 31.f * ex2(best + shift) > sum);
+                    if (lane == 0) ctl.one_part[s][warp & 3] = two ? 0u : ~0u;
+                    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                        for (int c = 4; c < kTile; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
-                        const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-                        if (mine == 0) {
-                            ref = best;
-                        } else if (__any_sync(kFull, best > ref + 8.f)) {
-                            const float now = fmaxf(ref, best);
-                            const float f = now == ref ? 1.f : ex2(ref - now);
-                            // O holds the products of the step before: these scores were issued behind them, and
-                            // their barrier waits for every matrix instruction issued so far
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t hi[16];
 #pragma unroll
-                            for (int g = 0; g < HD / 32; ++g) {
-                                float o[32];
-                                tm_ld32(to + g * 32, o);
-                                tm_wait_ld();
-#pragma unroll
-                                for (int c = 0; c < 32; ++c) o[c] *= f;
-                                tm_st32(to + g * 32, reinterpret_cast<uint32_t *>(o));
-                            }
-                            sum *= f;
-                            ref = now;
+                        for (int c = 0; c < 16; ++c) {
+                            float *a = x + g * 32 + 2 * c;
+                            const float2 y = fma2(make_float2(a[0], a[1]), make_float2(scale, scale), make_float2(shift, shift));
+                            a[0] = ex2(y.x);
+                            a[1] = ex2(y.y);
+                            part[c & 1] = add2(part[c & 1], make_float2(a[0], a[1]));
+                            hi[c] = bf16_pair(a[0], a[1]);
                         }
-                        const float shift = ref == -INFINITY ? 0.f : -ref;
-                        float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            uint32_t hi[16], lo[16];
+                        tm_st16(ts + g * 16, hi);
+                        if (two) {
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
-                                const float a = ex2(fmaf(x[g * 32 + 2 * c], scale, shift));
-                                const float b = ex2(fmaf(x[g * 32 + 2 * c + 1], scale, shift));
-                                part[(2 * c) & 3] += a;
-                                part[(2 * c + 1) & 3] += b;
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-                                memcpy(&hi[c], &h, 4);
-                                const __nv_bfloat162 l = __floats2bfloat162_rn(a - __uint_as_float(hi[c] << 16),
-                                                                               b - __uint_as_float(hi[c] & 0xffff0000u));
-                                memcpy(&lo[c], &l, 4);
+                                const float *a = x + g * 32 + 2 * c;
+                                const float2 d = fma2(make_float2(__uint_as_float(hi[c] << 16), __uint_as_float(hi[c] & 0xffff0000u)),
+                                                      make_float2(-1.f, -1.f), make_float2(a[0], a[1]));
+                                hi[c] = bf16_pair(d.x, d.y);
                             }
-                            tm_st16(ts + g * 16, hi);
-                            tm_st16(ts + 64 + g * 16, lo);
+                            tm_st16(ts + 64 + g * 16, hi);
                         }
-                        sum += (part[0] + part[1]) + (part[2] + part[3]);
-                        tm_wait_st();
+                        if (g == 1) {   // the products with the first 64 tokens may begin
+                            tm_wait_st();
+                            tm_fence_before();
+                            __syncwarp();
+                            mbar_arrive(smem_addr(&ctl.p_full[s][0]));
+                        }
                     }
-                    tm_fence_before();
-                    mbar_arrive(smem_addr(&ctl.p_full[s]));
-                    ++step;
-                    ++mine;
+                    const float2 both_parts = add2(part[0], part[1]);
+                    sum += both_parts.x + both_parts.y;
+                    tm_wait_st();
+                } else {
+                    if (lane == 0) ctl.one_part[s][warp & 3] = ~0u;
+                    __syncwarp();
+                    mbar_arrive(smem_addr(&ctl.p_full[s][0]));
                 }
-                v.advance<M::NV>();
+                tm_fence_before();
+                mbar_arrive(smem_addr(&ctl.p_full[s][1]));
+                ++step;
+                ++mine;
             }
             if (!ok) break;
-            // The item's end: all products are in, and both streams say what they have.
+            // The item's end: all products are in, and both streams say what they have (through the free scores).
             if (mine > 0 && !(ok = await_warp(ctl, &ctl.o_full[s], ends++ & 1))) break;
             tm_fence_after();
-            if (!both) ml[s * kTile + r] = make_float2(ref, sum);
+            if (!both) {
+                tm_st2(ts, __float_as_uint(ref), __float_as_uint(sum));
+                tm_wait_st();
+            }
             tm_fence_before();
             mbar_arrive(smem_addr(&ctl.e_full));
             if (!(ok = await_warp(ctl, &ctl.e_full, (item_no - 1) & 1))) break;
             tm_fence_after();
             if (live) {
                 const bool dirty = ctl.dirty[item_no & 1] == item_no;
-                float f[2], top = ref, all = sum;
-                if (both) {
-                    f[0] = f[1] = 1.f;
-                } else {
-                    const float2 a = ml[r], b = ml[kTile + r];
-                    top = fmaxf(a.x, b.x);
-                    const float at = top == -INFINITY ? 0.f : top;
-                    f[0] = ex2(a.x - at);
-                    f[1] = ex2(b.x - at);
-                    all = f[0] * a.y + f[1] * b.y;
-                }
-                const bool second = !both && tiles > 1;
-                const float inv = all == 0.f ? 0.f : 1.f / all;
-                const bool whole = it.whole();
-                const long long at = static_cast<long long>(it.slot(blockIdx.x)) * p.slot_rows + (both ? s * kTile : 0) + r;
-                // one tile: each stream's threads write half of the columns
-                const int g0 = both ? 0 : s * (HD / 64), g1 = both ? HD / 32 : g0 + HD / 64;
-                for (int g = g0; g < g1; ++g) {
-                    float o[32];
-                    tm_ld32((both ? to : tmem + lanes + 256) + g * 32, o);
+                float f[2] = {1.f, 1.f}, top = ref, all = sum;
+                if (!both) {
+                    float a[4];
+                    tm_ld2(tmem + lanes, a);
+                    tm_ld2(tmem + lanes + kTile, a + 2);
                     tm_wait_ld();
-                    if (!both) {
+                    top = fmaxf(a[0], a[2]);
+                    const float at = top == -INFINITY ? 0.f : top;
+                    f[0] = ex2(a[0] - at);
+                    f[1] = ex2(a[2] - at);
+                    all = f[0] * a[1] + f[1] * a[3];
+                }
+                const bool second = !both && tiles > 1, whole = it.whole();
+                if (whole) {
+                    const float inv = all == 0.f ? 0.f : 1.f / all;
+                    f[0] *= inv;
+                    f[1] *= inv;
+                }
+                // 16 columns of the row's result, ready to be written.
+                const auto result = [&](int g, float *o) {
+                    tm_ld16((both ? to : tmem + lanes + 256) + g * 16, o);
+                    float o1[16];
+                    if (second) tm_ld16(tmem + lanes + 256 + kTile + g * 16, o1);
+                    tm_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] *= f[0];
-                    }
-                    if (second) {
-                        float o1[32];
-                        tm_ld32(tmem + lanes + 256 + kTile + g * 32, o1);
-                        tm_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] = fmaf(o1[c], f[1], o[c]);
-                    }
+                    for (int c = 0; c < 16; ++c) o[c] = second ? fmaf(o1[c], f[1], o[c] * f[0]) : o[c] * f[0];
                     if (dirty && r < rows)
                         for (int u = max(max(base, 0), it.tile0 * kTile); u < min(seen, it.tile1 * kTile); ++u) {
                             if (!(seen_bits(p, it.s, tok, u) & 1u)) continue;
@@ -553,35 +634,61 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                             const __nv_bfloat16 *vr =
                                 static_cast<const __nv_bfloat16 *>(p.v_cache) +
                                 ((static_cast<long long>(b) * p.num_kv_heads + it.kvh) * p.block_size + u % p.block_size) * HD;
-                            for (int c = 0; c < 32; ++c) {
-                                const float x = __bfloat162float(vr[g * 32 + c]);
-                                if (!isfinite(x)) o[c] += x;
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                const float y = __bfloat162float(vr[g * 16 + c]);
+                                if (!isfinite(y)) o[c] += y;
                             }
                         }
-                    if (r < rows && whole) {
-                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) +
-                                             multi_row(p, it.s, it.kvh, row0 + r, HD) + g * 32;
-#pragma unroll
-                        for (int c = 0; c < 32; c += 8) {
-                            uint4 x;
-                            uint32_t *w = &x.x;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const __nv_bfloat162 h =
-                                    __floats2bfloat162_rn(o[c + 2 * e] * inv, o[c + 2 * e + 1] * inv);
-                                memcpy(&w[e], &h, 4);
-                            }
-                            *reinterpret_cast<uint4 *>(out + c) = x;
-                        }
-                    } else if (r < rows) {
-#pragma unroll
-                        for (int c = 0; c < 32; c += 4)
-                            store4(p.part_acc + at * HD + g * 32 + c, make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]));
+                };
+                // Rows go through the warp's own rows of its Q tile, so that they are written to memory in full lines.
+                const int g0 = both ? 0 : s * (HD / 32), g1 = both ? HD / 16 : g0 + HD / 32;
+                const auto flush = [&](char *dst, long long at, int chunks) {
+                    __syncwarp();
+                    const int per = 32 / chunks;   // rows per turn
+                    for (int k = 0; k < 32; k += per) {
+                        const int row = k + lane / chunks;
+                        const long long to_row = __shfl_sync(kFull, at, row);
+                        if ((warp & 3) * 32 + row < rows)
+                            *reinterpret_cast<uint4 *>(dst + to_row + (lane % chunks) * 16) =
+                                *staged((warp & 3) * 32 + row, lane % chunks);
                     }
+                    __syncwarp();
+                };
+                if (whole) {
+#pragma unroll 1
+                    for (int g = g0; g < g1; ++g) {
+                        float o[16];
+                        result(g, o);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            *staged(r, (g - g0) * 2 + c) =
+                                make_uint4(bf16_pair(o[8 * c], o[8 * c + 1]), bf16_pair(o[8 * c + 2], o[8 * c + 3]),
+                                           bf16_pair(o[8 * c + 4], o[8 * c + 5]), bf16_pair(o[8 * c + 6], o[8 * c + 7]));
+                    }
+                    flush(static_cast<char *>(p.out) + g0 * 32, row_at * 2, (g1 - g0) * 2);
+                } else {
+                    const long long at = static_cast<long long>(it.slot(blockIdx.x)) * p.slot_rows + (both ? s * kTile : 0) + r;
+#pragma unroll 1
+                    for (int h = g0; h < g1; h += HD / 32) {   // as many columns as a staged row holds
+#pragma unroll 1
+                        for (int g = h; g < h + HD / 32; ++g) {
+                            float o[16];
+                            result(g, o);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                store4(reinterpret_cast<float *>(staged(r, (g - h) * 4 + c)),
+                                       make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
+                        }
+                        flush(reinterpret_cast<char *>(p.part_acc) + h * 64, at * HD * 4, HD / 8);
+                    }
+                    if (r < rows && (both || s == 0))
+                        *reinterpret_cast<float2 *>(p.part_ml + 2 * at) = make_float2(top, all);
                 }
-                if (!whole && r < rows && (both || s == 0))
-                    *reinterpret_cast<float2 *>(p.part_ml + 2 * at) = make_float2(top, all);
             }
+            __syncwarp();
+            spot = ctl.walk[warp].spot;
+            left = ctl.walk[warp].left;
         }
     }
 
