@@ -98,16 +98,22 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 // The same for the lanes (rows) whose bits in `off` are clear.
-__device__ __forceinline__ void mma_ts_lanes(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, const uint32_t (&off)[4]) {
+__device__ __forceinline__ void mma_ts_lanes(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, const uint4 &off) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
+        "r"(a), "l"(b), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w)
         : "memory");
 }
 // Arrives at `bar` once every matrix instruction issued so far is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
 }
 
 // Shared-memory operand in 128-byte swizzled rows; 8-row groups follow each other.
@@ -171,7 +177,7 @@ struct Smem {
 
 struct Control {
     uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], s_full[2], p_full[2][2], o_full[2], q_full, e_full;
-    uint32_t one_part[2][4];   // by stream and quarter of its rows: all ones if this step's p is one bf16 part
+    alignas(16) uint32_t one_part[2][4];   // by stream and quarter of its rows: all ones if this step's p is one bf16 part
     struct {
         MultiSpot spot;
         long long left;
@@ -343,49 +349,49 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
     } else if (warp == 9) {
         // --------------------------------------------- matrix instructions ---
-        if (lane == 0) {
-            Ring k, v;
-            uint32_t items = 0, steps[2] = {0, 0};
-            bool ok = true;
-            while (ok && Axis::next(p, spot, left, it)) {
-                const bool both = it.s.c * p.group - it.m * kMultiMmaRows > kTile;
-                const int tiles = it.tile1 - it.tile0, count = both ? 2 * tiles : tiles;
-                if (!(ok = await(ctl, &ctl.q_full, items++ & 1))) break;
-                tm_fence_after();
-                const auto scores = [&](int j) {
-                    const int s = j & 1;
-                    if ((!both || s == 0) && !await(ctl, &ctl.k_full[k.slot], k.phase)) return false;
-                    const uint64_t a = smem_desc(smem + (both ? s * M::TILE : 0), 16);
-                    const uint64_t b = smem_desc(smem + M::K + k.slot * M::TILE, 16);
+        // The whole warp walks, on values that the compiler can see to be the same in all lanes (operands of the
+        // matrix instruction live in uniform registers: moving them there one by one takes longer than the
+        // instruction itself), and one lane issues.
+        const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+        Ring k, v;
+        uint32_t items = 0, steps[2] = {0, 0};
+        bool ok = true;
+        while (ok && Axis::next(p, spot, left, it)) {
+            const bool both = __shfl_sync(kFull, it.s.c * p.group - it.m * kMultiMmaRows > kTile, 0);
+            const int tiles = __shfl_sync(kFull, it.tile1 - it.tile0, 0), count = both ? 2 * tiles : tiles;
+            if (!(ok = await_warp(ctl, &ctl.q_full, items++ & 1))) break;
+            tm_fence_after();
+            const auto scores = [&](int j) {
+                const int s = j & 1;
+                if ((!both || s == 0) && !await_warp(ctl, &ctl.k_full[k.slot], k.phase)) return false;
+                const uint64_t a = smem_desc(smem + (both ? s * M::TILE : 0), 16);
+                const uint64_t b = smem_desc(smem + M::K + k.slot * M::TILE, 16);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < HD / 16; ++kk) {
                         const uint32_t at = ((kk / 4) * M::SLAB + (kk % 4) * 32) >> 4;
-                        mma_ss(tmem + s * kTile, a + at, b + at, kIdescS, kk > 0);
+                        mma_ss(tm + s * kTile, a + at, b + at, kIdescS, kk > 0);
                     }
                     mma_commit(smem_addr(&ctl.s_full[s]));
-                    if (!both || s == 1) {
-                        mma_commit(smem_addr(&ctl.k_empty[k.slot]));
-                        k.advance<M::NK>();
-                    }
-                    return true;
-                };
-                ok = scores(0) && (count < 2 || scores(1));
-                for (int j = 0; ok && j < count; ++j) {
-                    const int s = j & 1;
-                    if ((!both || s == 0) && !(ok = await(ctl, &ctl.v_full[v.slot], v.phase))) break;
-                    const uint32_t pt = tmem + s * kTile, o = tmem + 256 + s * kTile;
-                    const uint64_t b = smem_desc(smem + M::V + v.slot * M::TILE, M::SLAB);
+                    if (!both || s == 1) mma_commit(smem_addr(&ctl.k_empty[k.slot]));
+                }
+                __syncwarp();
+                if (!both || s == 1) k.advance<M::NK>();
+                return true;
+            };
+            ok = scores(0) && (count < 2 || scores(1));
+            for (int j = 0; ok && j < count; ++j) {
+                const int s = j & 1;
+                if ((!both || s == 0) && !(ok = await_warp(ctl, &ctl.v_full[v.slot], v.phase))) break;
+                const uint32_t pt = tm + s * kTile, o = tm + 256 + s * kTile;
+                const uint64_t b = smem_desc(smem + M::V + v.slot * M::TILE, M::SLAB);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (!(ok = await(ctl, &ctl.p_full[s][half], steps[s] & 1))) break;
-                        tm_fence_after();
-                        uint32_t off[4];
-                        bool two = false;
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            off[w] = ctl.one_part[s][w];
-                            two |= off[w] == 0u;
-                        }
+                for (int half = 0; half < 2; ++half) {
+                    if (!(ok = await_warp(ctl, &ctl.p_full[s][half], steps[s] & 1))) break;
+                    tm_fence_after();
+                    const uint4 off = *reinterpret_cast<const uint4 *>(ctl.one_part[s]);
+                    const bool two = __any_sync(kFull, (off.x & off.y & off.z & off.w) == 0u);
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
                             mma_ts(o, pt + kk * 8, b + ((kk * 16 * 128) >> 4), kIdescO, j >= 2 || kk > 0);
@@ -394,15 +400,17 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                             for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
                                 mma_ts_lanes(o, pt + 64 + kk * 8, b + ((kk * 16 * 128) >> 4), kIdescO, off);
                     }
-                    if (!ok) break;
-                    ++steps[s];
-                    if (j + 2 >= count) mma_commit(smem_addr(&ctl.o_full[s]));
-                    if (!both || s == 1) {
-                        mma_commit(smem_addr(&ctl.v_empty[v.slot]));
-                        v.advance<M::NV>();
-                    }
-                    if (j + 2 < count) ok = scores(j + 2);
+                    __syncwarp();
                 }
+                if (!ok) break;
+                ++steps[s];
+                if (elect_one()) {
+                    if (j + 2 >= count) mma_commit(smem_addr(&ctl.o_full[s]));
+                    if (!both || s == 1) mma_commit(smem_addr(&ctl.v_empty[v.slot]));
+                }
+                __syncwarp();
+                if (!both || s == 1) v.advance<M::NV>();
+                if (j + 2 < count) ok = scores(j + 2);
             }
         }
     }
