@@ -83,39 +83,47 @@ __device__ __forceinline__ void tm_st2(uint32_t addr, uint32_t a, uint32_t b) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%2], {%0, %1};" ::"r"(a), "r"(b), "r"(addr) : "memory");
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// One lane of the warp, always the same: its mask as the operand `lead` below.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes;
+}
+
+// Matrix instructions, executed by the whole warp and issued by its leading lane: a branch around them would take
+// their operands out of the uniform registers that the instruction reads, and moving them back there takes longer
+// than the instruction.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(lead)
         : "memory");
 }
 // The same for the lanes (rows) whose bits in `off` are clear.
-__device__ __forceinline__ void mma_ts_lanes(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, const uint4 &off) {
+__device__ __forceinline__ void mma_ts_lanes(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, const uint4 &off,
+                                             uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w)
+        "{\n\t.reg .pred p, l;\n\tsetp.eq.b32 p, 0, 0;\n\tsetp.ne.b32 l, %8, 0;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w), "r"(lead)
         : "memory");
 }
 // Arrives at `bar` once every matrix instruction issued so far is done.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %1, 0;\n\t"
+        "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(lead)
+        : "memory");
 }
-
-__device__ __forceinline__ bool elect_one() {
-    uint32_t yes;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
-    return yes != 0;
-}
-
 // Shared-memory operand in 128-byte swizzled rows; 8-row groups follow each other.
 // K-major (Q, K): the row is along head_dim.  MN-major (V): the row is along
 // head_dim too, but that is N, so the next 64 columns are `next` bytes away.
@@ -202,12 +210,11 @@ struct Ring {
 
 // Waits give up after about two seconds, or when another role has; every role
 // then leaves its loop.
-__device__ __forceinline__ bool await(Control &c, uint64_t *bar, uint32_t parity) {
-    const uint32_t b = smem_addr(bar);
-    if (mbar_try_wait(b, parity)) return true;
+__device__ __forceinline__ bool await_slow(Control &c, uint32_t bar, uint32_t parity) {
     const uint64_t start = global_timer_ns();
+#pragma unroll 1
     for (uint32_t spin = 1;; ++spin) {
-        if (mbar_try_wait(b, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if ((spin & 63u) == 0) {
             if (*static_cast<volatile int *>(&c.failed)) return false;
             if (global_timer_ns() - start > kWaitLimitNs) {
@@ -218,9 +225,11 @@ __device__ __forceinline__ bool await(Control &c, uint64_t *bar, uint32_t parity
     }
 }
 
-// The same for a whole warp: all lanes go on, or none.
+// For a whole warp: all lanes go on, or none.
 __device__ __forceinline__ bool await_warp(Control &c, uint64_t *bar, uint32_t parity) {
-    return __all_sync(kFull, await(c, bar, parity));
+    const uint32_t b = smem_addr(bar);
+    if (__all_sync(kFull, mbar_try_wait(b, parity))) return true;
+    return __all_sync(kFull, await_slow(c, b, parity));
 }
 
 // Which of the 32 positions from u on a row sees, as bits.
@@ -349,10 +358,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
     } else if (warp == 9) {
         // --------------------------------------------- matrix instructions ---
-        // The whole warp walks, on values that the compiler can see to be the same in all lanes (operands of the
-        // matrix instruction live in uniform registers: moving them there one by one takes longer than the
-        // instruction itself), and one lane issues.
-        const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+        // The whole warp walks, on values that the compiler can see to be the same in all lanes.
+        const uint32_t tm = __shfl_sync(kFull, tmem, 0), lead = elect_one();
         Ring k, v;
         uint32_t items = 0, steps[2] = {0, 0};
         bool ok = true;
@@ -361,22 +368,22 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const int tiles = __shfl_sync(kFull, it.tile1 - it.tile0, 0), count = both ? 2 * tiles : tiles;
             if (!(ok = await_warp(ctl, &ctl.q_full, items++ & 1))) break;
             tm_fence_after();
+            // The loops are kept short: this warp's instructions come through the same cache as the softmax's many.
             const auto scores = [&](int j) {
                 const int s = j & 1;
                 if ((!both || s == 0) && !await_warp(ctl, &ctl.k_full[k.slot], k.phase)) return false;
-                const uint64_t a = smem_desc(smem + (both ? s * M::TILE : 0), 16);
-                const uint64_t b = smem_desc(smem + M::K + k.slot * M::TILE, 16);
-                if (elect_one()) {
+                uint64_t a = smem_desc(smem + (both ? s * M::TILE : 0), 16);
+                uint64_t b = smem_desc(smem + M::K + k.slot * M::TILE, 16);
+#pragma unroll 1
+                for (int slab = 0; slab < HD / 64; ++slab, a += M::SLAB >> 4, b += M::SLAB >> 4)
 #pragma unroll
-                    for (int kk = 0; kk < HD / 16; ++kk) {
-                        const uint32_t at = ((kk / 4) * M::SLAB + (kk % 4) * 32) >> 4;
-                        mma_ss(tm + s * kTile, a + at, b + at, kIdescS, kk > 0);
-                    }
-                    mma_commit(smem_addr(&ctl.s_full[s]));
-                    if (!both || s == 1) mma_commit(smem_addr(&ctl.k_empty[k.slot]));
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss(tm + s * kTile, a + 2 * kk, b + 2 * kk, kIdescS, slab + kk > 0, lead);
+                mma_commit(smem_addr(&ctl.s_full[s]), lead);
+                if (!both || s == 1) {
+                    mma_commit(smem_addr(&ctl.k_empty[k.slot]), lead);
+                    k.advance<M::NK>();
                 }
-                __syncwarp();
-                if (!both || s == 1) k.advance<M::NK>();
                 return true;
             };
             ok = scores(0) && (count < 2 || scores(1));
@@ -385,30 +392,26 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 if ((!both || s == 0) && !(ok = await_warp(ctl, &ctl.v_full[v.slot], v.phase))) break;
                 const uint32_t pt = tm + s * kTile, o = tm + 256 + s * kTile;
                 const uint64_t b = smem_desc(smem + M::V + v.slot * M::TILE, M::SLAB);
-#pragma unroll
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     if (!(ok = await_warp(ctl, &ctl.p_full[s][half], steps[s] & 1))) break;
                     tm_fence_after();
                     const uint4 off = *reinterpret_cast<const uint4 *>(ctl.one_part[s]);
                     const bool two = __any_sync(kFull, (off.x & off.y & off.z & off.w) == 0u);
-                    if (elect_one()) {
+                    const uint64_t vb = b + half * (4 * 16 * 128 >> 4);
+                    const uint32_t pa = pt + half * 32;
 #pragma unroll
-                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                            mma_ts(o, pt + kk * 8, b + ((kk * 16 * 128) >> 4), kIdescO, j >= 2 || kk > 0);
-                        if (two)
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts(o, pa + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, j >= 2 || half + kk > 0, lead);
+                    if (two)
 #pragma unroll
-                            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                                mma_ts_lanes(o, pt + 64 + kk * 8, b + ((kk * 16 * 128) >> 4), kIdescO, off);
-                    }
-                    __syncwarp();
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ts_lanes(o, pa + 64 + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, off, lead);
                 }
                 if (!ok) break;
                 ++steps[s];
-                if (elect_one()) {
-                    if (j + 2 >= count) mma_commit(smem_addr(&ctl.o_full[s]));
-                    if (!both || s == 1) mma_commit(smem_addr(&ctl.v_empty[v.slot]));
-                }
-                __syncwarp();
+                if (j + 2 >= count) mma_commit(smem_addr(&ctl.o_full[s]), lead);
+                if (!both || s == 1) mma_commit(smem_addr(&ctl.v_empty[v.slot]), lead);
                 if (!both || s == 1) v.advance<M::NV>();
                 if (j + 2 < count) ok = scores(j + 2);
             }
