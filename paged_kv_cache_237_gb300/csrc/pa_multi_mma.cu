@@ -232,6 +232,18 @@ __device__ __forceinline__ bool await_warp(Control &c, uint64_t *bar, uint32_t p
     return __all_sync(kFull, await_slow(c, b, parity));
 }
 
+// For a warp and two barriers, the second only if it is needed.  A wait costs about
+// 100 cycles even when there is nothing to wait for.  (All lanes look at the same.)
+__device__ __forceinline__ bool await_two(Control &c, uint64_t *first, uint32_t parity_a, uint64_t *second,
+                                          uint32_t parity_b, bool need_b) {
+    const uint32_t a = smem_addr(first), b = smem_addr(second);
+    const bool there_a = mbar_try_wait(a, parity_a);
+    const bool there_b = !need_b || mbar_try_wait(b, parity_b);
+    if (__all_sync(kFull, there_a && there_b)) return true;
+    const bool ok = await_slow(c, a, parity_a) && (!need_b || await_slow(c, b, parity_b));
+    return __all_sync(kFull, ok);
+}
+
 // Which of the 32 positions from u on a row sees, as bits.
 __device__ __forceinline__ uint32_t seen_bits(const MultiParams &p, const MultiSeq &s, int tok, int u) {
     const auto below = [](int count) { return count <= 0 ? 0u : (count >= 32 ? ~0u : (1u << count) - 1u); };
@@ -272,13 +284,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&ctl.s_full[i]), 1);
-            mbar_init(smem_addr(&ctl.p_full[i][0]), kTile);
-            mbar_init(smem_addr(&ctl.p_full[i][1]), kTile);
+            mbar_init(smem_addr(&ctl.p_full[i][0]), 4);
+            mbar_init(smem_addr(&ctl.p_full[i][1]), 4);
             mbar_init(smem_addr(&ctl.o_full[i]), 1);
             ctl.dirty[i] = 0;
         }
-        mbar_init(smem_addr(&ctl.q_full), 2 * kTile);
-        mbar_init(smem_addr(&ctl.e_full), 2 * kTile);
+        mbar_init(smem_addr(&ctl.q_full), 8);
+        mbar_init(smem_addr(&ctl.e_full), 8);
         ctl.failed = 0;
         fence_mbar_init();
         prefetch_tensormap(&tmK);
@@ -361,59 +373,65 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         // The whole warp walks, on values that the compiler can see to be the same in all lanes.
         const uint32_t tm = __shfl_sync(kFull, tmem, 0), lead = elect_one();
         Ring k, v;
-        uint32_t items = 0, steps[2] = {0, 0};
+        uint32_t items = 0, used = 0;   // used: the streams' phases of p_full, a bit each
         bool ok = true;
         while (ok && Axis::next(p, spot, left, it)) {
             const bool both = __shfl_sync(kFull, it.s.c * p.group - it.m * kMultiMmaRows > kTile, 0);
             const int tiles = __shfl_sync(kFull, it.tile1 - it.tile0, 0), count = both ? 2 * tiles : tiles;
             if (!(ok = await_warp(ctl, &ctl.q_full, items++ & 1))) break;
             tm_fence_after();
-            // The loops are kept short: this warp's instructions come through the same cache as the softmax's many.
-            const auto scores = [&](int j) {
-                const int s = j & 1;
-                if ((!both || s == 0) && !await_warp(ctl, &ctl.k_full[k.slot], k.phase)) return false;
-                uint64_t a = smem_desc(smem + (both ? s * M::TILE : 0), 16);
-                uint64_t b = smem_desc(smem + M::K + k.slot * M::TILE, 16);
+            // Products of step q, then scores of step q + 2.  The loops are kept short: this warp's instructions come
+            // through the same cache as the softmax's many.
 #pragma unroll 1
-                for (int slab = 0; slab < HD / 64; ++slab, a += M::SLAB >> 4, b += M::SLAB >> 4)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(tm + s * kTile, a + 2 * kk, b + 2 * kk, kIdescS, slab + kk > 0, lead);
-                mma_commit(smem_addr(&ctl.s_full[s]), lead);
-                if (!both || s == 1) {
-                    mma_commit(smem_addr(&ctl.k_empty[k.slot]), lead);
-                    k.advance<M::NK>();
-                }
-                return true;
-            };
-            ok = scores(0) && (count < 2 || scores(1));
-            for (int j = 0; ok && j < count; ++j) {
-                const int s = j & 1;
-                if ((!both || s == 0) && !(ok = await_warp(ctl, &ctl.v_full[v.slot], v.phase))) break;
-                const uint32_t pt = tm + s * kTile, o = tm + 256 + s * kTile;
-                const uint64_t b = smem_desc(smem + M::V + v.slot * M::TILE, M::SLAB);
+            for (int q = -2; q < count; ++q) {
+                const int s = q & 1;
+                const bool more = q + 2 < count, last = !both || s == 1;
+                if (q >= 0) {
+                    const uint32_t pt = tm + s * kTile, o = tm + 256 + s * kTile;
+                    const uint64_t b = smem_desc(smem + M::V + v.slot * M::TILE, M::SLAB);
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    if (!(ok = await_warp(ctl, &ctl.p_full[s][half], steps[s] & 1))) break;
-                    tm_fence_after();
-                    const uint4 off = *reinterpret_cast<const uint4 *>(ctl.one_part[s]);
-                    const bool two = __any_sync(kFull, (off.x & off.y & off.z & off.w) == 0u);
-                    const uint64_t vb = b + half * (4 * 16 * 128 >> 4);
-                    const uint32_t pa = pt + half * 32;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(o, pa + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, j >= 2 || half + kk > 0, lead);
-                    if (two)
+                    for (int half = 0; half < 2; ++half) {
+                        // beside the weights: V for the first half, the next scores' K for the second
+                        if (!(ok = await_two(ctl, &ctl.p_full[s][half], (used >> s) & 1u,
+                                             half == 0 ? &ctl.v_full[v.slot] : &ctl.k_full[k.slot],
+                                             half == 0 ? v.phase : k.phase, half == 0 || more)))
+                            break;
+                        tm_fence_after();
+                        const uint4 off = *reinterpret_cast<const uint4 *>(ctl.one_part[s]);
+                        const uint64_t vb = b + half * (4 * 16 * 128 >> 4);
+                        const uint32_t pa = pt + half * 32;
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_ts_lanes(o, pa + 64 + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, off, lead);
+                            mma_ts(o, pa + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, q >= 2 || half + kk > 0, lead);
+                        if (__any_sync(kFull, (off.x & off.y & off.z & off.w) == 0u))
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ts_lanes(o, pa + 64 + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, off, lead);
+                    }
+                    if (!ok) break;
+                    used ^= 1u << s;
+                    if (!more) mma_commit(smem_addr(&ctl.o_full[s]), lead);
+                    if (last) {
+                        mma_commit(smem_addr(&ctl.v_empty[v.slot]), lead);
+                        v.advance<M::NV>();
+                    }
+                } else if (more && !(ok = await_warp(ctl, &ctl.k_full[k.slot], k.phase))) {
+                    break;
                 }
-                if (!ok) break;
-                ++steps[s];
-                if (j + 2 >= count) mma_commit(smem_addr(&ctl.o_full[s]), lead);
-                if (!both || s == 1) mma_commit(smem_addr(&ctl.v_empty[v.slot]), lead);
-                if (!both || s == 1) v.advance<M::NV>();
-                if (j + 2 < count) ok = scores(j + 2);
+                if (more) {
+                    uint64_t a = smem_desc(smem + (both ? s * M::TILE : 0), 16);
+                    uint64_t b = smem_desc(smem + M::K + k.slot * M::TILE, 16);
+#pragma unroll 1
+                    for (int slab = 0; slab < HD / 64; ++slab, a += M::SLAB >> 4, b += M::SLAB >> 4)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ss(tm + s * kTile, a + 2 * kk, b + 2 * kk, kIdescS, slab + kk > 0, lead);
+                    mma_commit(smem_addr(&ctl.s_full[s]), lead);
+                    if (last) {
+                        mma_commit(smem_addr(&ctl.k_empty[k.slot]), lead);
+                        k.advance<M::NK>();
+                    }
+                }
             }
         }
     }
@@ -431,6 +449,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         // 16 bytes c of this thread's row in its stream's tile of Q, where its results are staged too.
         const auto staged = [&](int row, int c) {
             return reinterpret_cast<uint4 *>(smem_p + s * M::TILE + (c / 8) * M::SLAB + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+        };
+        const auto arrive = [&](uint64_t *bar) {
+            tm_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(bar));
         };
         while (ok) {
             if (!Axis::next(p, spot, left, it)) break;
@@ -463,8 +486,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 }
                 fence_proxy_async_smem();
             }
-            tm_fence_before();
-            mbar_arrive(smem_addr(&ctl.q_full));
+            arrive(&ctl.q_full);
             const bool live = (warp & 3) * 32 < rows;   // this warp has rows
             float ref = -INFINITY, sum = 0.f;
             const int tiles = it.tile1 - it.tile0;
@@ -522,12 +544,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     if (masked) hide(0), hide(1);
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < kTile / 2; c += 2) top[c / 2 & 3] = fmaxf(top[c / 2 & 3], fmaxf(x[c], x[c + 1]));
+                    for (int c = 0; c < kTile / 2; c += 2) top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], x[c]), x[c + 1]);
                     tm_wait_ld();
                     if (masked) hide(2), hide(3);
 #pragma unroll
                     for (int c = kTile / 2; c < kTile; c += 2)
-                        top[c / 2 & 3] = fmaxf(top[c / 2 & 3], fmaxf(x[c], x[c + 1]));
+                        top[c / 2 & 3] = fmaxf(fmaxf(top[c / 2 & 3], x[c]), x[c + 1]);
                     const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
                     if (mine == 0) {
                         ref = best;
@@ -579,9 +601,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         }
                         if (g == 1) {   // the products with the first 64 tokens may begin
                             tm_wait_st();
-                            tm_fence_before();
-                            __syncwarp();
-                            mbar_arrive(smem_addr(&ctl.p_full[s][0]));
+                            arrive(&ctl.p_full[s][0]);
                         }
                     }
                     const float2 both_parts = add2(part[0], part[1]);
@@ -589,11 +609,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     tm_wait_st();
                 } else {
                     if (lane == 0) ctl.one_part[s][warp & 3] = ~0u;
-                    __syncwarp();
-                    mbar_arrive(smem_addr(&ctl.p_full[s][0]));
+                    arrive(&ctl.p_full[s][0]);
                 }
-                tm_fence_before();
-                mbar_arrive(smem_addr(&ctl.p_full[s][1]));
+                arrive(&ctl.p_full[s][1]);
                 ++step;
                 ++mine;
             }
@@ -605,8 +623,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 tm_st2(ts, __float_as_uint(ref), __float_as_uint(sum));
                 tm_wait_st();
             }
-            tm_fence_before();
-            mbar_arrive(smem_addr(&ctl.e_full));
+            arrive(&ctl.e_full);
             if (!(ok = await_warp(ctl, &ctl.e_full, (item_no - 1) & 1))) break;
             tm_fence_after();
             if (live) {
