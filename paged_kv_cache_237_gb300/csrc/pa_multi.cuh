@@ -4,8 +4,9 @@
 //
 // Work.  A sequence's c queries times the `group` query heads of one KV head
 // are rows R = token * group + head of that head's problem; an item is up to
-// ROWS of them, and costs one unit per KT tokens of the cache that any of its
-// rows sees, plus START units for its beginning and end.  All items of the
+// ROWS of them, and costs units for each KT tokens of the cache that any of its
+// rows sees (three, or two if it has at most HALF rows; one where HALF = ROWS),
+// and START units for its beginning and end.  All items of the
 // batch lie end to end on one axis of units (sequence, KV head, row block), and
 // each CTA takes an equal stretch of it, whatever the lengths.  A CTA whose
 // stretch holds an item whole writes its rows; where a stretch ends inside an
@@ -70,9 +71,9 @@ struct MultiItem {
 };
 
 // The axis for items of ROWS rows and units of KT tokens.
-template <int ROWS_, int KT, int START>
+template <int ROWS_, int HALF, int KT, int START>
 struct MultiAxis {
-    static constexpr int ROWS = ROWS_, kStart = START;
+    static constexpr int ROWS = ROWS_;
 
     static __device__ __forceinline__ int row_blocks(const MultiParams &p, const MultiSeq &s) {
         return (s.c * p.group + ROWS - 1) / ROWS;
@@ -91,14 +92,28 @@ struct MultiAxis {
         return t > 0 ? t : 1;
     }
 
+    // Units of one tile.
+    static __device__ __forceinline__ int cost(const MultiParams &p, const MultiSeq &s, int m) {
+        return HALF < ROWS ? (s.c * p.group - m * ROWS > HALF ? 3 : 2) : 1;
+    }
+
     static __device__ __forceinline__ int units(const MultiParams &p, const MultiSeq &s, int m) {
-        return tiles(p, s, m) + START;
+        return tiles(p, s, m) * cost(p, s, m) + START;
+    }
+
+    // Tiles that lie before unit `at` of an item: where a stretch that begins or ends there cuts it.
+    static __device__ __forceinline__ int tiles_before(const MultiParams &p, const MultiSeq &s, int m, int at) {
+        if (at <= START) return 0;
+        const unsigned u = at - START;
+        return HALF < ROWS ? (cost(p, s, m) == 3 ? u / 3u : u / 2u) : u;
     }
 
     // Units of one KV head of a sequence.
     static __device__ __forceinline__ long long head_units(const MultiParams &p, const MultiSeq &s) {
         const int blocks = row_blocks(p, s);
-        if (p.see != kSeeChain || s.n == 0) return static_cast<long long>(blocks) * units(p, s, 0);
+        if (blocks == 0) return 0;
+        if (p.see != kSeeChain || s.n == 0)
+            return static_cast<long long>(blocks - 1) * units(p, s, 0) + units(p, s, blocks - 1);
         long long u = 0;
         for (int m = 0; m < blocks; ++m) u += units(p, s, m);
         return u;
@@ -107,9 +122,10 @@ struct MultiAxis {
     // The next item of a walk from `spot` over `left` units; false at its end.
     static __device__ __forceinline__ bool next(const MultiParams &p, MultiSpot &spot, long long &left, MultiItem &it) {
         while (left > 0) {
-            const int count = tiles(p, spot.s, spot.m), all = count + START;
+            const int all = units(p, spot.s, spot.m);
             const int end = static_cast<int>(spot.at + left < all ? spot.at + left : all);
-            it = MultiItem{spot.seq, spot.kvh, spot.m, max(0, spot.at - START), max(0, end - START), count, spot.s};
+            it = MultiItem{spot.seq, spot.kvh, spot.m, tiles_before(p, spot.s, spot.m, spot.at),
+                           tiles_before(p, spot.s, spot.m, end), tiles(p, spot.s, spot.m), spot.s};
             left -= end - spot.at;
             spot.at = 0;
             if (++spot.m >= row_blocks(p, spot.s)) {
@@ -177,7 +193,8 @@ struct MultiLocator {
                 rest -= head * p.num_kv_heads;
                 continue;
             }
-            const int kvh = static_cast<int>(rest / head);
+            const int kvh = rest >> 32 || head >> 32 ? static_cast<int>(rest / head)
+                                                     : static_cast<int>(static_cast<unsigned>(rest) / static_cast<unsigned>(head));
             rest -= kvh * head;
             int m = 0;
             while (rest >= Axis::units(p, s, m)) rest -= Axis::units(p, s, m++);
@@ -187,11 +204,24 @@ struct MultiLocator {
     }
 };
 
-// CTAs that share the axis (each has a unit at least), and where CTA b starts.
-__device__ __forceinline__ long long multi_ctas(long long total, int grid) { return total < grid ? total : grid; }
-__device__ __forceinline__ long long multi_start(long long total, long long ctas, long long b) {
-    return b * (total / ctas) + min(b, total % ctas);
-}
+// The axis in equal stretches: the CTAs that have one (a unit at least), and where
+// CTA b's starts.  One division, in 32 bits where the axis is not absurdly long.
+struct MultiSplit {
+    long long each;
+    int ctas, extra;   // the first `extra` stretches have a unit more
+
+    __device__ __forceinline__ MultiSplit(long long total, int grid) {
+        ctas = total < grid ? static_cast<int>(total) : grid;
+        const unsigned d = ctas > 0 ? ctas : 1;
+        if (total >> 32) {
+            each = total / d;
+        } else {
+            each = static_cast<unsigned>(total) / d;
+        }
+        extra = static_cast<int>(total - each * d);
+    }
+    __device__ __forceinline__ long long start(int b) const { return b * each + min(b, extra); }
+};
 
 // Whether a row's query (token `tok` of its sequence) sees cache position u < n.
 __device__ __forceinline__ bool multi_sees(const MultiParams &p, const MultiSeq &s, int tok, int u) {
@@ -208,6 +238,11 @@ __device__ __forceinline__ long long multi_row(const MultiParams &p, const Multi
     return ((static_cast<long long>(s.start) + tok) * p.num_q_heads + kvh * p.group + (R - tok * p.group)) * hd;
 }
 
+// CTAs of a pass at most (a workspace has two partials for each), and the rows
+// of its items.
+constexpr int kMultiSimtCtas = 608, kMultiSimtRows = 32;
+constexpr int kMultiMmaCtas = 152, kMultiMmaRows = 256;
+
 // ------------------------------------------------------------------ join ---
 // grid (CTAs of the pass - 1, row chunks): the CTAs of column x look at the
 // boundary between stretches x and x + 1; the first boundary inside an item
@@ -215,47 +250,65 @@ __device__ __forceinline__ long long multi_row(const MultiParams &p, const Multi
 // partials k in the axis' order, a warp per row.
 template <typename OutT, int HD, typename Axis>
 __global__ void __launch_bounds__(256) multi_join_kernel(const MultiParams p, int pass_grid) {
-    constexpr int ROWS = Axis::ROWS, START = Axis::kStart;
+    constexpr int ROWS = Axis::ROWS;
     griddep_wait();
     int flags = 0;
     const MultiLocator<Axis, 256> loc(p, flags);
-    const long long ctas = multi_ctas(loc.total, pass_grid);
-    const long long b = blockIdx.x + 1;
-    if (b >= ctas) return;
+    const MultiSplit split(loc.total, pass_grid);
+    const int b = blockIdx.x + 1;
+    if (b >= split.ctas) return;
     __shared__ MultiSpot s_spot;
-    const long long unit = multi_start(loc.total, ctas, b);
+    const long long unit = split.start(b);
     loc.find(p, unit, &s_spot);
     __syncthreads();
     const MultiSpot spot = s_spot;
-    if (spot.at <= START) return;                              // the item begins with CTA b
-    const long long begin = unit - spot.at;
-    if (multi_start(loc.total, ctas, b - 1) > begin + START) return;   // an earlier boundary cuts it too
-    const long long end = begin + Axis::units(p, spot.s, spot.m);
-    int parts = 1;
-    while (b + parts - 1 < ctas && multi_start(loc.total, ctas, b + parts - 1) < end) ++parts;
-    const int rows = min(ROWS, spot.s.c * p.group - spot.m * ROWS);
+    const auto cut = [&](long long at) { return Axis::tiles_before(p, spot.s, spot.m, static_cast<int>(at)); };
+    if (cut(spot.at) == 0) return;                             // the item begins with CTA b
+    const long long begin = unit - spot.at, end = begin + Axis::units(p, spot.s, spot.m);
+    if (b > 1 && split.start(b - 1) > begin && cut(split.start(b - 1) - begin) > 0)
+        return;                                                // an earlier boundary cuts it too
+    // CTA b - 1 has the item's first partial; of those after it, each that holds a tile of the item has one.  Warp 0
+    // lists their places in order.
+    __shared__ int s_part[kMultiSimtCtas];
+    __shared__ int s_parts;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) {
+        if (lane == 0) s_part[0] = 2 * (b - 1) + 1;
+        int parts = 1;
+        for (int first = b;; first += 32) {
+            const int cta = first + lane;
+            const long long from = split.start(cta), to = split.start(cta + 1);
+            const bool inside = cta < split.ctas && from < end;
+            const bool has = inside && cut(from - begin) < cut((to < end ? to : end) - begin);
+            const unsigned have = __ballot_sync(kFull, has);
+            if (has) s_part[parts + __popc(have & ((1u << lane) - 1u))] = 2 * cta;
+            parts += __popc(have);
+            if (__ballot_sync(kFull, !inside)) break;
+        }
+        if (lane == 0) s_parts = parts;
+    }
+    __syncthreads();
+    const int parts = s_parts, rows = min(ROWS, spot.s.c * p.group - spot.m * ROWS);
     constexpr int V = HD / 32;
     for (int r = blockIdx.y * 8 + warp; r < rows; r += gridDim.y * 8) {
-        auto at = [&](int k) {
-            const long long slot = k == 0 ? 2 * (b - 1) + 1 : 2 * (b + k - 1);
-            return slot * p.slot_rows + r;
-        };
         float M = -INFINITY;
-        for (int k = lane; k < parts; k += 32) M = fmaxf(M, p.part_ml[2 * at(k)]);
+        for (int k = lane; k < parts; k += 32) M = fmaxf(M, p.part_ml[2 * (static_cast<long long>(s_part[k]) * p.slot_rows + r)]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
         const float ref = M == -INFINITY ? 0.f : M;
         float L = 0.f, acc[V] = {};
-#pragma unroll 4
+#pragma unroll 8
         for (int k = 0; k < parts; ++k) {
-            const long long i = at(k);
+            const long long i = static_cast<long long>(s_part[k]) * p.slot_rows + r;
             const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * i);
-            const float *a = p.part_acc + i * HD + lane * V;
+            float a[V];
+            if constexpr (V == 4)
+                *reinterpret_cast<float4 *>(a) = *reinterpret_cast<const float4 *>(p.part_acc + i * HD + lane * V);
+            else
+                *reinterpret_cast<float2 *>(a) = *reinterpret_cast<const float2 *>(p.part_acc + i * HD + lane * V);
+            // (a partial that saw nothing is all zeros: its reference is -inf, its sums were never added to)
             const float f = exp2f(ml.x - ref);
             L += f * ml.y;
-            // a partial that saw nothing has no rows to add (its weight is zero)
-            if (ml.x == -INFINITY && ml.y == 0.f) continue;
 #pragma unroll
             for (int v = 0; v < V; ++v) acc[v] += f * a[v];
         }
@@ -273,7 +326,7 @@ template <typename OutT, int HD, typename Axis>
 int launch_join(const MultiParams &p, int pass_grid, cudaStream_t st) {
     if (pass_grid < 2) return PA_OK;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(pass_grid - 1, (min(Axis::ROWS, p.slot_rows) + 31) / 32);
+    cfg.gridDim = dim3(pass_grid - 1, (min(Axis::ROWS, p.slot_rows) + 15) / 16);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -284,11 +337,6 @@ int launch_join(const MultiParams &p, int pass_grid, cudaStream_t st) {
     const cudaError_t e = cudaLaunchKernelEx(&cfg, multi_join_kernel<OutT, HD, Axis>, p, pass_grid);
     return e == cudaSuccess ? PA_OK : pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
 }
-
-// CTAs of a pass at most (a workspace has two partials for each), and the rows
-// of its items.
-constexpr int kMultiSimtCtas = 608, kMultiSimtRows = 32;
-constexpr int kMultiMmaCtas = 152, kMultiMmaRows = 256;
 
 int launch_multi_simt(const MultiParams &p, int head_dim, int dev, cudaStream_t st);   // fp32
 int launch_multi_mma(const MultiParams &p, int head_dim, int dev, cudaStream_t st);    // bf16

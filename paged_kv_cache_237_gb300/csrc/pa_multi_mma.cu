@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kTile = 128;                 // tokens per tile, and rows per stream
 constexpr int kMmaThreads = 384;
-using Axis = MultiAxis<kMultiMmaRows, kTile, 2>;
+using Axis = MultiAxis<kMultiMmaRows, kTile, kTile, 13>;
 
 // ---------------------------------------------------------------- tcgen05 ---
 __device__ __forceinline__ void tm_alloc(uint32_t dst, uint32_t cols) {
@@ -301,10 +301,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     int flags = 0;
     const MultiLocator<Axis, kMmaThreads> loc(p, flags);
     if (flags && blockIdx.x == 0) flag_status(p.status, flags);
-    const long long ctas = multi_ctas(loc.total, gridDim.x);
-    const bool idle = blockIdx.x >= ctas;
-    const long long unit = idle ? 0 : multi_start(loc.total, ctas, blockIdx.x);
-    long long left = idle ? 0 : multi_start(loc.total, ctas, blockIdx.x + 1) - unit;
+    const MultiSplit split(loc.total, gridDim.x);
+    const bool idle = static_cast<int>(blockIdx.x) >= split.ctas;
+    const long long unit = idle ? 0 : split.start(blockIdx.x);
+    long long left = idle ? 0 : split.start(blockIdx.x + 1) - unit;
     if (!idle) loc.find(p, unit, &ctl.spot);
     tm_fence_before();
     __syncthreads();

@@ -10,7 +10,7 @@ namespace pa {
 namespace {
 
 constexpr int kRows = 32, kTile = 16, kThreads = 128, kTok = kTile / 8;
-using Axis = MultiAxis<kRows, kTile, 2>;
+using Axis = MultiAxis<kRows, kRows, kTile, 2>;
 
 __device__ __forceinline__ float4 load4(const float *x) { return *reinterpret_cast<const float4 *>(x); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16 *x) {
@@ -37,10 +37,10 @@ __global__ void __launch_bounds__(kThreads) multi_simt_kernel(const MultiParams 
     int flags = 0;
     const MultiLocator<Axis, kThreads> loc(p, flags);
     if (flags && blockIdx.x == 0) flag_status(p.status, flags);
-    const long long ctas = multi_ctas(loc.total, gridDim.x);
-    if (blockIdx.x >= ctas) return;
-    const long long unit = multi_start(loc.total, ctas, blockIdx.x);
-    long long left = multi_start(loc.total, ctas, blockIdx.x + 1) - unit;
+    const MultiSplit split(loc.total, gridDim.x);
+    if (static_cast<int>(blockIdx.x) >= split.ctas) return;
+    const long long unit = split.start(blockIdx.x);
+    long long left = split.start(blockIdx.x + 1) - unit;
     loc.find(p, unit, &s_spot);
     __syncthreads();
     MultiSpot spot = s_spot;
