@@ -240,7 +240,7 @@ __device__ __forceinline__ long long multi_row(const MultiParams &p, const Multi
 
 // CTAs of a pass at most (a workspace has two partials for each), and the rows
 // of its items.
-constexpr int kMultiSimtCtas = 608, kMultiSimtRows = 32;
+constexpr int kMultiSimtCtas = 608, kMultiSimtRows = 64;
 constexpr int kMultiMmaCtas = 152, kMultiMmaRows = 256;
 
 // ------------------------------------------------------------------ join ---
