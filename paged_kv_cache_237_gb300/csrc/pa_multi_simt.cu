@@ -22,8 +22,6 @@
 namespace pa {
 namespace {
 
-constexpr int kTile = 64;
-
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
     asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
@@ -37,23 +35,24 @@ __device__ __forceinline__ float4 load4(const float *x) { return *reinterpret_ca
 
 template <int HD, int R>
 struct Shape {
+    static constexpr int T = R == 16 ? 32 : 64;                // tokens per tile
     static constexpr int L = R == 16 ? 32 : 16, THREADS = R / 4 * L;
-    static constexpr int TOK = kTile / L, COLS = HD / L;       // a thread's tokens and columns
+    static constexpr int TOK = T / L, COLS = HD / L;       // a thread's tokens and columns
     static constexpr int LDK = HD + 4, LDP = R + 4;            // padded rows of Q and K, and of P (by token)
     // P lies over K where two CTAs would not fit an SM otherwise; the next K then waits for the products.
     static constexpr bool OVER = HD == 128 && R == 64;
-    static constexpr int Q = 0, K = Q + R * LDK, V = K + kTile * LDK, P = OVER ? K : V + kTile * HD;
-    static constexpr int FLOATS = (OVER ? V + kTile * HD : P + kTile * LDP);
+    static constexpr int Q = 0, K = Q + R * LDK, V = K + T * LDK, P = OVER ? K : V + T * HD;
+    static constexpr int FLOATS = OVER ? V + T * HD : P + T * LDP;
     static constexpr int BYTES = FLOATS * 4;
-    static constexpr int CTAS = BYTES <= 72 * 1024 ? 3 : 2;    // per SM
-    using Axis = MultiAxis<R, R, kTile, 2>;
+    static constexpr int CTAS = R == 64 ? 2 : 4;               // per SM
+    using Axis = MultiAxis<R, R, T, 2>;
 };
 
 template <int HD, int R>
 __global__ void __launch_bounds__(Shape<HD, R>::THREADS, Shape<HD, R>::CTAS) multi_simt_kernel(const MultiParams p) {
     using S = Shape<HD, R>;
     using Axis = typename S::Axis;
-    constexpr int L = S::L, THREADS = S::THREADS, TOK = S::TOK, COLS = S::COLS, VEC = COLS < 4 ? COLS : 4;
+    constexpr int kTile = S::T, L = S::L, THREADS = S::THREADS, TOK = S::TOK, COLS = S::COLS, VEC = COLS < 4 ? COLS : 4;
     extern __shared__ __align__(16) float smem[];
     __shared__ MultiSpot s_spot;
     __shared__ int s_page[2][kTile / 16];
