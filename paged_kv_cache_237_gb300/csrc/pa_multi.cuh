@@ -232,6 +232,39 @@ __device__ __forceinline__ bool multi_sees(const MultiParams &p, const MultiSeq 
     return (j >> 6) < p.words && ((p.mask[static_cast<long long>(s.start + tok) * p.words + (j >> 6)] >> (j & 63)) & 1ull);
 }
 
+// Which of the 32 positions from u on a row sees, as bits.
+__device__ __forceinline__ uint32_t multi_seen_bits(const MultiParams &p, const MultiSeq &s, int tok, int u) {
+    const auto below = [](int count) { return count <= 0 ? 0u : (count >= 32 ? ~0u : (1u << count) - 1u); };
+    const int base = s.n - s.c;
+    if (p.see == kSeeAll) return below(s.n - u);
+    if (p.see == kSeeChain) return below(min(s.n, base + tok + 1) - u);
+    uint32_t bits = below(base - u);
+    const int j = u - base;   // first position's node, negative before the tree
+    if (j > -32 && u < s.n) {
+        const unsigned long long *row = p.mask + static_cast<long long>(s.start + tok) * p.words;
+        const int w = j >> 6;
+        const unsigned long long a = w >= 0 && w < p.words ? row[w] : 0ull;
+        const unsigned long long b = w + 1 >= 0 && w + 1 < p.words ? row[w + 1] : 0ull;
+        const int sh = j & 63;
+        bits |= static_cast<uint32_t>(sh ? (a >> sh) | (b << (64 - sh)) : a);
+    }
+    return bits & below(s.n - u);
+}
+
+// Sets the bf16 values of 16 bytes in shared memory that are not finite to zero; whether there were any.
+__device__ __forceinline__ bool clear_not_finite(uint4 &at) {
+    uint4 x = at;
+    uint32_t *w = &x.x;
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if ((w[e] & 0x7f80u) == 0x7f80u) bad = true, w[e] &= 0xffff0000u;
+        if ((w[e] & 0x7f800000u) == 0x7f800000u) bad = true, w[e] &= 0xffffu;
+    }
+    if (bad) at = x;
+    return bad;
+}
+
 // Element offset of row R of KV head kvh's problem in q and out.
 __device__ __forceinline__ long long multi_row(const MultiParams &p, const MultiSeq &s, int kvh, int R, int hd) {
     const int tok = R / p.group;
@@ -340,5 +373,6 @@ int launch_join(const MultiParams &p, int pass_grid, cudaStream_t st) {
 
 int launch_multi_simt(const MultiParams &p, int head_dim, int dev, cudaStream_t st);   // fp32
 int launch_multi_mma(const MultiParams &p, int head_dim, int dev, cudaStream_t st);    // bf16
+int launch_multi_few(const MultiParams &p, int head_dim, int dev, cudaStream_t st);    // bf16, few rows per sequence
 
 }  // namespace pa

@@ -244,25 +244,6 @@ __device__ __forceinline__ bool await_two(Control &c, uint64_t *first, uint32_t 
     return __all_sync(kFull, ok);
 }
 
-// Which of the 32 positions from u on a row sees, as bits.
-__device__ __forceinline__ uint32_t seen_bits(const MultiParams &p, const MultiSeq &s, int tok, int u) {
-    const auto below = [](int count) { return count <= 0 ? 0u : (count >= 32 ? ~0u : (1u << count) - 1u); };
-    const int base = s.n - s.c;
-    if (p.see == kSeeAll) return below(s.n - u);
-    if (p.see == kSeeChain) return below(min(s.n, base + tok + 1) - u);
-    uint32_t bits = below(base - u);
-    const int j = u - base;   // first position's node, negative before the tree
-    if (j > -32 && u < s.n) {
-        const unsigned long long *row = p.mask + static_cast<long long>(s.start + tok) * p.words;
-        const int w = j >> 6;
-        const unsigned long long a = w >= 0 && w < p.words ? row[w] : 0ull;
-        const unsigned long long b = w + 1 >= 0 && w + 1 < p.words ? row[w + 1] : 0ull;
-        const int sh = j & 63;
-        bits |= static_cast<uint32_t>(sh ? (a >> sh) | (b << (64 - sh)) : a);
-    }
-    return bits & below(s.n - u);
-}
-
 template <int HD>
 __global__ void __launch_bounds__(kMmaThreads, 1)
     multi_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -510,18 +491,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         if (u0 + j >= seen) {
                             *at = make_uint4(0u, 0u, 0u, 0u);
                         } else {
-                            uint4 x = *at;
-                            uint32_t *w = &x.x;
-                            bool bad = false;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if ((w[e] & 0x7f80u) == 0x7f80u) bad = true, w[e] &= 0xffff0000u;
-                                if ((w[e] & 0x7f800000u) == 0x7f800000u) bad = true, w[e] &= 0xffffu;
-                            }
-                            if (bad) {
-                                *at = x;
-                                ctl.dirty[item_no & 1] = item_no;
-                            }
+                            if (clear_not_finite(*at)) ctl.dirty[item_no & 1] = item_no;
                         }
                     }
                     fence_proxy_async_smem();
@@ -536,7 +506,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     for (int g = 2; g < 4; ++g) tm_ld32(ts + g * 32, x + g * 32);
                     const bool masked = u0 + kTile > clear;
                     const auto hide = [&](int g) {
-                        const uint32_t bits = seen_bits(p, it.s, tok, u0 + g * 32);
+                        const uint32_t bits = multi_seen_bits(p, it.s, tok, u0 + g * 32);
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
                             if (!((bits >> c) & 1u)) x[g * 32 + c] = -INFINITY;
@@ -656,7 +626,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     for (int c = 0; c < 16; ++c) o[c] = second ? fmaf(o1[c], f[1], o[c] * f[0]) : o[c] * f[0];
                     if (dirty && r < rows)
                         for (int u = max(max(base, 0), it.tile0 * kTile); u < min(seen, it.tile1 * kTile); ++u) {
-                            if (!(seen_bits(p, it.s, tok, u) & 1u)) continue;
+                            if (!(multi_seen_bits(p, it.s, tok, u) & 1u)) continue;
                             const int b = p.block_tables[static_cast<long long>(it.seq) * p.width + u / p.block_size];
                             if (b < 0 || b >= p.num_blocks) continue;
                             const __nv_bfloat16 *vr =
