@@ -324,26 +324,42 @@ __global__ void __launch_bounds__(256) multi_join_kernel(const MultiParams p, in
     const int parts = s_parts, rows = min(ROWS, spot.s.c * p.group - spot.m * ROWS);
     constexpr int V = HD / 32;
     for (int r = blockIdx.y * 8 + warp; r < rows; r += gridDim.y * 8) {
-        float M = -INFINITY;
-        for (int k = lane; k < parts; k += 32) M = fmaxf(M, p.part_ml[2 * (static_cast<long long>(s_part[k]) * p.slot_rows + r)]);
+        // Eight partials at a time, all of their loads in flight at once.
+        constexpr int kBatch = 8;
+        float M = -INFINITY, L = 0.f, acc[V] = {};
+        for (int k0 = 0; k0 < parts; k0 += kBatch) {
+            float2 ml[kBatch];
+            float a[kBatch][V];
+            float top = M;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        const float ref = M == -INFINITY ? 0.f : M;
-        float L = 0.f, acc[V] = {};
-#pragma unroll 8
-        for (int k = 0; k < parts; ++k) {
-            const long long i = static_cast<long long>(s_part[k]) * p.slot_rows + r;
-            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * i);
-            float a[V];
-            if constexpr (V == 4)
-                *reinterpret_cast<float4 *>(a) = *reinterpret_cast<const float4 *>(p.part_acc + i * HD + lane * V);
-            else
-                *reinterpret_cast<float2 *>(a) = *reinterpret_cast<const float2 *>(p.part_acc + i * HD + lane * V);
+            for (int k = 0; k < kBatch; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int v = 0; v < V; ++v) a[k][v] = 0.f;
+                if (k0 + k < parts) {
+                    const long long i = static_cast<long long>(s_part[k0 + k]) * p.slot_rows + r;
+                    ml[k] = *reinterpret_cast<const float2 *>(p.part_ml + 2 * i);
+                    if constexpr (V == 4)
+                        *reinterpret_cast<float4 *>(a[k]) = *reinterpret_cast<const float4 *>(p.part_acc + i * HD + lane * V);
+                    else
+                        *reinterpret_cast<float2 *>(a[k]) = *reinterpret_cast<const float2 *>(p.part_acc + i * HD + lane * V);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
             // (a partial that saw nothing is all zeros: its reference is -inf, its sums were never added to)
-            const float f = exp2f(ml.x - ref);
-            L += f * ml.y;
+            const float ref = top == -INFINITY ? 0.f : top, keep = exp2f(M - ref);
+            M = top;
+            L *= keep;
 #pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] += f * a[v];
+            for (int v = 0; v < V; ++v) acc[v] *= keep;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const float f = exp2f(ml[k].x - ref);
+                L += f * ml[k].y;
+#pragma unroll
+                for (int v = 0; v < V; ++v) acc[v] += f * a[k][v];
+            }
         }
         // l is zero only for a row that sees nothing; a sum that is not a number stays one
         const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -359,7 +375,7 @@ template <typename OutT, int HD, typename Axis>
 int launch_join(const MultiParams &p, int pass_grid, cudaStream_t st) {
     if (pass_grid < 2) return PA_OK;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(pass_grid - 1, (min(Axis::ROWS, p.slot_rows) + 15) / 16);
+    cfg.gridDim = dim3(pass_grid - 1, min((min(Axis::ROWS, p.slot_rows) + 7) / 8, 16));
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
