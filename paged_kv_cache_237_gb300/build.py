@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_SOURCES = ["pa_decode.cu", "pa_decode_simt.cu", "pa_cache.cu", "pa_decode_q4.cu", "pa_cache_q4.cu",
-                "pa_tables.cu", "pa_tree.cu", "pa_multi.cu", "pa_multi_simt.cu",
+                "pa_tables.cu", "pa_tree.cu", "pa_multi.cu", "pa_multi_f32.cu",
                 "pa_multi_mma.cu", "pa_multi_few.cu"]
 CXX_SOURCES = ["block_manager.cpp", "pa_api.cpp"]
 HEADERS = ["pa_internal.h", "pa_decode_common.cuh", "pa_q4.cuh", "pa_multi.cuh"]

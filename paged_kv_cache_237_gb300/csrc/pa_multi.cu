@@ -19,10 +19,10 @@ MultiLayout multi_layout(int num_tokens, int group, int head_dim, bool f32) {
     const long long need = static_cast<long long>(num_tokens) * group;
     const auto least = [&](int most) { return static_cast<int>(need < most ? need : most); };
     MultiLayout l;
-    l.rows = least(f32 ? pa::kMultiSimtRows : pa::kMultiMmaRows);
-    size_t slots = 2ull * (f32 ? pa::kMultiSimtCtas : pa::kMultiMmaCtas) * l.rows;
+    l.rows = least(f32 ? pa::kMultiF32Rows : pa::kMultiMmaRows);
+    size_t slots = 2ull * (f32 ? pa::kMultiFewCtas : pa::kMultiMmaCtas) * l.rows;
     if (!f32) {   // the pass for few rows has more CTAs with fewer rows each; both fit
-        const size_t few = 2ull * pa::kMultiSimtCtas * least(16);
+        const size_t few = 2ull * pa::kMultiFewCtas * least(16);
         slots = slots > few ? slots : few;
     }
     l.acc = align256(slots * 2 * sizeof(float));
@@ -99,7 +99,7 @@ int decode_multi(void *out, const void *q, const void *k_cache, const void *v_ca
     if (cudaGetDevice(&dev) != cudaSuccess) return pa_fail(PA_ERR_CUDA, "pa_decode_tree/cross: no CUDA device");
     if (sm_count(dev) <= 0) return pa_fail(PA_ERR_CUDA, "pa_decode_tree/cross: cannot query the SM count");
     const cudaStream_t st = static_cast<cudaStream_t>(a->stream);
-    if (a->dtype == PA_F32) return pa::launch_multi_simt(p, head_dim, dev, st);
+    if (a->dtype == PA_F32) return pa::launch_multi_f32(p, head_dim, dev, st);
     // By the batch's average rows per sequence and KV head (all that the host knows).
     const bool few = static_cast<long long>(num_tokens) * p.group <= kFewRows * static_cast<long long>(a->num_seqs);
     return few ? pa::launch_multi_few(p, head_dim, dev, st) : pa::launch_multi_mma(p, head_dim, dev, st);

@@ -273,7 +273,7 @@ __device__ __forceinline__ long long multi_row(const MultiParams &p, const Multi
 
 // CTAs of a pass at most (a workspace has two partials for each), and the rows
 // of its items.
-constexpr int kMultiSimtCtas = 608, kMultiSimtRows = 64;
+constexpr int kMultiFewCtas = 608, kMultiF32Rows = 32;
 constexpr int kMultiMmaCtas = 152, kMultiMmaRows = 256;
 
 // ------------------------------------------------------------------ join ---
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(256) multi_join_kernel(const MultiParams p, in
         return;                                                // an earlier boundary cuts it too
     // CTA b - 1 has the item's first partial; of those after it, each that holds a tile of the item has one.  Warp 0
     // lists their places in order.
-    __shared__ int s_part[kMultiSimtCtas];
+    __shared__ int s_part[kMultiFewCtas];
     __shared__ int s_parts;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
@@ -387,7 +387,7 @@ int launch_join(const MultiParams &p, int pass_grid, cudaStream_t st) {
     return e == cudaSuccess ? PA_OK : pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
 }
 
-int launch_multi_simt(const MultiParams &p, int head_dim, int dev, cudaStream_t st);   // fp32
+int launch_multi_f32(const MultiParams &p, int head_dim, int dev, cudaStream_t st);   // fp32
 int launch_multi_mma(const MultiParams &p, int head_dim, int dev, cudaStream_t st);    // bf16
 int launch_multi_few(const MultiParams &p, int head_dim, int dev, cudaStream_t st);    // bf16, few rows per sequence
 

@@ -333,7 +333,7 @@ int multi_few(const MultiParams &p, int dev, cudaStream_t st) {
     CUtensorMap mk, mv;
     if (!host::make_map(&mk, p.k_cache, p.total_rows, HD) || !host::make_map(&mv, p.v_cache, p.total_rows, HD))
         return pa_fail(PA_ERR_CUDA, "pa_decode_tree/cross: cuTensorMapEncodeTiled failed");
-    const int grid = min(host::sm_count(dev) * min(occ, Ring<HD>::CTAS), kMultiSimtCtas);
+    const int grid = min(host::sm_count(dev) * min(occ, Ring<HD>::CTAS), kMultiFewCtas);
     const cudaError_t e = host::launch_dependent(kernel, grid, kThreads, Ring<HD>::BYTES, st, mk, mv, p);
     if (e != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
     return launch_join<__nv_bfloat16, HD, Axis>(p, grid, st);
