@@ -228,6 +228,14 @@ def _check_cuda(t: torch.Tensor, name: str, dtypes, dev=None):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _check_int32(dev: torch.device, **tensors) -> None:
+    """``_check_cuda`` of several int32 tensors on one device."""
+    at, i32 = dev.index, torch.int32
+    for name, t in tensors.items():
+        if not (t.__class__ is torch.Tensor and t.dtype is i32 and t.get_device() == at and t.is_contiguous()):
+            _check_cuda(t, name, (i32,), dev)
+
+
 def _dtype_code(dt: torch.dtype) -> int:
     if dt == torch.float32:
         return PA_F32
@@ -420,13 +428,9 @@ def pa_reshape_and_cache(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor
     T = slot_mapping.shape[0]
     if tuple(k.shape) != (T, Hkv, hd) or tuple(v.shape) != (T, Hkv, hd) or v_cache.shape != k_cache.shape:
         raise ValueError("inconsistent shapes")
-    with torch.cuda.device(dev):
-        rc = _lib.pa_reshape_and_cache(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                       slot_mapping.data_ptr(), T, Hkv, hd, bs, nb,
-                                       _dtype_code(k_cache.dtype),
-                                       status.ptr() if status is not None else None,
-                                       _stream_ptr(stream, dev))
-    _raise(rc)
+    _call(dev, _lib.pa_reshape_and_cache, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          slot_mapping.data_ptr(), T, Hkv, hd, bs, nb, _dtype_code(k_cache.dtype),
+          status.ptr() if status is not None else None, _stream_ptr(stream, dev))
 
 
 def pa_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src_dst_pairs: torch.Tensor, *,
@@ -683,8 +687,7 @@ def _multi_call(tree, out, q, k_cache, v_cache, block_tables, context_lens, quer
     dev = q.device
     for name, t in (("out", out), ("k_cache", k_cache), ("v_cache", v_cache)):
         _check_cuda(t, name, (q.dtype,), dev)
-    for name, t in (("block_tables", block_tables), ("context_lens", context_lens), ("query_start", query_start)):
-        _check_cuda(t, name, (torch.int32,), dev)
+    _check_int32(dev, block_tables=block_tables, context_lens=context_lens, query_start=query_start)
     if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
         raise ValueError("q must be [T, Hq, hd], caches [num_blocks, Hkv, bs, hd], tables [S, max_blocks]")
     T, Hq, hd = q.shape
@@ -723,10 +726,9 @@ def pa_build_tree(tree_mask: torch.Tensor, positions: torch.Tensor | None, paren
     """
     _check_cuda(tree_mask, "tree_mask", (torch.int64,))
     dev = tree_mask.device
-    for name, t in (("parents", parents), ("query_start", query_start), ("context_lens", context_lens)):
-        _check_cuda(t, name, (torch.int32,), dev)
+    _check_int32(dev, parents=parents, query_start=query_start, context_lens=context_lens)
     if positions is not None:
-        _check_cuda(positions, "positions", (torch.int32,), dev)
+        _check_int32(dev, positions=positions)
     T, S = parents.shape[0], context_lens.shape[0]
     if (tree_mask.dim() != 2 or tree_mask.shape[0] != T or parents.shape != (T,) or context_lens.shape != (S,)
             or query_start.shape != (S + 1,) or (positions is not None and positions.shape != (T,))):
@@ -755,18 +757,17 @@ def pa_accept_tree(accepted_lens: torch.Tensor, accepted_nodes: torch.Tensor, ne
     """
     _check_cuda(accepted_nodes, "accepted_nodes", (torch.int32,))
     dev = accepted_nodes.device
-    for name, t in (("accepted_lens", accepted_lens), ("next_tokens", next_tokens), ("new_lens", new_lens),
-                    ("draft_tokens", draft_tokens), ("target_tokens", target_tokens), ("query_start", query_start),
-                    ("context_lens", context_lens), ("block_tables", block_tables)):
-        _check_cuda(t, name, (torch.int32,), dev)
+    _check_int32(dev, accepted_lens=accepted_lens, next_tokens=next_tokens, new_lens=new_lens,
+                 draft_tokens=draft_tokens, target_tokens=target_tokens, query_start=query_start,
+                 context_lens=context_lens, block_tables=block_tables)
     _check_cuda(slot_pairs, "slot_pairs", (torch.int64,), dev)
     if parents is not None:
-        _check_cuda(parents, "parents", (torch.int32,), dev)
+        _check_int32(dev, parents=parents)
     if accepted_nodes.dim() != 2 or block_tables.dim() != 2 or draft_tokens.dim() != 1:
         raise ValueError("accepted_nodes must be [S, M], block_tables [S, max_blocks], draft_tokens [T]")
     (S, M), T = accepted_nodes.shape, draft_tokens.shape[0]
-    if (any(t.shape != (S,) for t in (accepted_lens, next_tokens, new_lens, context_lens))
-            or slot_pairs.shape != (S, M, 2) or target_tokens.shape != (T,) or query_start.shape != (S + 1,)
+    if (accepted_lens.shape != (S,) or next_tokens.shape != (S,) or new_lens.shape != (S,)
+            or context_lens.shape != (S,) or slot_pairs.shape != (S, M, 2) or target_tokens.shape != (T,) or query_start.shape != (S + 1,)
             or block_tables.shape[0] != S or (parents is not None and parents.shape != (T,))):
         raise ValueError("inconsistent shapes")
     _call(dev, _lib.pa_accept_tree, accepted_lens.data_ptr(), accepted_nodes.data_ptr(), next_tokens.data_ptr(),
