@@ -529,7 +529,15 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_hea
  *
  * out = softmax over the seen t of scale * (q . K[t]), times V[t]; a row that sees
  * nothing (n_i = 0, an empty mask) is zero.  What a row does not see has weight
- * zero, whatever its cache slots hold (NaN included).
+ * zero, whatever its cache slots hold (NaN included); a value that it sees and that is
+ * not finite leaves its column of the row without a finite result (an infinity may come
+ * out as NaN in PA_BF16, as in pa_decode).
+ * Arithmetic: scores, maxima, sums and results are fp32.  PA_BF16: q, K and V enter
+ * exactly, weights as two bf16 parts (16 bits), or as one (2^-8 at most, at random)
+ * where the batch has many rows per sequence and no weight of 32 rows and 64 or 128
+ * tokens is above 1/32 of its row's sum so far.  PA_F32: q, K, V and weights as two
+ * tf32 parts each, three of their four products (3 * 2^-20 of a product's size at most,
+ * far less on average).
  *
  * args as for pa_decode: num_seqs, max_blocks_per_seq, num_blocks, dtype,
  * max_context_len (longer entries are clamped and flagged), dev_status, stream, and

@@ -7,7 +7,19 @@ namespace {
 
 using namespace pa::host;
 
-constexpr int kFewRows = 24;
+// Which bf16 pass a batch takes, by what the host knows of it: the average rows per
+// sequence and KV head, in blocks of 16 (the few-rows pass reads K and V once per
+// block, the tcgen05 pass once per 256 rows), and the longest context.  Measured, few
+// rows against tcgen05 (us): 32 sequences of 2000..4000 tokens, 8 KV heads of 128:
+// 16 rows 87 / 100, 24 rows 140 / 100; 64 sequences of 350..700 tokens: 16 rows
+// 43 / 68, 32 rows 68 / 68, 48 rows 85 / 71 (heads of 64: 51 / 59, 64 rows 63 / 59);
+// 8 sequences of 450..900: 64 rows 32 / 35, 96 rows 36 / 36.
+bool few_rows(const pa::MultiParams &p, int head_dim) {
+    const long long rows = (static_cast<long long>(p.num_tokens) * p.group + p.num_seqs - 1) / p.num_seqs;
+    const long long blocks = (rows + 15) / 16;
+    return blocks == 1 ||
+           (blocks <= 6 && blocks * p.num_seqs * p.num_kv_heads * p.ctx_cap * (head_dim / 64) <= 1200000);
+}
 
 struct MultiLayout {
     size_t acc, bytes;   // where the rows' sums start, and the workspace's size
@@ -100,8 +112,7 @@ int decode_multi(void *out, const void *q, const void *k_cache, const void *v_ca
     if (sm_count(dev) <= 0) return pa_fail(PA_ERR_CUDA, "pa_decode_tree/cross: cannot query the SM count");
     const cudaStream_t st = static_cast<cudaStream_t>(a->stream);
     if (a->dtype == PA_F32) return pa::launch_multi_f32(p, head_dim, dev, st);
-    // By the batch's average rows per sequence and KV head (all that the host knows).
-    const bool few = static_cast<long long>(num_tokens) * p.group <= kFewRows * static_cast<long long>(a->num_seqs);
+    const bool few = few_rows(p, head_dim);
     return few ? pa::launch_multi_few(p, head_dim, dev, st) : pa::launch_multi_mma(p, head_dim, dev, st);
 }
 

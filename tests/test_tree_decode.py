@@ -77,6 +77,8 @@ def check(pa, b, scale, **kw):
     return out
 
 
+# Head counts that put a test's batch into items of few rows (4 query heads a KV head at most) or many (16).
+WIDTHS = [2, 16]
 LENS = [0, 1, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 257, 400]
 
 
@@ -89,7 +91,8 @@ def counts(kind, lens, most, seed):
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", multi_ref.KINDS)
 @pytest.mark.parametrize("dtype,hd,bs", TYPES)
-@pytest.mark.parametrize("most,Hq,Hkv", [(1, 4, 2), (9, 4, 2), (40, 2, 2), (70, 6, 2), (150, 4, 1)])
+@pytest.mark.parametrize("most,Hq,Hkv", [(1, 4, 2), (9, 4, 2), (40, 2, 2), (70, 6, 2), (150, 4, 1), (30, 32, 2),
+                                          (120, 16, 2), (8, 32, 1)])
 def test_edge_lengths(pa, kind, dtype, hd, bs, most, Hq, Hkv):
     b = Batch(kind, LENS, counts(kind, LENS, most, most), Hq, Hkv, hd, bs, dtype, most + hd, padding=3)
     check(pa, b, hd ** -0.5)
@@ -108,16 +111,18 @@ def test_head_groups(pa, kind, group, dtype):
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", multi_ref.KINDS)
 @pytest.mark.parametrize("dtype,hd,bs", TYPES)
-def test_one_long_sequence_and_many_short_ones(pa, kind, dtype, hd, bs):
+@pytest.mark.parametrize("width", WIDTHS)
+def test_one_long_sequence_and_many_short_ones(pa, kind, dtype, hd, bs, width):
     """The axis is cut inside the long one and between the short ones."""
     lens = [9000] + [int(x) for x in np.random.default_rng(1).integers(1, 40, size=300)]
-    b = Batch(kind, lens, counts(kind, lens, 3, 2), 2, 1, hd, bs, dtype, 3)
+    b = Batch(kind, lens, counts(kind, lens, 3, 2), width, 1, hd, bs, dtype, 3)
     check(pa, b, hd ** -0.5)
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype,hd,bs", TYPES)
-def test_arbitrary_masks_and_empty_rows(pa, dtype, hd, bs):
+@pytest.mark.parametrize("width", [1, *WIDTHS])
+def test_arbitrary_masks_and_empty_rows(pa, dtype, hd, bs, width):
     """Bits in any pattern (later tokens, not itself); rows that see nothing at all are zero."""
     rng = np.random.default_rng(4)
     news = [130, 64, 65, 5, 1]
@@ -125,7 +130,7 @@ def test_arbitrary_masks_and_empty_rows(pa, dtype, hd, bs):
     see = [rng.random((c, c)) < 0.3 for c in news]
     see[0][7] = see[2][64] = see[3][:] = False
     see[4][:] = False
-    b = Batch("mask", lens, news, 4, 2, hd, bs, dtype, 5, see=see)
+    b = Batch("mask", lens, news, 2 * width, 2, hd, bs, dtype, 5, see=see)
     out = check(pa, b, 0.2)
     at = b.start
     for row in (at[0] + 7, at[2] + 64, *range(at[3], at[5])):
@@ -136,11 +141,12 @@ def test_arbitrary_masks_and_empty_rows(pa, dtype, hd, bs):
 @pytest.mark.parametrize("kind", ["mask", "chain"])
 @pytest.mark.parametrize("dtype,hd,bs", TYPES)
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_hidden_tokens_may_hold_anything(pa, kind, dtype, hd, bs, bad):
+@pytest.mark.parametrize("width", WIDTHS)
+def test_hidden_tokens_may_hold_anything(pa, kind, dtype, hd, bs, bad, width):
     """A drafted token whose values or keys are not finite spoils the rows that see it and no other."""
     c, n = 20, 150
     for side in ("v", "k"):
-        b = Batch(kind, [n, n], [c, c], 4, 2, hd, bs, dtype, 6)
+        b = Batch(kind, [n, n], [c, c], 2 * width, 2, hd, bs, dtype, 6)
         if kind == "mask":
             b.see[0][:, 11] = False
             b.see[0][[12, 14], 11] = True
@@ -155,7 +161,7 @@ def test_hidden_tokens_may_hold_anything(pa, kind, dtype, hd, bs, bad):
         sees = b.visible(0)[:, pos]
         rows = torch.from_numpy(np.flatnonzero(sees))
         hit = torch.zeros_like(clean, dtype=torch.bool)
-        hit[rows[:, None], torch.tensor([2, 3])] = True          # the query heads of KV head 1
+        hit[rows, width:] = True          # the query heads of KV head 1
         if side == "v":
             hit[:, :, 5:] = False
         got = out.double().cpu()
@@ -172,8 +178,9 @@ def test_hidden_tokens_may_hold_anything(pa, kind, dtype, hd, bs, bad):
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", multi_ref.KINDS)
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_bad_device_data_is_flagged_and_harmless(pa, kind, dtype):
-    b = Batch(kind, [100, 50, 300], [4, 3, 20], 4, 2, 64, 16, dtype, 8)
+@pytest.mark.parametrize("width", WIDTHS)
+def test_bad_device_data_is_flagged_and_harmless(pa, kind, dtype, width):
+    b = Batch(kind, [100, 50, 300], [4, 3, 20], 2 * width, 2, 64, 16, dtype, 8)
     ref = b.reference(0.1)
     # a block id out of range reads as zeros
     b.tables[0, 2] = 10**6
@@ -220,9 +227,10 @@ def test_mask_shorter_than_the_tree_hides_the_rest(pa, dtype):
 @pytest.mark.gpu
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_scales(pa, scale, dtype):
+@pytest.mark.parametrize("width", WIDTHS)
+def test_scales(pa, scale, dtype, width):
     """Flat, reversed and peaked scores."""
-    b = Batch("cross", [700, 40], [9, 30], 4, 2, 128, 16, dtype, 10)
+    b = Batch("cross", [700, 40], [9, 30], 2 * width, 2, 128, 16, dtype, 10)
     out, _ = b.on_gpu(pa, scale)
     ref = b.reference(scale)
     if dtype == torch.float32 and scale == 3.0:
@@ -250,10 +258,11 @@ def test_one_query_is_a_decode_step(pa, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_repeatable_on_other_streams_and_in_graphs(pa, dtype):
+@pytest.mark.parametrize("width", WIDTHS)
+def test_repeatable_on_other_streams_and_in_graphs(pa, dtype, width):
     """Bit-identical results from call to call, on a side stream without a workspace, and replayed."""
     from paged_kv_cache_237_gb300.engine import TreeDecodeStep
-    b = Batch("mask", [3100, 40, 900], [20, 5, 33], 8, 2, 128, 16, dtype, 12)
+    b = Batch("mask", [3100, 40, 900], [20, 5, 33], 2 * width, 2, 128, 16, dtype, 12)
     first, _ = b.on_gpu(pa, 0.1)
     args = [b.q.cuda(), b.k.cuda(), b.v.cuda(), torch.from_numpy(b.tables).cuda(),
             torch.tensor(b.lens, dtype=torch.int32).cuda(), torch.from_numpy(b.start).cuda(), 0.1]
@@ -287,7 +296,8 @@ def test_repeatable_on_other_streams_and_in_graphs(pa, dtype):
 
 
 @pytest.mark.gpu
-def test_large_offsets(pa):
+@pytest.mark.parametrize("width", WIDTHS)
+def test_large_offsets(pa, width):
     """A cache whose element offsets pass 2^31."""
     bs, hd, Hkv = 32, 128, 4
     nb = 2**31 // (bs * hd * Hkv) + 40
@@ -295,7 +305,7 @@ def test_large_offsets(pa):
     v = torch.zeros_like(k)
     ids = torch.tensor([nb - 1, 3, nb - 20, nb - 7, 2], dtype=torch.int32)
     g = torch.Generator().manual_seed(0)
-    small = Batch("chain", [150], [30], 8, Hkv, hd, bs, torch.bfloat16, 13)
+    small = Batch("chain", [150], [30], Hkv * width, Hkv, hd, bs, torch.bfloat16, 13)
     small.tables = np.arange(5, dtype=np.int32)[None]
     small.k, small.v = (torch.randn(5, Hkv, bs, hd, generator=g).bfloat16() for _ in range(2))
     k[ids.long().cuda()], v[ids.long().cuda()] = small.k.cuda(), small.v.cuda()
@@ -321,3 +331,73 @@ def test_binding_checks_shapes_and_types(pa):
             ("workspace", torch.zeros(64, dtype=torch.uint8, device="cuda"), pa.PAError)]:
         with pytest.raises(error):
             pa.pa_decode_tree(**{**good, name: bad})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,hd", [(torch.bfloat16, 128), (torch.float32, 64)])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_peaked_and_rising_scores(pa, dtype, hd, width):
+    """Scores that rise along the context by much more than fp32's exponent holds, and one token that outweighs all:
+    running maxima move at almost every step."""
+    b = Batch("cross", [1500, 300], [10, 7], width, 1, hd, 16, dtype, 15)
+    b.q[:] = b.q.abs()
+    t = torch.arange(1500)
+    blocks = torch.from_numpy(b.tables[0]).long()[t // 16]
+    b.k[blocks, 0, t % 16] = (t[:, None] * 0.02).expand(-1, hd).to(dtype)
+    t = torch.arange(300)
+    blocks = torch.from_numpy(b.tables[1]).long()[t // 16]
+    b.k[blocks, 0, t % 16] *= 0.01
+    b.k[int(b.tables[1, 11]), 0, 3] = 5.0
+    out, flags = b.on_gpu(pa, hd ** -0.5)
+    assert flags == 0
+    ref = b.reference(hd ** -0.5)
+    # a score is off by at most (hd + 2) 2^-21 of the sum of |scale q k|, here up to 30 x 0.8 hd / sqrt(hd); a weight by e
+    # to twice that, and the result by so much of the values (below 5)
+    e = 2 * (hd + 2) * 2.0 ** -21 * 24 * hd ** 0.5
+    tol = 2.0 ** -8 * ref.abs() + 2e-3 if dtype == torch.bfloat16 else 5 * e + 1e-5
+    assert ((out.double().cpu() - ref).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_visible_infinities_show(pa, dtype, width):
+    """An infinite value that every row sees leaves every row's column without a finite result, and no other column.
+    (In bf16 not always an infinity: a weight enters as two parts, hi + lo, and lo is zero for a weight that one part
+    holds, and of either sign; infinity times zero, and infinities of two signs, are not numbers.)"""
+    b = Batch("cross", [400, 90], [12, 3], width, 1, 64, 16, dtype, 16)
+    at = lambda i, u: (int(b.tables[i, u // 16]), 0, u % 16)
+    b.v[at(0, 7)][0] = float("inf")
+    b.v[at(0, 300)][1] = -float("inf")
+    b.v[at(0, 200)][2], b.v[at(0, 201)][2] = float("inf"), -float("inf")
+    out = b.on_gpu(pa, 0.125)[0].double().cpu()
+    assert not out[:12, :, :3].isfinite().any() and out[:12, :, 2].isnan().all()
+    if dtype == torch.float32:
+        assert (out[:12, :, 0] == float("inf")).all() and (out[:12, :, 1] == -float("inf")).all()
+    ref = b.reference(0.125)
+    assert_decode_close(out[:12, :, 3:], ref[:12, :, 3:], dtype)
+    assert_decode_close(out[12:], ref[12:], dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_two_streams_with_workspaces_of_their_own(pa, dtype):
+    batches = [Batch("mask", [2000, 70], [20, 9], 16, 2, 64, 16, dtype, 17), Batch("cross", [900] * 8, [60] * 8, 2, 2, 128,
+                                                                                  16, dtype, 18)]
+    calls = []
+    for b in batches:
+        args = [torch.zeros_like(b.q).cuda(), b.q.cuda(), b.k.cuda(), b.v.cuda(), torch.from_numpy(b.tables).cuda(),
+                torch.tensor(b.lens, dtype=torch.int32).cuda(), torch.from_numpy(b.start).cuda(), 0.1]
+        T, Hq, hd = b.q.shape
+        ws = torch.empty(pa.pa_decode_tree_workspace_size(T, Hq, b.k.shape[1], hd), dtype=torch.uint8, device="cuda")
+        kw = dict(max_context_len=max(b.lens), workspace=ws, stream=torch.cuda.Stream())
+        if b.kind == "mask":
+            kw["tree_mask"] = b.mask.cuda()
+        calls.append((pa.pa_decode_tree if b.kind == "mask" else pa.pa_decode_cross, args, kw))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for call, args, kw in calls:
+            call(*args, **kw)
+    torch.cuda.synchronize()
+    for b, (_, args, _) in zip(batches, calls):
+        assert_decode_close(args[0], b.reference(0.1), dtype)
