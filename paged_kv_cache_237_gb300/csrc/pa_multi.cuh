@@ -4,9 +4,9 @@
 //
 // Work.  A sequence's c queries times the `group` query heads of one KV head
 // are rows R = token * group + head of that head's problem; an item is up to
-// ROWS of them, and costs units for each KT tokens of the cache that any of its
-// rows sees (three, or two if it has at most HALF rows; one where HALF = ROWS),
-// and START units for its beginning and end.  All items of the
+// ROWS of them, and costs a unit for each KT tokens of the cache that any of its
+// rows sees (two, if it has more than HALF rows), and START units for its
+// beginning and end.  All items of the
 // batch lie end to end on one axis of units (sequence, KV head, row block), and
 // each CTA takes an equal stretch of it, whatever the lengths.  A CTA whose
 // stretch holds an item whole writes its rows; where a stretch ends inside an
@@ -94,7 +94,7 @@ struct MultiAxis {
 
     // Units of one tile.
     static __device__ __forceinline__ int cost(const MultiParams &p, const MultiSeq &s, int m) {
-        return HALF < ROWS ? (s.c * p.group - m * ROWS > HALF ? 3 : 2) : 1;
+        return HALF < ROWS && s.c * p.group - m * ROWS > HALF ? 2 : 1;
     }
 
     static __device__ __forceinline__ int units(const MultiParams &p, const MultiSeq &s, int m) {
@@ -103,9 +103,7 @@ struct MultiAxis {
 
     // Tiles that lie before unit `at` of an item: where a stretch that begins or ends there cuts it.
     static __device__ __forceinline__ int tiles_before(const MultiParams &p, const MultiSeq &s, int m, int at) {
-        if (at <= START) return 0;
-        const unsigned u = at - START;
-        return HALF < ROWS ? (cost(p, s, m) == 3 ? u / 3u : u / 2u) : u;
+        return at <= START ? 0 : (at - START) >> (cost(p, s, m) - 1);
     }
 
     // Units of one KV head of a sequence.

@@ -32,7 +32,15 @@ namespace {
 
 constexpr int kTile = 128;                 // tokens per tile, and rows per stream
 constexpr int kMmaThreads = 384;
-using Axis = MultiAxis<kMultiMmaRows, kTile, kTile, 13>;
+
+// A tile for both streams takes twice as long as one for one of them where the
+// softmax bounds both (head_dim 64), and no longer where the copies bound the second
+// (128).  Measured with the other weights: prompts of 1..448 queries over inputs of
+// 1..1500 with heads of 64, 219 us (equal weights 274); trees of 16..64 nodes with
+// heads of 128, 383 us (weights of two and one 486).  A beginning and end take as long
+// as 6 or 7 units (3 units: 261; 2: 466).
+template <int HD>
+using AxisOf = MultiAxis<kMultiMmaRows, HD == 64 ? kTile : kMultiMmaRows, kTile, HD == 64 ? 6 : 7>;
 
 // ---------------------------------------------------------------- tcgen05 ---
 __device__ __forceinline__ void tm_alloc(uint32_t dst, uint32_t cols) {
@@ -249,6 +257,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     multi_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const MultiParams p) {
     using M = Smem<HD>;
+    using Axis = AxisOf<HD>;
     constexpr uint32_t kIdescS = mma_idesc(kTile, false), kIdescO = mma_idesc(HD, true);
     extern __shared__ uint8_t smem_raw[];
     __shared__ Control ctl;
@@ -731,7 +740,7 @@ int multi_mma(const MultiParams &p, int dev, cudaStream_t st) {
     const int grid = min(host::sm_count(dev), kMultiMmaCtas);
     const cudaError_t e = host::launch_dependent(kernel, grid, kMmaThreads, Smem<HD>::BYTES, st, mk, mv, p);
     if (e != cudaSuccess) return pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
-    return launch_join<__nv_bfloat16, HD, Axis>(p, grid, st);
+    return launch_join<__nv_bfloat16, HD, AxisOf<HD>>(p, grid, st);
 }
 
 }  // namespace
