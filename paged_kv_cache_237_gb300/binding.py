@@ -396,20 +396,21 @@ def _decode_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, ma
     return _PreparedCall(_lib.pa_decode, out, operands, sizes, args, dev, keep)
 
 
-def _workspace(workspace, need, skip_counter_reset, dev, stream):
+def _workspace(workspace, need, skip_counter_reset, dev, stream, zeroed=True):
     """The caller's workspace, checked, or a zeroed one when one is needed: made
     on the stream that uses it, so that its zeros are there in time and its
     memory is not handed out again before the call is done with it."""
     if need and workspace is None:
+        make = torch.zeros if zeroed else torch.empty
         if stream is None:
-            return torch.zeros(need, dtype=torch.uint8, device=dev), True
+            return make(need, dtype=torch.uint8, device=dev), True
         if not isinstance(stream, torch.cuda.Stream):
             handle = int(getattr(stream, "cuda_stream", stream))
             # handle 0 is the default stream, but torch takes it for "no handle given"
             # and wraps a stream of its own pool, which nothing orders with the call
             stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
         with torch.cuda.stream(stream):
-            return torch.zeros(need, dtype=torch.uint8, device=dev), True
+            return make(need, dtype=torch.uint8, device=dev), True
     if workspace is not None:
         _check_cuda(workspace, "workspace", (torch.uint8,), dev)
     return workspace, skip_counter_reset
@@ -702,7 +703,8 @@ def _multi_call(tree, out, q, k_cache, v_cache, block_tables, context_lens, quer
         if tree_mask.dim() != 2 or tree_mask.shape[0] != T:
             raise ValueError("tree_mask must be [T, words]")
         words = tree_mask.shape[1]
-    workspace, _ = _workspace(workspace, pa_decode_tree_workspace_size(T, Hq, Hkv, hd), False, dev, stream)
+    workspace, _ = _workspace(workspace, pa_decode_tree_workspace_size(T, Hq, Hkv, hd), False, dev, stream,
+                              zeroed=False)
     args = _DecodeArgs(S, block_tables.shape[1], nb, _dtype_code(q.dtype), 0, max_context_len, _ptr(workspace),
                        workspace.numel() if workspace is not None else 0, status.ptr() if status is not None else None)
     operands = (q, k_cache, v_cache, block_tables, context_lens, query_start)

@@ -101,7 +101,8 @@ int decode_multi(void *out, const void *q, const void *k_cache, const void *v_ca
     p.num_blocks = a->num_blocks;
     p.width = a->max_blocks_per_seq;
     const long long table_cap = static_cast<long long>(a->max_blocks_per_seq) * block_size;
-    p.ctx_cap = static_cast<int>(a->max_context_len < table_cap ? a->max_context_len : table_cap);
+    const long long cap = a->max_context_len < table_cap ? a->max_context_len : table_cap;
+    p.ctx_cap = static_cast<int>(cap < INT_MAX - 1024 ? cap : INT_MAX - 1024);   // positions of a whole tile fit an int
     p.words = mask_words;
     p.see = see;
     p.slot_rows = lay.rows;

@@ -59,7 +59,7 @@ struct Shape {
     static constexpr int Q = 0, K = Q + R * HD, V = K + kTile * LDK, P = V + kTile * LDV, TOP = P + R * kTile;
     static constexpr int BYTES = (TOP + kWarps * R) * 4;
     static constexpr int CTAS = HD == 64 ? 3 : 2;      // per SM
-    using Axis = MultiAxis<R, R, kTile, 2>;
+    using Axis = MultiAxis<R, R, kTile, 1>;
 };
 
 template <int HD, int MT>
