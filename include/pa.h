@@ -542,8 +542,9 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_hea
  * args as for pa_decode: num_seqs, max_blocks_per_seq, num_blocks, dtype,
  * max_context_len (longer entries are clamped and flagged), dev_status, stream, and
  * a workspace of pa_decode_tree_workspace_size bytes (both calls), which needs no
- * zeros and follows the rule of one call at a time.  phase, simt, partition_size
- * and the fused write's pointers must be 0 (PA_ERR_UNSUPPORTED).  A sequence whose
+ * zeros and may be shared with pa_decode under the same rule of one call at a time
+ * (its first 256 bytes are left as they are).  phase, simt, partition_size and the
+ * fused write's pointers must be 0 (PA_ERR_UNSUPPORTED).  A sequence whose
  * rows of query_start run backwards or leave [0, num_tokens] has no queries
  * (flagged PA_STATUS_BAD_TREE); one with c_i > n_i in pa_decode_tree gets zero rows
  * (PA_STATUS_BAD_CONTEXT_LEN); a block id out of range reads as zeros (flagged).
@@ -574,7 +575,8 @@ size_t pa_decode_tree_workspace_size(int num_tokens, int num_q_heads, int num_kv
  * [num_tokens] (may be NULL) = n_i - c_i + depth, depth counted from 0.  Trees of
  * more than 64 * mask_words nodes are flagged (PA_STATUS_BAD_TREE): the nodes past
  * that see nothing.  A parent that is not an earlier node counts as none (flagged).
- * Rows of no sequence are left as they were. */
+ * Rows of no sequence are left as they were.  2^30 or more words of masks:
+ * PA_ERR_UNSUPPORTED. */
 int pa_build_tree(uint64_t *tree_mask, int32_t *positions, const int32_t *parents, const int32_t *query_start,
                   const int32_t *context_lens, int num_seqs, int num_tokens, int mask_words, int32_t *dev_status,
                   void *stream);

@@ -18,12 +18,12 @@ bool few_rows(const pa::MultiParams &p, int head_dim) {
     const long long rows = (static_cast<long long>(p.num_tokens) * p.group + p.num_seqs - 1) / p.num_seqs;
     const long long blocks = (rows + 15) / 16;
     return blocks == 1 ||
-           (blocks <= 6 && blocks * p.num_seqs * p.num_kv_heads * p.ctx_cap * (head_dim / 64) <= 1200000);
+           (blocks <= 6 && 1.0 * blocks * p.num_seqs * p.num_kv_heads * p.ctx_cap * (head_dim / 64) <= 1.2e6);
 }
 
 struct MultiLayout {
-    size_t acc, bytes;   // where the rows' sums start, and the workspace's size
-    int rows;            // rows per partial
+    size_t ml, acc, bytes;   // where the rows' maxima and sums start, where their values do, and the workspace's size
+    int rows;                // rows per partial
 };
 
 // num_tokens rows of `group` heads: an item has no more rows than that.
@@ -37,7 +37,8 @@ MultiLayout multi_layout(int num_tokens, int group, int head_dim, bool f32) {
         const size_t few = 2ull * pa::kMultiFewCtas * least(16);
         slots = slots > few ? slots : few;
     }
-    l.acc = align256(slots * 2 * sizeof(float));
+    l.ml = kWorkspaceHeader;   // pa_decode's counter stays as it is: the workspace may serve both
+    l.acc = l.ml + align256(slots * 2 * sizeof(float));
     l.bytes = l.acc + align256(slots * head_dim * sizeof(float));
     return l;
 }
@@ -89,7 +90,7 @@ int decode_multi(void *out, const void *q, const void *k_cache, const void *v_ca
     p.context_lens = context_lens;
     p.query_start = query_start;
     p.mask = reinterpret_cast<const unsigned long long *>(mask);
-    p.part_ml = static_cast<float *>(a->workspace);
+    p.part_ml = reinterpret_cast<float *>(static_cast<char *>(a->workspace) + lay.ml);
     p.part_acc = reinterpret_cast<float *>(static_cast<char *>(a->workspace) + lay.acc);
     p.status = a->dev_status;
     p.num_seqs = a->num_seqs;

@@ -178,3 +178,30 @@ def test_steps_share_a_workspace_and_follow_their_attributes(pa):
     assert_decode_close(c.decode(), cross.reference(0.02), torch.bfloat16)
     with pytest.raises(ValueError, match="workspace"):
         CrossDecodeStep(*args(cross), workspace=ws[:1000])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("width", [4, 30, 90])
+def test_a_workspace_serves_decode_steps_too(pa, width):
+    """pa_decode counts on the first bytes of its workspace from call to call."""
+    from paged_kv_cache_237_gb300.engine import DecodeStep, TreeDecodeStep
+    b = multi_ref.Batch("mask", [4000, 900, 30], [width, 30, 4], 8, 2, 128, 16, torch.bfloat16, 3)
+    T = int(b.start[-1])
+    q, k, v, tables = b.q.cuda(), b.k.cuda(), b.v.cuda(), torch.from_numpy(b.tables).cuda()
+    lens = torch.tensor(b.lens, dtype=torch.int32).cuda()
+    plain = DecodeStep(q[:3].contiguous(), k, v, tables, lens, 0.1, 4000)
+    want = plain.decode().clone()
+    need = max(pa.pa_decode_tree_workspace_size(T, 8, 2, 128), plain.workspace.numel())
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    ws[:256] = torch.arange(256, dtype=torch.uint8)
+    tree = TreeDecodeStep(q, k, v, tables, lens, torch.from_numpy(b.start).cuda(), 0.1, 4000,
+                          tree_mask=b.mask.cuda(), workspace=ws)
+    tree.decode()
+    assert torch.equal(ws[:256].cpu(), torch.arange(256, dtype=torch.uint8))
+    ws[:256] = 0
+    one = DecodeStep(q[:3].contiguous(), k, v, tables, lens, 0.1, 4000, workspace=ws)
+    for _ in range(3):
+        tree.decode()
+        one.out.zero_()
+        assert torch.equal(one.decode(), want)
+    assert_decode_close(tree.decode(), b.reference(0.1), torch.bfloat16)
