@@ -203,6 +203,8 @@ extern "C" int pa_build_tree(uint64_t *tree_mask, int32_t *positions, const int3
     PaTraceRange trace("pa_build_tree");
     if (num_seqs < 0 || num_tokens < 0 || mask_words < 1 || mask_words > PA_TREE_MAX_NODES / 64)
         return pa_fail(PA_ERR_INVALID_ARG, "pa_build_tree: bad sizes");
+    if (static_cast<long long>(num_tokens) * mask_words >= INT_MAX / 2)
+        return pa_fail(PA_ERR_UNSUPPORTED, "pa_build_tree: 2^30 or more words of masks");
     if (num_seqs == 0 || num_tokens == 0) return PA_OK;
     if (!tree_mask || !parents || !query_start || !context_lens)
         return pa_fail(PA_ERR_INVALID_ARG, "pa_build_tree: null pointer");

@@ -56,6 +56,12 @@ def test_bad_arguments_are_refused_on_the_host(pa):
     assert move(groups=0) == 0 and move(per=0) == 0
 
 
+def test_masks_past_32_bits_are_refused(pa):
+    L, F = pa._lib, FAKE
+    assert L.pa_build_tree(F, F, F, F, F, 1, 2**26, 16, None, None) == -2
+    assert L.pa_build_tree(F, F, F, F, F, 1, 2**31 - 1, 1, None, None) == -2
+
+
 # ------------------------------------------------------------- on the GPU ---
 
 def layout(news, padding=0):
