@@ -2,11 +2,11 @@
 //
 // The products run on mma.m16n8k8 with tf32 operands, each fp32 operand as the
 // sum of two of them (x = hi + lo, 11 bits each): a b ~ hi hi + hi lo + lo hi, off by
-// 3 * 2^-20 of |a b| at most and far less on average, so that sums of head_dim or of the tokens
-// keep about 22 bits; plain fp32 FMAs keep 24 and take eight times as long for 16
-// rows and more.  Sums are fp32: a tile's products with V start from zero in the
-// tensor core and are added to the row's sums by ordinary additions, since the
-// tensor core cuts its sums off where additions round.
+// 3 * 2^-20 of |a b| at most and far less on average, so that sums of head_dim or of the
+// tokens keep about 22 bits (results 4 to 6 * 10^-7 off in the 2-norm); plain fp32 FMAs keep
+// 24 and take eight times as long for 16 rows and more.  Sums are fp32: a tile's products
+// with V start from zero in the tensor core and are added to the row's sums by ordinary
+// additions, since the tensor core cuts its sums off where additions round.
 //
 // An item is R = 16 MT rows (query tokens x the heads of one KV head) against a
 // stretch of the sequence's cache in tiles of 64 tokens, a CTA of 4 warps:
@@ -15,10 +15,14 @@
 //            the products' operand is read;
 //   products each warp a quarter of head_dim, all rows and tokens (V is split once).
 // K and V come by cp.async: the next tile's K while this one's products run, its V
-// while the next scores do; two CTAs per SM fill each other's gaps.
-//   MT = 1: few rows per sequence, bound by the copies and their latency;
+// while the next scores do; two to four CTAs per SM fill each other's gaps.
+//   MT = 1: few rows per sequence, bound by the copies and their latency.  24
+//   multi-head sequences of up to 4000 tokens with 1 to 12 rows: 308 us, 4.8 TB/s
+//   (0.71 of the copy rate).
 //   MT = 2: many rows, bound by the tensor pipe (8 cycles an instruction, three for
-//   each 16 x 8 x 8 products: 98 TFLOP/s).  Four would need an SM for one CTA.
+//   each 16 x 8 x 8 products: 98 TFLOP/s, and rows that fill up to 16) and by what lies
+//   between its phases; 47 % of its cycles busy.  16 sequences of 100 to 1200 tokens, 24
+//   heads of 64, 1 to 300 queries: 257 us.  Four row tiles would need an SM for one CTA.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -52,13 +56,22 @@ __device__ __forceinline__ int a_place(int row, int col, int steps) {
     return (((row >> 4) * steps + (col >> 3)) * 32 + (row & 7) * 4 + (col & 3)) * 4 + ((col >> 2) & 1) * 2 + ((row >> 3) & 1);
 }
 
+// Place of 16 bytes c of token j in K's and V's tiles: so that an operand's 32 values lie in 32 banks (K's of 8 tokens and
+// 4 columns, V's of 4 tokens and 8 columns).
+template <int HD>
+__device__ __forceinline__ int k_place(int j, int c) { return j * HD + (c ^ (j & 7)) * 4; }
+template <int HD>
+__device__ __forceinline__ int v_place(int j, int c) { return j * HD + (c ^ (2 * (j & 3))) * 4; }
+
 template <int HD, int MT>
 struct Shape {
     static constexpr int R = 16 * MT;
-    static constexpr int LDK = HD + 4, LDV = HD + 8;   // banks 4 g + t for K's operand, 8 t + g for V's
-    static constexpr int Q = 0, K = Q + R * HD, V = K + kTile * LDK, P = V + kTile * LDV, TOP = P + R * kTile;
+    // Four of the k steps of few rows' Q stay in registers, which leaves room for a third CTA on the SM (24 multi-head
+    // sequences of up to 4000 tokens: 308 us, two CTAs 339; all of Q there spills, 478).
+    static constexpr int QB = HD == 128 && MT == 1 ? 1 : 0;
+    static constexpr int Q = 0, K = Q + R * (HD - 32 * QB), V = K + kTile * HD, P = V + kTile * HD, TOP = P + R * kTile;
     static constexpr int BYTES = (TOP + kWarps * R) * 4;
-    static constexpr int CTAS = HD == 64 ? 3 : 2;      // per SM
+    static constexpr int CTAS = HD == 64 ? 4 : (MT == 1 ? 3 : 2);   // per SM
     using Axis = MultiAxis<R, R, kTile, 1>;
 };
 
@@ -66,7 +79,7 @@ template <int HD, int MT>
 __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kernel(const MultiParams p) {
     using S = Shape<HD, MT>;
     using Axis = typename S::Axis;
-    constexpr int R = S::R, KS = HD / 8, NV = HD / 32;   // k steps of the scores; n tiles of a warp's columns
+    constexpr int R = S::R, KS = HD / 8 - 4 * S::QB, NV = HD / 32;   // k steps of the scores; n tiles of a warp's columns
     extern __shared__ __align__(16) float smem[];
     __shared__ MultiSpot s_spot;
     __shared__ int s_page[2][kTile / 16];
@@ -102,29 +115,42 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
             }
             return static_cast<int>((static_cast<long long>(b) * p.num_kv_heads + it.kvh) * p.block_size);
         };
-        const auto copy = [&](int t, const void *cache, float *dst, int ld) {
+        const auto copy = [&](int t, const void *cache, float *dst, bool is_k) {
             // a column of pieces per thread, every kThreads / (HD / 4)-th token
             const int c = tid % (HD / 4) * 4;
             const float *src = static_cast<const float *>(cache) + c;
 #pragma unroll 8
             for (int j = tid / (HD / 4); j < kTile; j += kThreads / (HD / 4)) {
                 const int row = s_page[t & 1][j >> page_shift];
+                float *at = dst + (is_k ? k_place<HD>(j, c / 4) : v_place<HD>(j, c / 4));
                 if (row >= 0 && t * kTile + j < seen)
-                    cp_async_16(smem_addr(dst + j * ld + c), src + (static_cast<long long>(row) + (j & (p.block_size - 1))) * HD);
+                    cp_async_16(smem_addr(at), src + (static_cast<long long>(row) + (j & (p.block_size - 1))) * HD);
                 else
-                    store4(dst + j * ld + c, make_float4(0.f, 0.f, 0.f, 0.f));
+                    store4(at, make_float4(0.f, 0.f, 0.f, 0.f));
             }
             cp_async_commit();
         };
         __syncthreads();   // the item before is done with the shared memory
         if (tid < 2 * pages) s_page[(it.tile0 + tid / pages) & 1][tid % pages] = page_row(it.tile0 + tid / pages, tid % pages);
         __syncthreads();
-        copy(it.tile0, p.k_cache, smem + S::K, S::LDK);
-        copy(it.tile0, p.v_cache, smem + S::V, S::LDV);
-        for (int i = tid; i < R * (HD / 4); i += kThreads) {
-            const int r = i / (HD / 4), c = i % (HD / 4) * 4;
+        copy(it.tile0, p.k_cache, smem + S::K, true);
+        copy(it.tile0, p.v_cache, smem + S::V, false);
+        float qr[S::QB ? 4 : 1][4];   // rows g, g + 8 at columns t4, t4 + 4 of the first k steps
+        if constexpr (S::QB > 0) {
+            const float *lo = static_cast<const float *>(p.q) + multi_row(p, it.s, it.kvh, R0 + min(g, rows - 1), HD) + t4;
+            const float *hi = static_cast<const float *>(p.q) + multi_row(p, it.s, it.kvh, R0 + min(g + 8, rows - 1), HD) + t4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                qr[i][0] = g < rows ? lo[8 * i] * p.scale_log2 : 0.f;
+                qr[i][1] = g + 8 < rows ? hi[8 * i] * p.scale_log2 : 0.f;
+                qr[i][2] = g < rows ? lo[8 * i + 4] * p.scale_log2 : 0.f;
+                qr[i][3] = g + 8 < rows ? hi[8 * i + 4] * p.scale_log2 : 0.f;
+            }
+        }
+        for (int i = tid; i < R * KS * 2; i += kThreads) {
+            const int r = i / (KS * 2), c = i % (KS * 2) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < rows) x = load4(static_cast<const float *>(p.q) + multi_row(p, it.s, it.kvh, R0 + r, HD) + c);
+            if (r < rows) x = load4(static_cast<const float *>(p.q) + multi_row(p, it.s, it.kvh, R0 + r, HD) + 32 * S::QB + c);
             float *at = smem + S::Q + a_place(r, c, KS);   // columns c .. c + 3 are four lanes apart
             at[0] = x.x * p.scale_log2;
             at[4] = x.y * p.scale_log2;
@@ -149,45 +175,62 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
             if (tid < pages) next_page = page_row(t + 2, tid);
             cp_async_wait_group<1>();   // K is there, V may be on its way
             __syncthreads();
-            // The three products of each tile in sums of their own: an instruction waits some 20 cycles for the one
-            // before it in its sum.
-            float sc[MT][2][4], lh[MT][2][4], hl[MT][2][4];
+            // The large products and the small ones in sums of their own: an instruction waits some 20 cycles for the
+            // one before it in its sum.
+            float sc[MT][2][4], low[MT][2][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[mt][n][e] = lh[mt][n][e] = hl[mt][n][e] = 0.f;
-#pragma unroll 4
-            for (int kk = 0; kk < KS; ++kk) {
-                uint32_t bh[2][2], bl[2][2];
+                    for (int e = 0; e < 4; ++e) sc[mt][n][e] = low[mt][n][e] = 0.f;
+            // Four k steps, which share their places in K's rows; Q's from registers or shared memory.
+            const auto steps = [&](int block, const float4 (&q)[MT][4]) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float *at = smem + S::K + (16 * warp + 8 * n + g) * S::LDK + 8 * kk + t4;
-                    split_tf32(at[0], bh[n][0], bl[n][0]);
-                    split_tf32(at[4], bh[n][1], bl[n][1]);
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t bh[2][2], bl[2][2];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const float *at = smem + S::K + 32 * block + t4;   // of the row's 16 bytes 8 block + 2 i, + 1
+                        const int row = 16 * warp + 8 * n + g;
+                        split_tf32(at[k_place<HD>(row, 2 * i)], bh[n][0], bl[n][0]);
+                        split_tf32(at[k_place<HD>(row, 2 * i + 1)], bh[n][1], bl[n][1]);
+                    }
+                    uint32_t ah[MT][4], al[MT][4];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        split_tf32(q[mt][i].x, ah[mt][0], al[mt][0]);
+                        split_tf32(q[mt][i].y, ah[mt][1], al[mt][1]);
+                        split_tf32(q[mt][i].z, ah[mt][2], al[mt][2]);
+                        split_tf32(q[mt][i].w, ah[mt][3], al[mt][3]);
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) mma_tf32(low[mt][n], al[mt], bh[n][0], bh[n][1]);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) mma_tf32(low[mt][n], ah[mt], bl[n][0], bl[n][1]);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) mma_tf32(sc[mt][n], ah[mt], bh[n][0], bh[n][1]);
                 }
-                uint32_t ah[MT][4], al[MT][4];
+            };
+            float4 q[MT][4];
+            if constexpr (S::QB > 0) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const float4 q = load4(smem + S::Q + ((mt * KS + kk) * 32 + lane) * 4);
-                    split_tf32(q.x, ah[mt][0], al[mt][0]);
-                    split_tf32(q.y, ah[mt][1], al[mt][1]);
-                    split_tf32(q.z, ah[mt][2], al[mt][2]);
-                    split_tf32(q.w, ah[mt][3], al[mt][3]);
-                }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) mma_tf32(lh[mt][n], al[mt], bh[n][0], bh[n][1]);
+                for (int i = 0; i < 4; ++i) q[0][i] = make_float4(qr[i][0], qr[i][1], qr[i][2], qr[i][3]);
+                steps(0, q);
+            }
+#pragma unroll 1
+            for (int block = 0; block < KS / 4; ++block) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) mma_tf32(hl[mt][n], ah[mt], bl[n][0], bl[n][1]);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) mma_tf32(sc[mt][n], ah[mt], bh[n][0], bh[n][1]);
+                    for (int i = 0; i < 4; ++i) q[mt][i] = load4(smem + S::Q + ((mt * KS + 4 * block + i) * 32 + lane) * 4);
+                steps(block + S::QB, q);
             }
             const bool masked = u0 + kTile > clear;
             bool odd = false;   // a score that is not a number
@@ -197,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        sc[mt][n][e] += lh[mt][n][e] + hl[mt][n][e];
+                        sc[mt][n][e] += low[mt][n][e];
                         odd |= sc[mt][n][e] != sc[mt][n][e];
                     }
             if (__any_sync(kFull, odd)) {
@@ -207,9 +250,10 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
                 for (int i = 0; i < MT * 8; ++i) {
                     const int row = 16 * (i >> 3) + g + 8 * ((i >> 1) & 1), tok = 16 * warp + 8 * ((i >> 2) & 1) + 2 * t4 + (i & 1);
                     plain = 0.f;
+                    const float *q = static_cast<const float *>(p.q) + multi_row(p, it.s, it.kvh, R0 + min(row, rows - 1), HD);
 #pragma unroll 1
                     for (int d = 0; d < HD; ++d)
-                        plain = fmaf(smem[S::Q + a_place(row, d, KS)], smem[S::K + tok * S::LDK + d], plain);
+                        plain = fmaf(row < rows ? q[d] * p.scale_log2 : 0.f, smem[S::K + k_place<HD>(tok, d / 4) + d % 4], plain);
 #pragma unroll
                     for (int j = 0; j < MT * 8; ++j)
                         if (j == i) sc[j >> 3][(j >> 2) & 1][j & 3] = plain;
@@ -241,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
                 }
             cp_async_wait_group<0>();   // V too
             __syncthreads();            // maxima are there, K is free
-            if (t + 1 < it.tile1) copy(t + 1, p.k_cache, smem + S::K, S::LDK);
+            if (t + 1 < it.tile1) copy(t + 1, p.k_cache, smem + S::K, true);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -293,9 +337,9 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
                     }
 #pragma unroll
                     for (int n = 0; n < NV; ++n) {
-                        const float *at = smem + S::V + (8 * kk + t4) * S::LDV + warp * (HD / 4) + 8 * n + g;
+                        const float *at = smem + S::V + v_place<HD>(8 * kk + t4, warp * (HD / 16) + 2 * n + (g >> 2)) + (g & 3);
                         split_tf32(at[0], bh[n][0], bl[n][0]);
-                        split_tf32(at[4 * S::LDV], bh[n][1], bl[n][1]);
+                        split_tf32(at[4 * HD], bh[n][1], bl[n][1]);
                     }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
@@ -326,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
                 if (!__syncthreads_or(!isfinite(size)) || again) break;
 #pragma unroll 1
                 for (int i = tid; i < kTile * HD; i += kThreads) {
-                    float *at = smem + S::V + i / HD * S::LDV + i % HD;
+                    float *at = smem + S::V + i;
                     if (!isfinite(*at)) *at = 0.f;
                 }
                 any_dirty = true;
@@ -339,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[mt][n][e] += acc[mt][n][e];
             if (tid < pages) s_page[t & 1][tid] = next_page;
-            if (t + 1 < it.tile1) copy(t + 1, p.v_cache, smem + S::V, S::LDV);
+            if (t + 1 < it.tile1) copy(t + 1, p.v_cache, smem + S::V, false);
         }
         // Sums over the tokens of all warps.
 #pragma unroll
