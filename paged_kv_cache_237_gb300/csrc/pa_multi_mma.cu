@@ -16,10 +16,27 @@
 //   S = Q K^T      128 x 128 x head_dim, Q and K in shared memory (128-byte swizzle)
 //   O += P V       128 x head_dim x 128, P in tensor memory over S, V in shared
 //                  memory as it is cached (tokens x head_dim, the MN-major form)
-// p enters as the sum of two bf16 parts (about 16 significant bits), as in
-// pa_decode, so two products per tile of V.  Row maxima are references that only
-// move when a tile's maximum is more than 2^8 above: then the row's O and sum are
-// rescaled (p stays below 2^8, and fp32 sums lose nothing by it).
+//
+// p enters as the sum of two bf16 parts (about 16 significant bits, as in pa_decode),
+// the second product only where it can be told from none: a warp whose 32 rows have no
+// weight above 1/32 of their row's sum so far stores the first part alone.  A weight
+// is then off by 2^-8 of itself at most and without bias, so a row is off, in the root
+// mean square, by 2^-8 sqrt(sum w^2) / sum w <= 2^-8 / sqrt(32) = 7 * 10^-4 of its values'
+// spread if all of its weight lies in 32 tokens, and by less the more tokens share it; a
+// result's own rounding to bf16 takes up to 4 * 10^-3.
+// Row maxima are references that only move when a tile's maximum is more than 2^8
+// above: then the row's O and sum are rescaled (p stays below 2^8, and fp32 sums lose
+// nothing by it).
+//
+// What bounds it: a step of both streams takes some 3700 cycles, of which the tensor
+// core works 2048 with one part of p and up to 3072 with two (head_dim 128); the rest is
+// the chain from a stream's scores to its weights (tensor memory read, maximum,
+// exponentials, tensor memory written).  Short contexts pay each item's beginning and
+// end besides (Q, results, 6 or 7 steps' time).  Measured: 8 x 2000 queries of 64 / 8
+// heads of 128 over 4,000..16,384 tokens 5.0 to 5.3 ms, 1.25 PFLOP/s; 7 contexts of up
+// to 131,072 with 25 drafted tokens each 550 us, 5.1 TB/s; 32 lognormal contexts with
+// trees of 16..64 nodes 382 us; prompts of 1..448 queries over 1..1500 tokens, 20 heads
+// of 64: 218 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -304,127 +321,127 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     MultiItem it;
 
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 8) {
-        // ------------------------------------------------------- copies ---
-        const int pages = kTile / p.block_size, box_bytes = p.block_size * 128;
-        const uint64_t once = l2_evict_first_policy(), again = l2_normal_policy();
-        Ring k, v;
-        bool ok = true;
-        while (ok && Axis::next(p, spot, left, it)) {
-            const int seen = Axis::seen(p, it.s, it.m), rows = it.s.c * p.group - it.m * kMultiMmaRows;
-            const int lag = rows > kTile ? 0 : 1;   // a V tile is needed after the next tile's K if the streams alternate
-            const uint64_t policy = Axis::row_blocks(p, it.s) > 1 ? again : once;
-            const int32_t *table = p.block_tables + static_cast<long long>(it.seq) * p.width;
-            // Lane l holds page l of a window of 32 pages, as a row of the cache view.
-            const auto page_row = [&](int page) {
-                const long long u = static_cast<long long>(page) * p.block_size;
-                if (u >= seen || page >= it.tile1 * pages) return p.total_rows;
-                const int b = table[page];
-                if (b < 0 || b >= p.num_blocks) {
-                    flag_status(p.status, PA_STATUS_BAD_BLOCK_ID);
-                    return p.total_rows;
-                }
-                return static_cast<int>((static_cast<long long>(b) * p.num_kv_heads + it.kvh) * p.block_size);
-            };
-            int window = it.tile0 * pages, now = page_row(window + lane), ahead = page_row(window + 32 + lane);
-            int row = p.total_rows, row_v = p.total_rows;
-            const auto issue = [&](const CUtensorMap *map, int r, uint32_t dst, uint64_t *full) {
-                if (lane == 0) mbar_arrive_expect_tx(smem_addr(full), M::TILE);
-                __syncwarp();
-                if (lane < pages)
-#pragma unroll
-                    for (int h = 0; h < HD / 64; ++h)
-                        tma_load_2d_hint(dst + h * M::SLAB + lane * box_bytes, map, h * 64, r, smem_addr(full), policy);
-            };
-            for (int t = it.tile0; t < it.tile1 + lag; ++t) {
-                if (lag) row_v = row;
-                if (t < it.tile1) {
-                    if (t * pages >= window + 32) {
-                        window += 32;
-                        now = ahead;
-                        ahead = page_row(window + 32 + lane);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 8) {
+            // ------------------------------------------------------- copies ---
+            const int pages = kTile / p.block_size, box_bytes = p.block_size * 128;
+            const uint64_t once = l2_evict_first_policy(), again = l2_normal_policy();
+            Ring k, v;
+            bool ok = true;
+            while (ok && Axis::next(p, spot, left, it)) {
+                const int seen = Axis::seen(p, it.s, it.m), rows = it.s.c * p.group - it.m * kMultiMmaRows;
+                const int lag = rows > kTile ? 0 : 1;   // a V tile is needed after the next tile's K if the streams alternate
+                const uint64_t policy = Axis::row_blocks(p, it.s) > 1 ? again : once;
+                const int32_t *table = p.block_tables + static_cast<long long>(it.seq) * p.width;
+                // Lane l holds page l of a window of 32 pages, as a row of the cache view.
+                const auto page_row = [&](int page) {
+                    const long long u = static_cast<long long>(page) * p.block_size;
+                    if (u >= seen || page >= it.tile1 * pages) return p.total_rows;
+                    const int b = table[page];
+                    if (b < 0 || b >= p.num_blocks) {
+                        flag_status(p.status, PA_STATUS_BAD_BLOCK_ID);
+                        return p.total_rows;
                     }
-                    row = __shfl_sync(kFull, now, (t * pages - window + lane) & 31);
-                    if (!(ok = await_warp(ctl, &ctl.k_empty[k.slot], k.phase ^ 1))) break;
-                    issue(&tmK, row, smem + M::K + k.slot * M::TILE, &ctl.k_full[k.slot]);
-                    k.advance<M::NK>();
-                }
-                if (!lag) row_v = row;
-                if (t >= it.tile0 + lag) {
-                    if (!(ok = await_warp(ctl, &ctl.v_empty[v.slot], v.phase ^ 1))) break;
-                    issue(&tmV, row_v, smem + M::V + v.slot * M::TILE, &ctl.v_full[v.slot]);
-                    v.advance<M::NV>();
-                }
-            }
-        }
-    } else if (warp == 9) {
-        // --------------------------------------------- matrix instructions ---
-        // The whole warp walks, on values that the compiler can see to be the same in all lanes.
-        const uint32_t tm = __shfl_sync(kFull, tmem, 0), lead = elect_one();
-        Ring k, v;
-        uint32_t items = 0, used = 0;   // used: the streams' phases of p_full, a bit each
-        bool ok = true;
-        while (ok && Axis::next(p, spot, left, it)) {
-            const bool both = __shfl_sync(kFull, it.s.c * p.group - it.m * kMultiMmaRows > kTile, 0);
-            const int tiles = __shfl_sync(kFull, it.tile1 - it.tile0, 0), count = both ? 2 * tiles : tiles;
-            if (!(ok = await_warp(ctl, &ctl.q_full, items++ & 1))) break;
-            tm_fence_after();
-            // Products of step q, then scores of step q + 2.  The loops are kept short: this warp's instructions come
-            // through the same cache as the softmax's many.
-#pragma unroll 1
-            for (int q = -2; q < count; ++q) {
-                const int s = q & 1;
-                const bool more = q + 2 < count, last = !both || s == 1;
-                if (q >= 0) {
-                    const uint32_t pt = tm + s * kTile, o = tm + 256 + s * kTile;
-                    const uint64_t b = smem_desc(smem + M::V + v.slot * M::TILE, M::SLAB);
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        // beside the weights: V for the first half, the next scores' K for the second
-                        if (!(ok = await_two(ctl, &ctl.p_full[s][half], (used >> s) & 1u,
-                                             half == 0 ? &ctl.v_full[v.slot] : &ctl.k_full[k.slot],
-                                             half == 0 ? v.phase : k.phase, half == 0 || more)))
-                            break;
-                        tm_fence_after();
-                        const uint4 off = *reinterpret_cast<const uint4 *>(ctl.one_part[s]);
-                        const uint64_t vb = b + half * (4 * 16 * 128 >> 4);
-                        const uint32_t pa = pt + half * 32;
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ts(o, pa + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, q >= 2 || half + kk > 0, lead);
-                        if (__any_sync(kFull, (off.x & off.y & off.z & off.w) == 0u))
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_ts_lanes(o, pa + 64 + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, off, lead);
-                    }
-                    if (!ok) break;
-                    used ^= 1u << s;
-                    if (!more) mma_commit(smem_addr(&ctl.o_full[s]), lead);
-                    if (last) {
-                        mma_commit(smem_addr(&ctl.v_empty[v.slot]), lead);
-                        v.advance<M::NV>();
-                    }
-                } else if (more && !(ok = await_warp(ctl, &ctl.k_full[k.slot], k.phase))) {
-                    break;
-                }
-                if (more) {
-                    uint64_t a = smem_desc(smem + (both ? s * M::TILE : 0), 16);
-                    uint64_t b = smem_desc(smem + M::K + k.slot * M::TILE, 16);
-#pragma unroll 1
-                    for (int slab = 0; slab < HD / 64; ++slab, a += M::SLAB >> 4, b += M::SLAB >> 4)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(tm + s * kTile, a + 2 * kk, b + 2 * kk, kIdescS, slab + kk > 0, lead);
-                    mma_commit(smem_addr(&ctl.s_full[s]), lead);
-                    if (last) {
-                        mma_commit(smem_addr(&ctl.k_empty[k.slot]), lead);
+                    return static_cast<int>((static_cast<long long>(b) * p.num_kv_heads + it.kvh) * p.block_size);
+                };
+                int window = it.tile0 * pages, now = page_row(window + lane), ahead = page_row(window + 32 + lane);
+                int row = p.total_rows, row_v = p.total_rows;
+                const auto issue = [&](const CUtensorMap *map, int r, uint32_t dst, uint64_t *full) {
+                    if (lane == 0) mbar_arrive_expect_tx(smem_addr(full), M::TILE);
+                    __syncwarp();
+                    if (lane < pages)
+    #pragma unroll
+                        for (int h = 0; h < HD / 64; ++h)
+                            tma_load_2d_hint(dst + h * M::SLAB + lane * box_bytes, map, h * 64, r, smem_addr(full), policy);
+                };
+                for (int t = it.tile0; t < it.tile1 + lag; ++t) {
+                    if (lag) row_v = row;
+                    if (t < it.tile1) {
+                        if (t * pages >= window + 32) {
+                            window += 32;
+                            now = ahead;
+                            ahead = page_row(window + 32 + lane);
+                        }
+                        row = __shfl_sync(kFull, now, (t * pages - window + lane) & 31);
+                        if (!(ok = await_warp(ctl, &ctl.k_empty[k.slot], k.phase ^ 1))) break;
+                        issue(&tmK, row, smem + M::K + k.slot * M::TILE, &ctl.k_full[k.slot]);
                         k.advance<M::NK>();
                     }
+                    if (!lag) row_v = row;
+                    if (t >= it.tile0 + lag) {
+                        if (!(ok = await_warp(ctl, &ctl.v_empty[v.slot], v.phase ^ 1))) break;
+                        issue(&tmV, row_v, smem + M::V + v.slot * M::TILE, &ctl.v_full[v.slot]);
+                        v.advance<M::NV>();
+                    }
+                }
+            }
+        } else if (warp == 9) {
+            // --------------------------------------------- matrix instructions ---
+            // The whole warp walks, on values that the compiler can see to be the same in all lanes.
+            const uint32_t tm = __shfl_sync(kFull, tmem, 0), lead = elect_one();
+            Ring k, v;
+            uint32_t items = 0, used = 0;   // used: the streams' phases of p_full, a bit each
+            bool ok = true;
+            while (ok && Axis::next(p, spot, left, it)) {
+                const bool both = __shfl_sync(kFull, it.s.c * p.group - it.m * kMultiMmaRows > kTile, 0);
+                const int tiles = __shfl_sync(kFull, it.tile1 - it.tile0, 0), count = both ? 2 * tiles : tiles;
+                if (!(ok = await_warp(ctl, &ctl.q_full, items++ & 1))) break;
+                tm_fence_after();
+                // Products of step q, then scores of step q + 2.  The loops are kept short: this warp's instructions come
+                // through the same cache as the softmax's many.
+    #pragma unroll 1
+                for (int q = -2; q < count; ++q) {
+                    const int s = q & 1;
+                    const bool more = q + 2 < count, last = !both || s == 1;
+                    if (q >= 0) {
+                        const uint32_t pt = tm + s * kTile, o = tm + 256 + s * kTile;
+                        const uint64_t b = smem_desc(smem + M::V + v.slot * M::TILE, M::SLAB);
+    #pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            // beside the weights: V for the first half, the next scores' K for the second
+                            if (!(ok = await_two(ctl, &ctl.p_full[s][half], (used >> s) & 1u,
+                                                 half == 0 ? &ctl.v_full[v.slot] : &ctl.k_full[k.slot],
+                                                 half == 0 ? v.phase : k.phase, half == 0 || more)))
+                                break;
+                            tm_fence_after();
+                            const uint4 off = *reinterpret_cast<const uint4 *>(ctl.one_part[s]);
+                            const uint64_t vb = b + half * (4 * 16 * 128 >> 4);
+                            const uint32_t pa = pt + half * 32;
+    #pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ts(o, pa + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, q >= 2 || half + kk > 0, lead);
+                            if (__any_sync(kFull, (off.x & off.y & off.z & off.w) == 0u))
+    #pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    mma_ts_lanes(o, pa + 64 + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, off, lead);
+                        }
+                        if (!ok) break;
+                        used ^= 1u << s;
+                        if (!more) mma_commit(smem_addr(&ctl.o_full[s]), lead);
+                        if (last) {
+                            mma_commit(smem_addr(&ctl.v_empty[v.slot]), lead);
+                            v.advance<M::NV>();
+                        }
+                    } else if (more && !(ok = await_warp(ctl, &ctl.k_full[k.slot], k.phase))) {
+                        break;
+                    }
+                    if (more) {
+                        uint64_t a = smem_desc(smem + (both ? s * M::TILE : 0), 16);
+                        uint64_t b = smem_desc(smem + M::K + k.slot * M::TILE, 16);
+    #pragma unroll 1
+                        for (int slab = 0; slab < HD / 64; ++slab, a += M::SLAB >> 4, b += M::SLAB >> 4)
+    #pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ss(tm + s * kTile, a + 2 * kk, b + 2 * kk, kIdescS, slab + kk > 0, lead);
+                        mma_commit(smem_addr(&ctl.s_full[s]), lead);
+                        if (last) {
+                            mma_commit(smem_addr(&ctl.k_empty[k.slot]), lead);
+                            k.advance<M::NK>();
+                        }
+                    }
                 }
             }
         }
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // ------------------------------------------------------- softmax ---

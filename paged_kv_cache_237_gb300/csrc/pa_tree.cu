@@ -3,7 +3,11 @@
 // cache rows to where the sequence goes on (include/pa.h states the formulas).
 //
 // All three are bound by latency (launch and two or three dependent loads) at
-// a decode step's sizes; the move is a byte mover like the cache write.
+// a decode step's sizes; the move is a byte mover like the cache write.  Measured:
+// masks and positions of 8 trees of 5..32 nodes 7.2 us, of 500 trees of up to 250
+// nodes 8.2 us (the host's part of a call is 7); accepted paths and moves of 4
+// sequences with the write of their rows before it, three launches: 13.5 us on the
+// GPU, 24 as calls; of 250 sequences 28.
 #include <cuda_runtime.h>
 
 #include <climits>
