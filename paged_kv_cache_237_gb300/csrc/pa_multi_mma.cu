@@ -612,11 +612,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 ++mine;
             }
             if (!ok) break;
-            // The item's end: all products are in, and both streams say what they have (through the free scores).
+            // The item's end: all products are in, and both streams say what they have, in tensor memory.  In other
+            // columns than the item before: a stream without steps in this item does not wait for the other one, which
+            // may still be reading there.
             if (mine > 0 && !(ok = await_warp(ctl, &ctl.o_full[s], ends++ & 1))) break;
             tm_fence_after();
+            const uint32_t sums_at = 2 * (item_no & 1);
             if (!both) {
-                tm_st2(ts, __float_as_uint(ref), __float_as_uint(sum));
+                tm_st2(ts + sums_at, __float_as_uint(ref), __float_as_uint(sum));
                 tm_wait_st();
             }
             arrive(&ctl.e_full);
@@ -627,8 +630,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 float f[2] = {1.f, 1.f}, top = ref, all = sum;
                 if (!both) {
                     float a[4];
-                    tm_ld2(tmem + lanes, a);
-                    tm_ld2(tmem + lanes + kTile, a + 2);
+                    tm_ld2(tmem + lanes + sums_at, a);
+                    tm_ld2(tmem + lanes + kTile + sums_at, a + 2);
                     tm_wait_ld();
                     top = fmaxf(a[0], a[2]);
                     const float at = top == -INFINITY ? 0.f : top;

@@ -401,3 +401,16 @@ def test_two_streams_with_workspaces_of_their_own(pa, dtype):
     torch.cuda.synchronize()
     for b, (_, args, _) in zip(batches, calls):
         assert_decode_close(args[0], b.reference(0.1), dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hd", [64, 128])
+def test_many_short_items_in_a_row(pa, hd):
+    """Items of one tile each, one behind the other in every CTA: whatever a stream of rows
+    leaves for the other one must last until it is read.  Bit-equal from call to call."""
+    rng = np.random.default_rng(hd)
+    lens = rng.integers(1, 129, 3000).tolist()
+    b = Batch("cross", lens, [20] * 3000, 2, 2, hd, 16, torch.bfloat16, 5)
+    out = check(pa, b, hd ** -0.5)
+    for _ in range(20):
+        assert torch.equal(b.on_gpu(pa, hd ** -0.5)[0], out)
