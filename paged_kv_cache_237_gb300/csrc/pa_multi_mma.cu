@@ -20,10 +20,12 @@
 // p enters as the sum of two bf16 parts (about 16 significant bits, as in pa_decode),
 // the second product only where it can be told from none: a warp whose 32 rows have no
 // weight above 1/32 of their row's sum so far stores the first part alone.  A weight
-// is then off by 2^-8 of itself at most and without bias, so a row is off, in the root
-// mean square, by 2^-8 sqrt(sum w^2) / sum w <= 2^-8 / sqrt(32) = 7 * 10^-4 of its values'
-// spread if all of its weight lies in 32 tokens, and by less the more tokens share it; a
-// result's own rounding to bf16 takes up to 4 * 10^-3.
+// is then off by 2^-8 of itself at most.  Weights that differ are off independently, so a
+// row is off, in the root mean square, by 2^-8 sqrt(sum w^2) / sum w <= 2^-8 / sqrt(32) =
+// 7 * 10^-4 of its values' spread if all of its weight lies in 32 tokens, and by less the
+// more tokens share it.  Weights that are alike share their error, and the row is off by
+// 2^-8 of its result at most, as much as by the result's own rounding to bf16 (sums of the
+// rounded weights would cancel that, for a fifth more instructions in the step).
 // Row maxima are references that only move when a tile's maximum is more than 2^8
 // above: then the row's O and sum are rescaled (p stays below 2^8, and fp32 sums lose
 // nothing by it).

@@ -414,3 +414,34 @@ def test_many_short_items_in_a_row(pa, hd):
     out = check(pa, b, hd ** -0.5)
     for _ in range(20):
         assert torch.equal(b.on_gpu(pa, hd ** -0.5)[0], out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hd", [64, 128])
+def test_weights_that_are_alike(pa, hd):
+    """One token above 4095 equal ones, whose weight e^-s is as far from a bf16 value as can be:
+    a row is off by its weights' rounding (2^-8 of itself) and its own (2^-8), no more."""
+    n = 4096
+    grid = torch.arange(128, 256, dtype=torch.float64) / 256                       # bf16 values of [0.5, 1)
+    s = grid[:, None] * (grid + 0.5)[None, :].to(torch.bfloat16).double()          # products are exact in fp32
+    w = torch.exp(-s)
+    off = ((w.to(torch.bfloat16).double() - w).abs() / w).flatten()
+    i, j = divmod(int(off.argmax()), 128)
+    assert off.max() > 0.95 * 2 ** -8
+    b = Batch("cross", [n], [300], 2, 2, hd, 16, torch.bfloat16, 9)
+    b.q.zero_()
+    b.q[..., 0] = grid[i].to(torch.bfloat16)
+    b.k.masked_fill_(~b.k.isnan(), 0.0)
+    b.k[int(b.tables[0, 0]), :, 0, 0] = (grid[j] + 0.5).to(torch.bfloat16)
+    v0 = float(b.v[int(b.tables[0, 0]), :, 0].abs().max())
+    out = b.on_gpu(pa, 1.0)[0].double().cpu()
+    q, first = b.q[:1].clone(), b.start.copy()
+    b.q, b.start, b.news = q, np.array([0, 1], np.int32), [1]                      # all rows are the same
+    want = b.reference(1.0)
+    # fp32: the sum of 4096 weights is off by 4096 * 2^-24 at most; a product's sums by 2^-22 of the largest partial sum at
+    # each of 256 steps, in two parts of p; the first token's weight is one of 4095 * 0.5 and off by 2^-8 itself.
+    t = torch.arange(n)
+    v = b.v[torch.from_numpy(b.tables[0]).long()[t // 16], :, t % 16].double()
+    slack = 2 * 2 ** -8 + 2 ** -16 + 4096 * 2 ** -24
+    floor = 512 * 2 ** -22 * 2 * float(v.cumsum(0).abs().max()) / 4095 + 2 ** -8 * v0 / 2000
+    assert ((out - want).abs() <= slack * want.abs() + floor).all()
