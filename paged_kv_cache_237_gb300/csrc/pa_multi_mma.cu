@@ -31,14 +31,14 @@
 // nothing by it).
 //
 // What bounds it: a step of both streams takes some 3700 cycles, of which the tensor
-// core works 2048 with one part of p and up to 3072 with two (head_dim 128); the rest is
-// the chain from a stream's scores to its weights (tensor memory read, maximum,
-// exponentials, tensor memory written).  Short contexts pay each item's beginning and
-// end besides (Q, results, 6 or 7 steps' time).  Measured: 8 x 2000 queries of 64 / 8
-// heads of 128 over 4,000..16,384 tokens 5.0 to 5.3 ms, 1.25 PFLOP/s; 7 contexts of up
-// to 131,072 with 25 drafted tokens each 550 us, 5.1 TB/s; 32 lognormal contexts with
-// trees of 16..64 nodes 382 us; prompts of 1..448 queries over 1..1500 tokens, 20 heads
-// of 64: 218 us.
+// core works 2048 with one part of p, and half as many again at most with two (head_dim
+// 128); the rest is the chain from a stream's scores to its weights: tensor memory read,
+// maximum, exponentials, tensor memory written, three barrier operations.  Short contexts pay
+// each item's beginning and end besides (Q, results, 6 or 7 steps' time).  Measured: 8 x 2000
+// queries of 64 / 8 heads of 128 over 4,000..16,384 tokens 5.0 to 5.3 ms, 1.25 PFLOP/s; 7
+// contexts of up to 131,072 with 25 drafted tokens each 550 us, 5.1 TB/s; 32 lognormal
+// contexts with trees of 16..64 nodes 382 us; prompts of 1..448 queries over 1..1500
+// tokens, 20 heads of 64: 218 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
