@@ -3,8 +3,9 @@
 // The products run on mma.m16n8k8 with tf32 operands, each fp32 operand as the
 // sum of two of them (x = hi + lo, 11 bits each): a b ~ hi hi + hi lo + lo hi, off by
 // 3 * 2^-20 of |a b| at most and far less on average, so that sums of head_dim or of the
-// tokens keep about 22 bits (results 4 to 6 * 10^-7 off in the 2-norm); plain fp32 FMAs keep
-// 24 and take eight times as long for 16 rows and more.  Sums are fp32: a tile's products
+// tokens keep about 22 bits (results 0.5 to 1.0 * 10^-6 off in the 2-norm, mostly by the tensor
+// core's cut sums; plain fp32 operations 0.1 to 0.5); plain fp32 FMAs keep 24 and take eight
+// times as long for 16 rows and more.  Sums are fp32: a tile's products
 // with V start from zero in the tensor core and are added to the row's sums by ordinary
 // additions, since the tensor core cuts its sums off where additions round.
 //
