@@ -533,10 +533,8 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_hea
  * not finite leaves its column of the row without a finite result (an infinity may come
  * out as NaN in PA_BF16, as in pa_decode).
  * Arithmetic: scores, maxima, sums and results are fp32.  PA_BF16: q, K and V enter
- * exactly, weights as two bf16 parts (16 bits), or as one (off by 2^-8 of itself at most)
- * where the batch has many rows per sequence and no weight of 32 rows and 64 or 128
- * tokens is above 1/32 of its row's sum so far.  PA_F32: q, K, V and weights as two
- * tf32 parts each, three of their four products (3 * 2^-20 of a product's size at most,
+ * exactly, weights as two bf16 parts (16 bits), whatever the batch.  PA_F32: q, K, V and
+ * weights as two tf32 parts each, three of their four products (3 * 2^-20 of a product's size at most,
  * far less on average).
  *
  * args as for pa_decode: num_seqs, max_blocks_per_seq, num_blocks, dtype,

@@ -17,28 +17,24 @@
 //   O += P V       128 x head_dim x 128, P in tensor memory over S, V in shared
 //                  memory as it is cached (tokens x head_dim, the MN-major form)
 //
-// p enters as the sum of two bf16 parts (about 16 significant bits, as in pa_decode),
-// the second product only where it can be told from none: a warp whose 32 rows have no
-// weight above 1/32 of their row's sum so far stores the first part alone.  A weight
-// is then off by 2^-8 of itself at most.  Weights that differ are off independently, so a
-// row is off, in the root mean square, by 2^-8 sqrt(sum w^2) / sum w <= 2^-8 / sqrt(32) =
-// 7 * 10^-4 of its values' spread if all of its weight lies in 32 tokens, and by less the
-// more tokens share it.  Weights that are alike share their error, and the row is off by
-// 2^-8 of its result at most, as much as by the result's own rounding to bf16 (sums of the
-// rounded weights would cancel that, for a fifth more instructions in the step).
+// p enters as the sum of two bf16 parts (about 16 significant bits), as in pa_decode and
+// in the pass for few rows: a sequence's result keeps the same bits whatever shares its
+// batch.  One part alone would take a third of the matrix work away (32 contexts with
+// trees 382 us, below; 8 x 2000 queries 4.9 ms) and leave a row off by up to 2^-8 where
+// its weights are alike, as much as the rounding of its result to bf16.
 // Row maxima are references that only move when a tile's maximum is more than 2^8
 // above: then the row's O and sum are rescaled (p stays below 2^8, and fp32 sums lose
 // nothing by it).
 //
-// What bounds it: a step of both streams takes some 3700 cycles, of which the tensor
-// core works 2048 with one part of p, and half as many again at most with two (head_dim
-// 128); the rest is the chain from a stream's scores to its weights: tensor memory read,
-// maximum, exponentials, tensor memory written, three barrier operations.  Short contexts pay
+// What bounds it: the chain from a stream's scores to its weights: tensor memory read,
+// maximum, exponentials and their parts, tensor memory written, three barrier operations.
+// The tensor core works three quarters of the time that the chain takes (head_dim 128).
+// Short contexts pay
 // each item's beginning and end besides (Q, results, 6 or 7 steps' time).  Measured: 8 x 2000
-// queries of 64 / 8 heads of 128 over 4,000..16,384 tokens 5.0 to 5.3 ms, 1.25 PFLOP/s; 7
-// contexts of up to 131,072 with 25 drafted tokens each 550 us, 5.1 TB/s; 32 lognormal
-// contexts with trees of 16..64 nodes 382 us; prompts of 1..448 queries over 1..1500
-// tokens, 20 heads of 64: 218 us.
+// queries of 64 / 8 heads of 128 over 4,000..16,384 tokens 5.9 to 6.0 ms, 1.1 PFLOP/s; 7
+// contexts of up to 131,072 with 25 drafted tokens each 656 us, 4.3 TB/s; 32 lognormal
+// contexts with trees of 16..64 nodes 429 us; prompts of 1..448 queries over 1..1500
+// tokens, 20 heads of 64: 208 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -134,15 +130,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(lead)
         : "memory");
 }
-// The same for the lanes (rows) whose bits in `off` are clear.
-__device__ __forceinline__ void mma_ts_lanes(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, const uint4 &off,
-                                             uint32_t lead) {
-    asm volatile(
-        "{\n\t.reg .pred p, l;\n\tsetp.eq.b32 p, 0, 0;\n\tsetp.ne.b32 l, %8, 0;\n\t"
-        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w), "r"(lead)
-        : "memory");
-}
 // Arrives at `bar` once every matrix instruction issued so far is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t lead) {
     asm volatile(
@@ -212,7 +199,6 @@ struct Smem {
 
 struct Control {
     uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], s_full[2], p_full[2][2], o_full[2], q_full, e_full;
-    alignas(16) uint32_t one_part[2][4];   // by stream and quarter of its rows: all ones if this step's p is one bf16 part
     struct {
         MultiSpot spot;
         long long left;
@@ -406,16 +392,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                                                  half == 0 ? v.phase : k.phase, half == 0 || more)))
                                 break;
                             tm_fence_after();
-                            const uint4 off = *reinterpret_cast<const uint4 *>(ctl.one_part[s]);
                             const uint64_t vb = b + half * (4 * 16 * 128 >> 4);
                             const uint32_t pa = pt + half * 32;
     #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 mma_ts(o, pa + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, q >= 2 || half + kk > 0, lead);
-                            if (__any_sync(kFull, (off.x & off.y & off.z & off.w) == 0u))
     #pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    mma_ts_lanes(o, pa + 64 + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, off, lead);
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ts(o, pa + 64 + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, true, lead);
                         }
                         if (!ok) break;
                         used ^= 1u << s;
@@ -570,33 +554,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         ref = now;
                     }
                     const float shift = ref == -INFINITY ? 0.f : -ref;
-                    // One part is enough where no weight of the warp's rows is above 1/32 of its row's sum so far.
-                    const bool two = __any_sync(kFull, r < rows && 31.f * ex2(best + shift) > sum);
-                    if (lane == 0) ctl.one_part[s][warp & 3] = two ? 0u : ~0u;
                     float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        uint32_t hi[16];
+                        uint32_t hi[16], lo[16];
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {
-                            float *a = x + g * 32 + 2 * c;
+                            const float *a = x + g * 32 + 2 * c;
                             const float2 y = fma2(make_float2(a[0], a[1]), make_float2(scale, scale), make_float2(shift, shift));
-                            a[0] = ex2(y.x);
-                            a[1] = ex2(y.y);
-                            part[c & 1] = add2(part[c & 1], make_float2(a[0], a[1]));
-                            hi[c] = bf16_pair(a[0], a[1]);
+                            const float2 w = make_float2(ex2(y.x), ex2(y.y));
+                            part[c & 1] = add2(part[c & 1], w);
+                            hi[c] = bf16_pair(w.x, w.y);
+                            const float2 d = fma2(make_float2(__uint_as_float(hi[c] << 16), __uint_as_float(hi[c] & 0xffff0000u)),
+                                                  make_float2(-1.f, -1.f), w);
+                            lo[c] = bf16_pair(d.x, d.y);
                         }
                         tm_st16(ts + g * 16, hi);
-                        if (two) {
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) {
-                                const float *a = x + g * 32 + 2 * c;
-                                const float2 d = fma2(make_float2(__uint_as_float(hi[c] << 16), __uint_as_float(hi[c] & 0xffff0000u)),
-                                                      make_float2(-1.f, -1.f), make_float2(a[0], a[1]));
-                                hi[c] = bf16_pair(d.x, d.y);
-                            }
-                            tm_st16(ts + 64 + g * 16, hi);
-                        }
+                        tm_st16(ts + 64 + g * 16, lo);
                         if (g == 1) {   // the products with the first 64 tokens may begin
                             tm_wait_st();
                             arrive(&ctl.p_full[s][0]);
@@ -606,7 +580,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     sum += both_parts.x + both_parts.y;
                     tm_wait_st();
                 } else {
-                    if (lane == 0) ctl.one_part[s][warp & 3] = ~0u;
                     arrive(&ctl.p_full[s][0]);
                 }
                 arrive(&ctl.p_full[s][1]);
