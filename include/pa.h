@@ -534,8 +534,10 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_hea
  * out as NaN in PA_BF16, as in pa_decode).
  * Arithmetic: scores, maxima, sums and results are fp32.  PA_BF16: q, K and V enter
  * exactly, weights as two bf16 parts (16 bits), whatever the batch.  PA_F32: q, K, V and
- * weights as two tf32 parts each, three of their four products (3 * 2^-20 of a product's size at most,
- * far less on average).
+ * weights as two tf32 parts each, three of their four products, off by 2^-21 of a
+ * product at most and to either side: results as far off as with fp32 operations.  Sums
+ * over the tokens are divided at their end, so that values near fp32's largest may
+ * overflow in them.
  *
  * args as for pa_decode: num_seqs, max_blocks_per_seq, num_blocks, dtype,
  * max_context_len (longer entries are clamped and flagged), dev_status, stream, and

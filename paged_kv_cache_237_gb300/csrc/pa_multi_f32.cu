@@ -1,13 +1,15 @@
 // pa_decode_tree and pa_decode_cross over fp32 caches, on tensor cores.
 //
 // The products run on mma.m16n8k8 with tf32 operands, each fp32 operand as the
-// sum of two of them (x = hi + lo, 11 bits each): a b ~ hi hi + hi lo + lo hi, off by
-// 3 * 2^-20 of |a b| at most and far less on average, so that sums of head_dim or of the
-// tokens keep about 22 bits (results 0.5 to 1.0 * 10^-6 off in the 2-norm, mostly by the tensor
-// core's cut sums; plain fp32 operations 0.1 to 0.5); plain fp32 FMAs keep 24 and take eight
-// times as long for 16 rows and more.  Sums are fp32: a tile's products
-// with V start from zero in the tensor core and are added to the row's sums by ordinary
-// additions, since the tensor core cuts its sums off where additions round.
+// sum of two of them (x = hi + lo, hi rounded to its 11 bits and lo cut to its own, so
+// that one bit of x is lost at most): a b ~ hi hi + hi lo + lo hi, off by 2^-21 of |a b| at
+// most, and to either side, so that sums average it out.  Sums are fp32 and rounded: the
+// tensor core cuts its sums off, so each product hi hi of 8 columns or tokens starts from
+// zero there and is added to its sum by ordinary additions (those with a lo, 2^-11 of it,
+// stay in the tensor core over a tile).  Against 64 bits, in the 2-norm: 1.1 * 10^-7 off
+// on small trees and on decoders' prompts (plain fp32 operations 1.5 and 3.9); with hi cut
+// and sums in the tensor core 5.1 and 5.2, for 308 us against 337 and 257 against 282; with the
+// fourth product too 1.1, for 396 and 345.  fp32 FMAs take 521 and 375.
 //
 // An item is R = 16 MT rows (query tokens x the heads of one KV head) against a
 // stretch of the sequence's cache in tiles of 64 tokens, a CTA of 4 warps:
@@ -18,12 +20,12 @@
 // K and V come by cp.async: the next tile's K while this one's products run, its V
 // while the next scores do; two to four CTAs per SM fill each other's gaps.
 //   MT = 1: few rows per sequence, bound by the copies and their latency.  24
-//   multi-head sequences of up to 4000 tokens with 1 to 12 rows: 308 us, 4.8 TB/s
-//   (0.71 of the copy rate).
+//   multi-head sequences of up to 4000 tokens with 1 to 12 rows: 337 us, 4.4 TB/s
+//   (0.65 of the copy rate).
 //   MT = 2: many rows, bound by the tensor pipe (8 cycles an instruction, three for
 //   each 16 x 8 x 8 products: 98 TFLOP/s, and rows that fill up to 16) and by what lies
-//   between its phases; 47 % of its cycles busy.  16 sequences of 100 to 1200 tokens, 24
-//   heads of 64, 1 to 300 queries: 257 us.  Four row tiles would need an SM for one CTA.
+//   between its phases; some 40 % of its cycles busy.  16 sequences of 100 to 1200 tokens, 24
+//   heads of 64, 1 to 300 queries: 282 us.  Four row tiles would need an SM for one CTA.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -37,9 +39,11 @@ constexpr int kTile = 64, kThreads = kWarps * 32;
 
 __device__ __forceinline__ float4 load4(const float *x) { return *reinterpret_cast<const float4 *>(x); }
 
-// x = hi + lo in tf32's 11 bits each (the rest of lo is dropped).  An infinity leaves a NaN in lo.
-__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
-    hi = __float_as_uint(x) & 0xffffe000u;
+// x = hi + lo in tf32's 11 bits each: hi to the nearest (half = kNearest) or cut off (half = 0), and what lo cannot hold is
+// dropped.  An infinity leaves a NaN in lo, and so does a rounding past the largest fp32.
+constexpr uint32_t kNearest = 0x1000u;
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo, uint32_t half = kNearest) {
+    hi = (__float_as_uint(x) + half) & 0xffffe000u;
     lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
 }
 
@@ -49,6 +53,21 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
         "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// d += x, two at once.
+__device__ __forceinline__ void add2(float *d, const float *x) {
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(d[0]), "+f"(d[1])
+        : "f"(x[0]), "f"(x[1]));
+}
+
+// The same with the sum rounded: the product starts from zero.
+__device__ __forceinline__ void mma_tf32_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    mma_tf32(x, a, b0, b1);
+    add2(d, x);
+    add2(d + 2, x + 2);
 }
 
 // Place of element (row, col) of a matrix of 16-row tiles in the A operand's order: a lane's four values of a tile's 8
@@ -68,7 +87,7 @@ template <int HD, int MT>
 struct Shape {
     static constexpr int R = 16 * MT;
     // Four of the k steps of few rows' Q stay in registers, which leaves room for a third CTA on the SM (24 multi-head
-    // sequences of up to 4000 tokens: 308 us, two CTAs 339; all of Q there spills, 478).
+    // sequences of up to 4000 tokens, with sums left in the tensor core: 308 us, two CTAs 339; all of Q there spills, 478).
     static constexpr int QB = HD == 128 && MT == 1 ? 1 : 0;
     static constexpr int Q = 0, K = Q + R * (HD - 32 * QB), V = K + kTile * HD, P = V + kTile * HD, TOP = P + R * kTile;
     static constexpr int BYTES = (TOP + kWarps * R) * 4;
@@ -216,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) mma_tf32(sc[mt][n], ah[mt], bh[n][0], bh[n][1]);
+                        for (int n = 0; n < 2; ++n) mma_tf32_add(sc[mt][n], ah[mt], bh[n][0], bh[n][1]);
                 }
             };
             float4 q[MT][4];
@@ -316,9 +335,11 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
             __syncthreads();            // P is there
             float acc[MT][NV][4], cross[MT][NV][4];
             // A value that is not finite spoils every row here, seen or not (and an infinity becomes a NaN): then the
-            // tile's products are taken once more without such values, and the item's end adds them where they are seen.
+            // tile's products are taken once more without such values, and the item's end adds them where they are seen.  (The
+            // second time V's parts are cut: a value that rounds past the largest fp32 is finite.)
+            uint32_t half = kNearest;
 #pragma unroll 1
-            for (bool again = false;; again = true) {
+            for (bool again = false;; again = true, half = 0u) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -339,8 +360,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
 #pragma unroll
                     for (int n = 0; n < NV; ++n) {
                         const float *at = smem + S::V + v_place<HD>(8 * kk + t4, warp * (HD / 16) + 2 * n + (g >> 2)) + (g & 3);
-                        split_tf32(at[0], bh[n][0], bl[n][0]);
-                        split_tf32(at[4 * HD], bh[n][1], bl[n][1]);
+                        split_tf32(at[0], bh[n][0], bl[n][0], half);
+                        split_tf32(at[4 * HD], bh[n][1], bl[n][1], half);
                     }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
@@ -349,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                        for (int n = 0; n < NV; ++n) mma_tf32(acc[mt][n], ah[mt], bh[n][0], bh[n][1]);
+                        for (int n = 0; n < NV; ++n) mma_tf32_add(acc[mt][n], ah[mt], bh[n][0], bh[n][1]);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll

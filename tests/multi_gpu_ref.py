@@ -7,15 +7,15 @@ import torch
 def attend(q, k, v, scale, see=None):
     """Of one sequence: q [c, Hq, hd], k and v [n, Hkv, hd], see [c, n] bool or None.
 
-    (out, spread, size): out [c, Hq, hd]; spread [c, Hq, hd] = sum w |v| / sum w; size [c, Hq] = the largest
-    scale * sum |q_d k_d| of a seen position.  Rows that see nothing are zero."""
+    (out, spread, size, total): out [c, Hq, hd]; spread [c, Hq, hd] = sum w |v| / sum w; size [c, Hq] = the largest
+    scale * sum |q_d k_d| of a seen position; total [c, Hq] = sum w over the largest w.  Rows that see nothing are zero."""
     c, Hq, hd = q.shape
     n, Hkv, _ = k.shape
     group = Hq // Hkv
     out, spread = (torch.zeros(c, Hq, hd, dtype=torch.float64, device=q.device) for _ in range(2))
-    size = torch.zeros(c, Hq, dtype=torch.float64, device=q.device)
+    size, weights = (torch.zeros(c, Hq, dtype=torch.float64, device=q.device) for _ in range(2))
     if n == 0 or c == 0:
-        return out, spread, size
+        return out, spread, size, weights
     for h in range(Hkv):
         rows = q[:, h * group:(h + 1) * group].double()
         kh, vh = k[:, h].double(), v[:, h].double()
@@ -30,7 +30,8 @@ def attend(q, k, v, scale, see=None):
         out[:, at] = torch.einsum("cgn,nd->cgd", e, vh) / total
         spread[:, at] = torch.einsum("cgn,nd->cgd", e, vh.abs()) / total
         size[:, at] = y.amax(-1)
-    return out, spread, size
+        weights[:, at] = e.sum(-1)
+    return out, spread, size, weights
 
 
 def batch(b, scale):
@@ -65,3 +66,14 @@ def bf16_bound(out, spread, size, n, hd):
     denominator; sums over n tokens, in n / 16 such steps."""
     weight = 2.0 ** -16 + 2.0 ** -21 + 2 * (hd / 8) * 2.0 ** -22 * size[..., None] + (n / 16 + 8) * 2.0 ** -22
     return 2.0 ** -8 * out.abs() + (1 + 2.0 ** -8) * weight * spread
+
+
+def f32_bound(out, spread, size, n, hd):
+    """How far an fp32 result may be off, elementwise.  A product in two tf32 parts a side: 2^-21 of itself (2^-22 for the
+    product of the small parts, 2^-23 for what each side's parts leave out).  Eight of them in the tensor core, each cut
+    off at 2^-23 of the largest: 2^-20 of their sizes' sum.  Sums of hd in hd / 8 rounded steps and one for scale * q:
+    2^-24 each.  Weights: e to the score's error, and 2^-22 for the exponential; in numerator and denominator.  Sums over
+    n tokens in n / 8 rounded steps, and eight for the joins."""
+    product = 2.0 ** -21 + 2.0 ** -20
+    weight = torch.expm1(size[..., None] * (product + (hd / 8 + 1) * 2.0 ** -24)) + 2.0 ** -22
+    return (2 * weight + product + (n / 8 + 8) * 2.0 ** -24) * spread + 2.0 ** -23 * out.abs()

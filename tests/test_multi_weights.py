@@ -30,7 +30,7 @@ def test_results_are_off_by_their_rounding_and_little_more(pa, kind, hd, most, H
     lens = [3000, 1, 129, 2000, 600]
     b = Batch(kind, lens, [most, 1, most, most // 2, most], Hq, Hkv, hd, 16, torch.bfloat16, most + hd)
     scale = hd ** -0.5
-    out, spread, size = multi_gpu_ref.batch(b, scale)
+    out, spread, size, _ = multi_gpu_ref.batch(b, scale)
     bound = multi_gpu_ref.bf16_bound(out, spread, size, max(lens), hd)
     got, flags = multi_gpu_ref.repeated(b, times).on_gpu(pa, scale)
     assert flags == 0
