@@ -529,9 +529,10 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_hea
  *
  * out = softmax over the seen t of scale * (q . K[t]), times V[t]; a row that sees
  * nothing (n_i = 0, an empty mask) is zero.  What a row does not see has weight
- * zero, whatever its cache slots hold (NaN included); a value that it sees and that is
- * not finite leaves its column of the row without a finite result (an infinity may come
- * out as NaN in PA_BF16, as in pa_decode).
+ * zero, whatever its cache slots hold (NaN included).  A value that it sees and that is
+ * not finite makes its column of the row what the formula gives: an infinity that
+ * infinity, infinities of both signs or a NaN a NaN (and an infinity whose weight is below
+ * 2^-100 of the row's largest may come out as a NaN).
  * Arithmetic: scores, maxima, sums and results are fp32.  PA_BF16: q, K and V enter
  * exactly, weights as two bf16 parts (16 bits), whatever the batch.  PA_F32: q, K, V and
  * weights as two tf32 parts each, three of their four products, off by 2^-21 of a

@@ -263,6 +263,32 @@ __device__ __forceinline__ bool clear_not_finite(uint4 &at) {
     return bad;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    uint32_t u;
+    memcpy(&u, &h, 4);
+    return u;
+}
+// Two weights w = hi + lo in bf16 parts (off by 2^-16 of themselves at most).  hi is cut off and lo is what is left and 2^-23 of w, so
+// that neither is below zero nor, with w above zero (and not within 2^10 of the smallest fp32), zero: an infinite value stays an infinity in
+// both products.  Rounded parts would be off by 2^-17 and make it a NaN.
+__device__ __forceinline__ void weight_parts(float2 w, uint32_t &hi, uint32_t &lo) {
+    constexpr float over = 1.f + 0x1p-23f;
+    hi = __byte_perm(__float_as_uint(w.x), __float_as_uint(w.y), 0x7632);
+    const float2 rest = fma2(w, make_float2(over, over),
+                             make_float2(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xffff0000u)));
+    lo = bf16_pair(rest.x, rest.y);
+}
+
 // Element offset of row R of KV head kvh's problem in q and out.
 __device__ __forceinline__ long long multi_row(const MultiParams &p, const MultiSeq &s, int kvh, int R, int hd) {
     const int tok = R / p.group;

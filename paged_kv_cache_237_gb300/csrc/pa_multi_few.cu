@@ -18,7 +18,6 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <cstring>
 
 #include "pa_multi.cuh"
 
@@ -215,12 +214,8 @@ __global__ void __launch_bounds__(kThreads, Ring<HD>::CTAS)
             uint32_t pa[4], pb[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x0 = pr[e >> 1][2 * (e & 1)], x1 = pr[e >> 1][2 * (e & 1) + 1];
-                const __nv_bfloat162 hi = __floats2bfloat162_rn(x0, x1);
-                const float2 hf = __bfloat1622float2(hi);
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(x0 - hf.x, x1 - hf.y);
-                memcpy(&pa[e], &hi, 4);
-                memcpy(&pb[e], &lo, 4);
+                const float *x = &pr[e >> 1][2 * (e & 1)];
+                weight_parts(make_float2(x[0], x[1]), pa[e], pb[e]);
             }
             if (__any_sync(kFull, alpha_lo != 1.f || alpha_hi != 1.f)) {
 #pragma unroll

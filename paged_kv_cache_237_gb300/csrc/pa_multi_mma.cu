@@ -156,15 +156,6 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     float2 d;
     asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
@@ -172,12 +163,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
-}
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    uint32_t u;
-    memcpy(&u, &h, 4);
-    return u;
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -564,10 +549,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                             const float2 y = fma2(make_float2(a[0], a[1]), make_float2(scale, scale), make_float2(shift, shift));
                             const float2 w = make_float2(ex2(y.x), ex2(y.y));
                             part[c & 1] = add2(part[c & 1], w);
-                            hi[c] = bf16_pair(w.x, w.y);
-                            const float2 d = fma2(make_float2(__uint_as_float(hi[c] << 16), __uint_as_float(hi[c] & 0xffff0000u)),
-                                                  make_float2(-1.f, -1.f), w);
-                            lo[c] = bf16_pair(d.x, d.y);
+                            weight_parts(w, hi[c], lo[c]);
                         }
                         tm_st16(ts + g * 16, hi);
                         tm_st16(ts + 64 + g * 16, lo);
