@@ -86,6 +86,13 @@ struct MultiAxis {
         return s.n - s.c + last + 1;
     }
 
+    // Tokens that every row of row block m sees (not above s.n; below zero where no row sees anything).
+    static __device__ __forceinline__ int clear(const MultiParams &p, const MultiSeq &s, int m) {
+        if (p.see == kSeeAll) return s.n;
+        if (p.see == kSeeMask || s.n == 0) return s.n - s.c;
+        return s.n - s.c + m * ROWS / p.group + 1;   // of a chain, up to its first row's
+    }
+
     // An item of a row that sees nothing still has a tile: it writes the zeros.
     static __device__ __forceinline__ int tiles(const MultiParams &p, const MultiSeq &s, int m) {
         const int t = static_cast<int>((seen(p, s, m) + static_cast<unsigned>(KT - 1)) / KT);

@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
     MultiItem it;
     while (Axis::next(p, spot, left, it)) {
         const int R0 = it.m * R, rows = min(R, it.s.c * p.group - R0);
-        const int seen = Axis::seen(p, it.s, it.m), base = it.s.n - it.s.c;
-        const int clear = p.see == kSeeAll ? it.s.n : base;   // every row sees every position before
+        const int seen = Axis::seen(p, it.s, it.m);
+        const int clear = Axis::clear(p, it.s, it.m);   // every row sees every position before
         const int32_t *table = p.block_tables + static_cast<long long>(it.seq) * p.width;
         // First row of page j of tile t in the cache view; -1 for none (zeros).
         const auto page_row = [&](int t, int j) {

@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(kThreads, Ring<HD>::CTAS)
     MultiItem it;
     while (Axis::next(p, spot, left, it)) {
         const int R0 = it.m * kRows, rows = min(kRows, it.s.c * p.group - R0);
-        const int seen = Axis::seen(p, it.s, it.m), base = it.s.n - it.s.c;
-        const int clear = p.see == kSeeAll ? it.s.n : base;   // every row sees every position before
+        const int seen = Axis::seen(p, it.s, it.m);
+        const int clear = Axis::clear(p, it.s, it.m);   // every row sees every position before
         const int first = it.tile0 * kWarps, last = min(it.tile1 * kWarps, (seen + kChunk - 1) / kChunk);
         const int my_n = last > first + warp ? (last - first - warp + kWarps - 1) / kWarps : 0;
         const int32_t *table = p.block_tables + static_cast<long long>(it.seq) * p.width;
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, Ring<HD>::CTAS)
             }
             if (any_dirty) {
                 const int tok = (R0 + r) / p.group;
-                for (int u = max(max(base, 0), first * kChunk); u < min(seen, last * kChunk); ++u) {
+                for (int u = max(max(clear, 0), first * kChunk); u < min(seen, last * kChunk); ++u) {
                     if (!multi_sees(p, it.s, tok, u)) continue;
                     const int b = table[u / p.block_size];
                     if (b < 0 || b >= p.num_blocks) continue;

@@ -446,8 +446,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const int rows = both ? min(kTile, total - s * kTile) : total;   // of this stream's tile
             const int row0 = R0 + (both ? s * kTile : 0);
             const int tok = min(row0 + r, it.s.c * p.group - 1) / p.group;
-            const int seen = Axis::seen(p, it.s, it.m), base = it.s.n - it.s.c;
-            const int clear = p.see == kSeeAll ? it.s.n : base;   // every row sees every position before
+            const int seen = Axis::seen(p, it.s, it.m);
+            const int clear = Axis::clear(p, it.s, it.m);   // every row sees every position before
             // Where this row lies in q and out.
             const long long row_at = multi_row(p, it.s, it.kvh, min(row0 + r, it.s.c * p.group - 1), HD);
             if (both || s == 0) {
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 16; ++c) o[c] = second ? fmaf(o1[c], f[1], o[c] * f[0]) : o[c] * f[0];
                     if (dirty && r < rows)
-                        for (int u = max(max(base, 0), it.tile0 * kTile); u < min(seen, it.tile1 * kTile); ++u) {
+                        for (int u = max(max(clear, 0), it.tile0 * kTile); u < min(seen, it.tile1 * kTile); ++u) {
                             if (!(multi_seen_bits(p, it.s, tok, u) & 1u)) continue;
                             const int b = p.block_tables[static_cast<long long>(it.seq) * p.width + u / p.block_size];
                             if (b < 0 || b >= p.num_blocks) continue;
