@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
     extern __shared__ __align__(16) float smem[];
     __shared__ MultiSpot s_spot;
     __shared__ int s_page[2][kTile / 16];
+    __shared__ int s_odd[2];   // first tile of an item with values that are not finite, and the one behind the last
     griddep_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     float *const s_top = smem + S::TOP;
@@ -151,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
             cp_async_commit();
         };
         __syncthreads();   // the item before is done with the shared memory
+        if (tid == 0) s_odd[0] = it.tile1, s_odd[1] = 0;
         if (tid < 2 * pages) s_page[(it.tile0 + tid / pages) & 1][tid % pages] = page_row(it.tile0 + tid / pages, tid % pages);
         __syncthreads();
         copy(it.tile0, p.k_cache, smem + S::K, true);
@@ -181,7 +183,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
         // This lane's rows: 16 mt + g + 8 h.
         float m[MT][2], l[MT][2];
         float o[MT][NV][4];
-        bool any_dirty = false;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             m[mt][0] = m[mt][1] = -INFINITY;
@@ -395,7 +396,10 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
                     float *at = smem + S::V + i;
                     if (!isfinite(*at)) *at = 0.f;
                 }
-                any_dirty = true;
+                if (tid == 0) {
+                    s_odd[0] = min(s_odd[0], t);
+                    s_odd[1] = t + 1;
+                }
                 __syncthreads();
             }
 #pragma unroll
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
                 if (t4 == 0) s_top[warp * R + 16 * mt + g + 8 * h] = x;
             }
         __syncthreads();
-        const bool whole = it.whole();
+        const bool whole = it.whole(), any_odd = s_odd[1] > 0;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -433,9 +437,9 @@ __global__ void __launch_bounds__(kThreads, Shape<HD, MT>::CTAS) multi_f32_kerne
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     float2 x = make_float2(o[mt][n][2 * h] * inv, o[mt][n][2 * h + 1] * inv);
-                    if (any_dirty) {
+                    if (any_odd) {
                         const int tq = (R0 + r) / p.group;
-                        for (int u = it.tile0 * kTile; u < min(seen, it.tile1 * kTile); ++u) {
+                        for (int u = s_odd[0] * kTile; u < min(seen, s_odd[1] * kTile); ++u) {
                             const int b = table[u / p.block_size];
                             if (b < 0 || b >= p.num_blocks || !multi_sees(p, it.s, tq, u)) continue;
                             const float *v = static_cast<const float *>(p.v_cache) +

@@ -60,9 +60,11 @@ def test_values_that_are_not_finite_reach_the_rows_behind_them(pa, dtype, Hq, Hk
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("Hq,Hkv", [(16, 16), (32, 8)])
-def test_one_infinity_does_not_cost_more_than_the_chunk(pa, Hq, Hkv):
-    """Rows are mended at the end of their item, of the tokens that some of them do not see: not of the whole chunk."""
-    b = Batch("chain", [4000], [4000], Hq, Hkv, 128, 16, torch.bfloat16, 1)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_infinity_does_not_cost_more_than_the_chunk(pa, Hq, Hkv, dtype):
+    """Rows are mended at the end of their item, of the tokens that some of them do not see (fp32: of the tiles that hold such
+    values): not of the whole chunk."""
+    b = Batch("chain", [4000], [4000], Hq, Hkv, 128, 16, dtype, 1)
     args = [torch.empty_like(b.q).cuda(), b.q.cuda(), b.k.cuda(), b.v.cuda(), torch.from_numpy(b.tables).cuda(),
             torch.tensor(b.lens, dtype=torch.int32).cuda(), torch.from_numpy(b.start).cuda(), 0.1]
     ws = torch.empty(pa.pa_decode_tree_workspace_size(4000, Hq, Hkv, 128), dtype=torch.uint8, device="cuda")
