@@ -157,6 +157,11 @@ typedef struct pa_decode_args {
                                counter is zero, i.e. after any completed call
                                on this workspace, or when the caller zeroed its
                                first 8 bytes. */
+    int max_query_len;      /* pa_decode_tree and pa_decode_cross (others do not
+                               look at it): host upper bound of a sequence's
+                               queries, 0 for unknown.  It decides which kernels
+                               run, never what they compute: with it, a batch of
+                               short and long ones runs as both need. */
 } pa_decode_args;
 
 #define PA_PHASE_ALL 0
@@ -541,7 +546,9 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_hea
  * overflow in them.
  *
  * args as for pa_decode: num_seqs, max_blocks_per_seq, num_blocks, dtype,
- * max_context_len (longer entries are clamped and flagged), dev_status, stream, and
+ * max_context_len (longer entries are clamped and flagged), max_query_len (worth giving
+ * wherever sequences differ in their queries or q has padding: without it the kernels are
+ * picked by num_tokens / num_seqs), dev_status, stream, and
  * a workspace of pa_decode_tree_workspace_size bytes (both calls), which needs no
  * zeros and may be shared with pa_decode under the same rule of one call at a time
  * (its first 256 bytes are left as they are).  phase, simt, partition_size and the

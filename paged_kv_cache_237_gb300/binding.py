@@ -64,6 +64,7 @@ class _DecodeArgs(ctypes.Structure):
         ("slot_mapping", ctypes.c_void_p),
         ("simt", ctypes.c_int),
         ("skip_counter_reset", ctypes.c_int),
+        ("max_query_len", ctypes.c_int),
     ]
 
 
@@ -651,8 +652,9 @@ def pa_decode_tree_workspace_size(num_tokens: int, num_q_heads: int, num_kv_head
 
 def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                    block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor, scale: float, *,
-                   max_context_len: int, tree_mask: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                   status: DeviceStatus | None = None, stream=None) -> torch.Tensor:
+                   max_context_len: int, max_query_len: int = 0, tree_mask: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, status: DeviceStatus | None = None,
+                   stream=None) -> torch.Tensor:
     """Attention of drafted tokens over the paged cache; writes ``out``
     [T, Hq, hd] and returns it.
 
@@ -664,25 +666,29 @@ def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_
     the last sequence's are left as they were.  The workspace takes
     ``pa_decode_tree_workspace_size`` bytes, whatever the contexts; the other
     arguments are those of ``pa_decode``.
+
+    max_query_len, an upper bound of a sequence's rows (0: unknown), decides which
+    kernels run, never what they compute: give it where sequences differ in
+    their rows or q has padding.
     """
     return _multi_call(True, out, q, k_cache, v_cache, block_tables, context_lens, query_start, tree_mask, scale,
-                       max_context_len, workspace, status, stream)(stream)
+                       max_context_len, workspace, status, stream, max_query_len)(stream)
 
 
 def pa_decode_cross(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                     block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor, scale: float,
-                    *, max_context_len: int, workspace: torch.Tensor | None = None,
+                    *, max_context_len: int, max_query_len: int = 0, workspace: torch.Tensor | None = None,
                     status: DeviceStatus | None = None, stream=None) -> torch.Tensor:
     """Attention of any number of queries per request over the paged states of
     another sequence (an encoder's): every row of q [T, Hq, hd] from
     query_start[i] on sees all context_lens[i] tokens of block_tables[i].  The
     arguments are those of ``pa_decode_tree``."""
     return _multi_call(False, out, q, k_cache, v_cache, block_tables, context_lens, query_start, None, scale,
-                       max_context_len, workspace, status, stream)(stream)
+                       max_context_len, workspace, status, stream, max_query_len)(stream)
 
 
 def _multi_call(tree, out, q, k_cache, v_cache, block_tables, context_lens, query_start, tree_mask, scale,
-                max_context_len, workspace, status, stream=None) -> _PreparedCall:
+                max_context_len, workspace, status, stream=None, max_query_len=0) -> _PreparedCall:
     """The checks and arguments of pa_decode_tree and pa_decode_cross."""
     _check_cuda(q, "q", (torch.float32, torch.bfloat16))
     dev = q.device
@@ -706,7 +712,8 @@ def _multi_call(tree, out, q, k_cache, v_cache, block_tables, context_lens, quer
     workspace, _ = _workspace(workspace, pa_decode_tree_workspace_size(T, Hq, Hkv, hd), False, dev, stream,
                               zeroed=False)
     args = _DecodeArgs(S, block_tables.shape[1], nb, _dtype_code(q.dtype), 0, max_context_len, _ptr(workspace),
-                       workspace.numel() if workspace is not None else 0, status.ptr() if status is not None else None)
+                       workspace.numel() if workspace is not None else 0, status.ptr() if status is not None else None,
+                       max_query_len=max_query_len)
     operands = (q, k_cache, v_cache, block_tables, context_lens, query_start)
     sizes = [Hq, Hkv, hd, bs, float(scale), T]
     keep = (workspace, status, tree_mask, *operands)

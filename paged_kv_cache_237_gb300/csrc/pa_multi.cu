@@ -7,18 +7,57 @@ namespace {
 
 using namespace pa::host;
 
-// Which bf16 pass a batch takes, by what the host knows of it: the average rows per
-// sequence and KV head, in blocks of 16 (the few-rows pass reads K and V once per
-// block, the tcgen05 pass once per 256 rows), and the longest context.  Measured, few
-// rows against tcgen05 (us): 32 sequences of 2000..4000 tokens, 8 KV heads of 128:
+// Up to how many rows per sequence and KV head the pass for few rows is the faster one,
+// in blocks of 16, by what the host knows.  bf16: the few-rows pass reads K and V once per
+// block, the tcgen05 pass once per 256 rows; by blocks and the longest context.  Measured,
+// few rows against tcgen05 (us): 32 sequences of 2000..4000 tokens, 8 KV heads of 128:
 // 16 rows 87 / 100, 24 rows 140 / 100; 64 sequences of 350..700 tokens: 16 rows
 // 43 / 68, 32 rows 68 / 68, 48 rows 85 / 71 (heads of 64: 51 / 59, 64 rows 63 / 59);
 // 8 sequences of 450..900: 64 rows 32 / 35, 96 rows 36 / 36.
-bool few_rows(const pa::MultiParams &p, int head_dim) {
-    const long long rows = (static_cast<long long>(p.num_tokens) * p.group + p.num_seqs - 1) / p.num_seqs;
-    const long long blocks = (rows + 15) / 16;
-    return blocks == 1 ||
-           (blocks <= 6 && 1.0 * blocks * p.num_seqs * p.num_kv_heads * p.ctx_cap * (head_dim / 64) <= 1.2e6);
+// fp32: items of 16 against 32 rows, 32 sequences of 2000..4000 tokens, 8 KV heads of 128:
+// 16 rows 189 / 286, 24 rows 337 / 286 (sums left in the tensor core).
+constexpr int kFewBlocks = 6;
+int few_blocks(const pa::MultiParams &p, int head_dim, bool f32) {
+    if (f32) return 1;
+    int blocks = 1;
+    while (blocks < kFewBlocks && 1.0 * (blocks + 1) * p.num_seqs * p.num_kv_heads * p.ctx_cap * (head_dim / 64) <= 1.2e6)
+        ++blocks;
+    return blocks;
+}
+
+// The passes of a batch.  One, by the average rows, where no sequence can have many more
+// or the caller gave no bound on that (max_query_len 0).  Where one may have more than
+// kFewBlocks blocks and twice the average, the sequences of few rows run in one pass and
+// the others in another, if both are work enough (blocks of 16 rows x tokens x heads) to pay
+// for two more launches; else in one, by which of them are more.  Measured, all in the
+// few-rows pass / all in the tcgen05 pass / in both (us), a chunk beside requests of one
+// token with contexts of 200 to 1500: 127 and a chunk of 1500 over 8000, 32 heads of 128:
+// 1230 / 1011 / 530, fp32 5390 / 5280 / 4690; 127 and 600 over 1500, 32 / 8 heads: 231 /
+// 239 / 162, fp32 607 / 671 / 562; 16 heads of 64: 124 / 212 / 137; 7 and 600, 32 / 8
+// heads: 202 / 73 / 89; 127 and 1200, 4 / 1 heads: 222 / 69 / 83.
+int launch_passes(pa::MultiParams p, int head_dim, int max_query_len, bool f32, int dev, cudaStream_t st) {
+    const auto pass = [&](bool few) {
+        if (f32) return pa::launch_multi_f32(p, head_dim, few, dev, st);
+        return few ? pa::launch_multi_few(p, head_dim, dev, st) : pa::launch_multi_mma(p, head_dim, dev, st);
+    };
+    p.queries_above = 0;
+    p.queries_most = INT_MAX;
+    // rows behind the last sequence are none of the batch's
+    long long queries = p.num_tokens, most_queries = max_query_len < p.num_tokens ? max_query_len : p.num_tokens;
+    if (max_query_len > 0 && queries > most_queries * p.num_seqs) queries = most_queries * p.num_seqs;
+    const long long rows = (queries * p.group + p.num_seqs - 1) / p.num_seqs, longest = most_queries * p.group;
+    const int most = 16 * few_blocks(p, head_dim, f32);
+    if (longest <= 16 * kFewBlocks || longest <= 2 * rows) return pass(rows <= most);
+    const double block = 1.0 * p.num_kv_heads * p.ctx_cap * (head_dim / 64);
+    if (longest / 16 * block < 1.5e6 || p.num_seqs * block < 0.9e6) return pass(rows <= most && longest <= 16ll * p.num_seqs);
+    if (most >= p.group) {
+        p.queries_most = most / p.group;
+        const int rc = pass(true);
+        if (rc != PA_OK) return rc;
+        p.queries_above = p.queries_most;
+        p.queries_most = INT_MAX;
+    }
+    return pass(false);
 }
 
 struct MultiLayout {
@@ -60,9 +99,9 @@ int decode_multi(void *out, const void *q, const void *k_cache, const void *v_ca
     if (a->phase != PA_PHASE_ALL || a->simt || a->k_new || a->v_new || a->slot_mapping || a->partition_size)
         return pa_fail(PA_ERR_UNSUPPORTED,
                        "pa_decode_tree/cross: phase, simt, k_new, v_new, slot_mapping and partition_size must be 0");
-    if (a->num_blocks <= 0 || a->max_blocks_per_seq <= 0 || a->max_context_len < 0)
+    if (a->num_blocks <= 0 || a->max_blocks_per_seq <= 0 || a->max_context_len < 0 || a->max_query_len < 0)
         return pa_fail(PA_ERR_INVALID_ARG,
-                       "pa_decode_tree/cross: bad num_blocks, max_blocks_per_seq or max_context_len");
+                       "pa_decode_tree/cross: bad num_blocks, max_blocks_per_seq, max_context_len or max_query_len");
     if (a->num_seqs == 0 || num_tokens == 0) return PA_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start)
         return pa_fail(PA_ERR_INVALID_ARG, "pa_decode_tree/cross: null tensor pointer");
@@ -113,9 +152,7 @@ int decode_multi(void *out, const void *q, const void *k_cache, const void *v_ca
     if (cudaGetDevice(&dev) != cudaSuccess) return pa_fail(PA_ERR_CUDA, "pa_decode_tree/cross: no CUDA device");
     if (sm_count(dev) <= 0) return pa_fail(PA_ERR_CUDA, "pa_decode_tree/cross: cannot query the SM count");
     const cudaStream_t st = static_cast<cudaStream_t>(a->stream);
-    if (a->dtype == PA_F32) return pa::launch_multi_f32(p, head_dim, dev, st);
-    const bool few = few_rows(p, head_dim);
-    return few ? pa::launch_multi_few(p, head_dim, dev, st) : pa::launch_multi_mma(p, head_dim, dev, st);
+    return launch_passes(p, head_dim, a->max_query_len, a->dtype == PA_F32, dev, st);
 }
 
 }  // namespace

@@ -32,6 +32,7 @@ struct MultiParams {
     int32_t *status;
     int num_seqs, num_tokens, num_q_heads, num_kv_heads, group;
     int block_size, num_blocks, width, ctx_cap, words, see, slot_rows, total_rows;
+    int queries_above, queries_most;  // the pass' sequences: those of more queries than the one and not more than the other
     float scale_log2;
 };
 
@@ -49,6 +50,7 @@ __device__ __forceinline__ MultiSeq multi_seq(const MultiParams &p, int i, int &
         flags |= PA_STATUS_BAD_TREE;
         s.c = s.start = 0;
     }
+    if (s.c <= p.queries_above || s.c > p.queries_most) s.c = 0;   // another pass takes them
     if (p.see != kSeeAll && s.c > s.n) {   // queries whose rows the cache does not hold see nothing
         flags |= PA_STATUS_BAD_CONTEXT_LEN;
         s.n = 0;
@@ -296,6 +298,13 @@ __device__ __forceinline__ void weight_parts(float2 w, uint32_t &hi, uint32_t &l
     lo = bf16_pair(rest.x, rest.y);
 }
 
+// For tiles that several row blocks read, one after the other.
+__device__ __forceinline__ uint64_t l2_normal_policy() {
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+
 // Element offset of row R of KV head kvh's problem in q and out.
 __device__ __forceinline__ long long multi_row(const MultiParams &p, const MultiSeq &s, int kvh, int R, int hd) {
     const int tok = R / p.group;
@@ -418,7 +427,7 @@ int launch_join(const MultiParams &p, int pass_grid, cudaStream_t st) {
     return e == cudaSuccess ? PA_OK : pa_fail(PA_ERR_CUDA, cudaGetErrorString(e));
 }
 
-int launch_multi_f32(const MultiParams &p, int head_dim, int dev, cudaStream_t st);   // fp32
+int launch_multi_f32(const MultiParams &p, int head_dim, bool few, int dev, cudaStream_t st);   // fp32, items of 16 or 32 rows
 int launch_multi_mma(const MultiParams &p, int head_dim, int dev, cudaStream_t st);    // bf16
 int launch_multi_few(const MultiParams &p, int head_dim, int dev, cudaStream_t st);    // bf16, few rows per sequence
 

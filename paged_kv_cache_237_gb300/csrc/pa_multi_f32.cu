@@ -473,10 +473,7 @@ int multi_f32(const MultiParams &params, int dev, cudaStream_t st) {
 
 }  // namespace
 
-int launch_multi_f32(const MultiParams &p, int head_dim, int dev, cudaStream_t st) {
-    // By the batch's average rows per sequence and KV head (all that the host knows): measured on 32 sequences of
-    // 2000..4000 tokens, 8 KV heads of 128, 16 against 32 rows an item: 16 rows 189 / 286 us, 24 rows 337 / 286.
-    const bool few = static_cast<long long>(p.num_tokens) * p.group <= 16ll * p.num_seqs;
+int launch_multi_f32(const MultiParams &p, int head_dim, bool few, int dev, cudaStream_t st) {
     if (head_dim == 128) return few ? multi_f32<128, 1>(p, dev, st) : multi_f32<128, 2>(p, dev, st);
     return few ? multi_f32<64, 1>(p, dev, st) : multi_f32<64, 2>(p, dev, st);
 }

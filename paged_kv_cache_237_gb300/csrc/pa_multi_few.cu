@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, Ring<HD>::CTAS)
     loc.find(p, unit, &s_spot);
     __syncthreads();
     MultiSpot spot = s_spot;
-    const uint64_t once = l2_evict_first_policy();
+    const uint64_t once = l2_evict_first_policy(), again = l2_normal_policy();
     uint32_t n_issued = 0, n_done = 0;
     bool failed = false;
 
@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, Ring<HD>::CTAS)
         const int clear = Axis::clear(p, it.s, it.m);   // every row sees every position before
         const int first = it.tile0 * kWarps, last = min(it.tile1 * kWarps, (seen + kChunk - 1) / kChunk);
         const int my_n = last > first + warp ? (last - first - warp + kWarps - 1) / kWarps : 0;
+        const uint64_t policy = Axis::row_blocks(p, it.s) > 1 ? again : once;
         const int32_t *table = p.block_tables + static_cast<long long>(it.seq) * p.width;
         // Row of this warp's k-th chunk in the cache view; past the view for none (reads as zeros).
         const auto chunk_at = [&](int k) {
@@ -99,8 +100,8 @@ __global__ void __launch_bounds__(kThreads, Ring<HD>::CTAS)
                 mbar_arrive_expect_tx(bar, M::STAGE);
 #pragma unroll
                 for (int h = 0; h < M::HALVES; ++h) {
-                    tma_load_2d_hint(dst + h * M::HALF_BYTES, &tmK, h * 64, row, bar, once);
-                    tma_load_2d_hint(dst + M::PAGE + h * M::HALF_BYTES, &tmV, h * 64, row, bar, once);
+                    tma_load_2d_hint(dst + h * M::HALF_BYTES, &tmK, h * 64, row, bar, policy);
+                    tma_load_2d_hint(dst + M::PAGE + h * M::HALF_BYTES, &tmV, h * 64, row, bar, policy);
                 }
             }
             ++n_issued;

@@ -191,16 +191,21 @@ class _MultiStep(_KeptCall):
     """Holds the output, workspace and status word of a repeated step with
     several queries per sequence, and its call, checked once and kept until an
     attribute of the step is assigned (a tensor resized or moved in place, with
-    ``set_`` or ``.data``, is not noticed: assign it)."""
+    ``set_`` or ``.data``, is not noticed: assign it).
+
+    To keep a step while the number of rows changes, make q as long as it ever
+    gets and rewrite query_start: rows behind the last sequence's are not read.
+    Give max_query_len then, an upper bound of a sequence's rows."""
 
     tree_mask = None
 
     def __init__(self, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
                  context_lens: torch.Tensor, query_start: torch.Tensor, scale: float, max_context_len: int,
-                 workspace: torch.Tensor | None = None, status: binding.DeviceStatus | None = None):
+                 workspace: torch.Tensor | None = None, status: binding.DeviceStatus | None = None,
+                 max_query_len: int = 0):
         self.q, self.k_cache, self.v_cache = q, k_cache, v_cache
         self.block_tables, self.context_lens, self.query_start = block_tables, context_lens, query_start
-        self.scale, self.max_context_len = scale, max_context_len
+        self.scale, self.max_context_len, self.max_query_len = scale, max_context_len, max_query_len
         self.out = torch.empty_like(q)
         self.status = status if status is not None else binding.DeviceStatus(q.device)
         T, Hq, hd = q.shape
@@ -213,7 +218,8 @@ class _MultiStep(_KeptCall):
         if call is None:
             call = binding._multi_call(self._tree, self.out, self.q, self.k_cache, self.v_cache, self.block_tables,
                                        self.context_lens, self.query_start, self.tree_mask, self.scale,
-                                       self.max_context_len, self.workspace, self.status, stream)
+                                       self.max_context_len, self.workspace, self.status, stream,
+                                       self.max_query_len)
             if call.owns_workspace(self.workspace):
                 self._call = call
         return call(stream)
@@ -231,9 +237,9 @@ class TreeDecodeStep(_MultiStep):
     def __init__(self, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
                  context_lens: torch.Tensor, query_start: torch.Tensor, scale: float, max_context_len: int,
                  tree_mask: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                 status: binding.DeviceStatus | None = None):
+                 status: binding.DeviceStatus | None = None, max_query_len: int = 0):
         super().__init__(q, k_cache, v_cache, block_tables, context_lens, query_start, scale, max_context_len,
-                         workspace, status)
+                         workspace, status, max_query_len)
         self.tree_mask = tree_mask
 
     def write_tokens(self, k_new, v_new, slot_mapping, cow_pairs=None, stream=None) -> None:
