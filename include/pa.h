@@ -616,7 +616,9 @@ int pa_accept_tree(int32_t *accepted_lens, int32_t *accepted_nodes, int32_t *nex
  * Within a group every source is read before any destination is written, so a row
  * may be both.  Destinations must be distinct, and no slot of one group may be a
  * destination of another.  A group's rows of one head must fit in 48 KB (96 rows of
- * 128 fp32 values; PA_ERR_UNSUPPORTED). */
+ * 128 fp32 values, 192 of 128 bf16; PA_ERR_UNSUPPORTED): a smaller bound than
+ * pa_accept_tree's on max_accepted.  Longer paths go in several calls, pairs j from
+ * the first on: since a_j >= j, no call's sources are destinations of one before. */
 int pa_move_rows(void *k_cache, void *v_cache, const int64_t *slot_pairs, int num_groups, int pairs_per_group,
                  int num_kv_heads, int head_dim, int block_size, int num_blocks, int dtype, int32_t *dev_status,
                  void *stream);

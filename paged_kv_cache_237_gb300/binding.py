@@ -397,6 +397,16 @@ def _decode_call(out, q, k_cache, v_cache, block_tables, context_lens, scale, ma
     return _PreparedCall(_lib.pa_decode, out, operands, sizes, args, dev, keep)
 
 
+def _torch_stream(stream, dev) -> torch.cuda.Stream:
+    """A call's ``stream`` argument (a torch stream, another library's, or a handle) as torch's."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(getattr(stream, "cuda_stream", stream))
+    # handle 0 is the default stream, but torch takes it for "no handle given"
+    # and wraps a stream of its own pool, which nothing orders with the call
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+
+
 def _workspace(workspace, need, skip_counter_reset, dev, stream, zeroed=True):
     """The caller's workspace, checked, or a zeroed one when one is needed: made
     on the stream that uses it, so that its zeros are there in time and its
@@ -405,12 +415,7 @@ def _workspace(workspace, need, skip_counter_reset, dev, stream, zeroed=True):
         make = torch.zeros if zeroed else torch.empty
         if stream is None:
             return make(need, dtype=torch.uint8, device=dev), True
-        if not isinstance(stream, torch.cuda.Stream):
-            handle = int(getattr(stream, "cuda_stream", stream))
-            # handle 0 is the default stream, but torch takes it for "no handle given"
-            # and wraps a stream of its own pool, which nothing orders with the call
-            stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(_torch_stream(stream, dev)):
             return make(need, dtype=torch.uint8, device=dev), True
     if workspace is not None:
         _check_cuda(workspace, "workspace", (torch.uint8,), dev)
@@ -786,11 +791,16 @@ def pa_accept_tree(accepted_lens: torch.Tensor, accepted_nodes: torch.Tensor, ne
           _stream_ptr(stream, dev))
 
 
+MOVE_GROUP_BYTES = 48 * 1024   # of one head's rows in a group of pa_move_rows
+
+
 def pa_move_rows(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_pairs: torch.Tensor, *,
                  status: DeviceStatus | None = None, stream=None) -> None:
     """Move K/V rows from slot to slot, every KV head: slot_pairs int64
     [groups, pairs, 2] (source, destination), negative ones skipped.  Within a
-    group every source is read before any destination is written."""
+    group every source is read before any destination is written, and its rows
+    of one head fit in ``MOVE_GROUP_BYTES`` (``TreeDecodeStep.commit`` takes
+    longer paths)."""
     _check_cuda(k_cache, "k_cache", (torch.float32, torch.bfloat16))
     dev = k_cache.device
     _check_cuda(v_cache, "v_cache", (k_cache.dtype,), dev)

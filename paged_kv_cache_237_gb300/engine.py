@@ -10,6 +10,8 @@ token present.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import binding
@@ -256,8 +258,21 @@ class TreeDecodeStep(_MultiStep):
         return self.decode(stream)
 
     def commit(self, slot_pairs: torch.Tensor, stream=None) -> None:
-        """Move the kept path's rows (``pa_accept_tree``'s slot_pairs) to where the sequences go on."""
-        binding.pa_move_rows(self.k_cache, self.v_cache, slot_pairs, status=self.status, stream=stream)
+        """Move the kept path's rows (``pa_accept_tree``'s slot_pairs) to where the sequences go on.
+
+        Paths of more rows than one group of ``pa_move_rows`` holds go in several, from the first pair on: a path's j-th
+        row comes from the j-th drafted position or one behind it, so that no piece's sources are destinations of one
+        before."""
+        move = lambda pairs, on: binding.pa_move_rows(self.k_cache, self.v_cache, pairs, status=self.status, stream=on)
+        most = binding.MOVE_GROUP_BYTES // (self.k_cache.shape[-1] * self.k_cache.element_size())
+        if slot_pairs.dim() != 3 or slot_pairs.shape[1] <= most:
+            move(slot_pairs, stream)
+            return
+        binding._check_cuda(slot_pairs, "slot_pairs", (torch.int64,), self.k_cache.device)
+        with contextlib.nullcontext() if stream is None else \
+                torch.cuda.stream(binding._torch_stream(stream, self.k_cache.device)):
+            for piece in slot_pairs.split(most, dim=1):   # copied on the stream that moves them
+                move(piece.contiguous(), None)
 
 
 class CrossDecodeStep(_MultiStep):
