@@ -50,12 +50,15 @@ constexpr int kMmaThreads = 384;
 
 // A tile for both streams takes twice as long as one for one of them where the
 // softmax bounds both (head_dim 64), and no longer where the copies bound the second
-// (128).  Measured with the other weights: prompts of 1..448 queries over inputs of
-// 1..1500 with heads of 64, 219 us (equal weights 274); trees of 16..64 nodes with
-// heads of 128, 383 us (weights of two and one 486).  A beginning and end take as long
-// as 6 or 7 units (3 units: 261; 2: 466).
+// (128).  Measured, with the other weights in brackets, us: heads of 64, prompts of 1..448
+// queries over inputs of 1..1500 204 (equal weights 235), of 100..448 over 200..1500 120 (128),
+// 200 of 60..160 over 1..200 166 (189), trees with groups of 4 152 (155); heads of 128,
+// trees of 16..64 nodes with groups of 8 429 (weights of two and one 524), of 4 194 (219), but
+// prompts of 1..448 queries with a head each 308 (282).  A beginning and end take as long as
+// 6 or 5 units (head_dim 64, 10 units: 212, 124, 179; 3: 241, 136, 167; head_dim 128, 11: 452
+// and 198; 3: 458 and 206).
 template <int HD>
-using AxisOf = MultiAxis<kMultiMmaRows, HD == 64 ? kTile : kMultiMmaRows, kTile, HD == 64 ? 6 : 7>;
+using AxisOf = MultiAxis<kMultiMmaRows, HD == 64 ? kTile : kMultiMmaRows, kTile, HD == 64 ? 6 : 5>;
 
 // ---------------------------------------------------------------- tcgen05 ---
 __device__ __forceinline__ void tm_alloc(uint32_t dst, uint32_t cols) {
