@@ -62,7 +62,7 @@ int launch_passes(pa::MultiParams p, int head_dim, int max_query_len, bool f32, 
 
 struct MultiLayout {
     size_t ml, acc, bytes;   // where the rows' maxima and sums start, where their values do, and the workspace's size
-    int rows;                // rows per partial
+    int rows;                // rows of a place for a partial (the pass for few rows: its own)
 };
 
 // num_tokens rows of `group` heads: an item has no more rows than that.
@@ -70,7 +70,8 @@ MultiLayout multi_layout(int num_tokens, int group, int head_dim, bool f32) {
     const long long need = static_cast<long long>(num_tokens) * group;
     const auto least = [&](int most) { return static_cast<int>(need < most ? need : most); };
     MultiLayout l;
-    l.rows = least(f32 ? pa::kMultiF32Rows : pa::kMultiMmaRows);
+    // tcgen05: its streams keep sums there before, a half each
+    l.rows = f32 ? least(pa::kMultiF32Rows) : 2 * least(pa::kMultiMmaRows / 2);
     size_t slots = 2ull * (f32 ? pa::kMultiFewCtas : pa::kMultiMmaCtas) * l.rows;
     if (!f32) {   // the pass for few rows has more CTAs with fewer rows each; both fit
         const size_t few = 2ull * pa::kMultiFewCtas * least(16);

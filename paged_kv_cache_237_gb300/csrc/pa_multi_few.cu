@@ -343,7 +343,7 @@ int multi_few(const MultiParams &p, int dev, cudaStream_t st) {
 
 int launch_multi_few(const MultiParams &params, int head_dim, int dev, cudaStream_t st) {
     MultiParams p = params;
-    p.slot_rows = min(p.slot_rows, kRows);
+    p.slot_rows = static_cast<int>(min(static_cast<long long>(p.num_tokens) * p.group, static_cast<long long>(kRows)));
     return head_dim == 128 ? multi_few<128>(p, dev, st) : multi_few<64>(p, dev, st);
 }
 

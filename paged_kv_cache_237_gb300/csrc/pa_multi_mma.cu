@@ -24,17 +24,18 @@
 // its weights are alike, as much as the rounding of its result to bf16.
 // Row maxima are references that only move when a tile's maximum is more than 2^8
 // above: then the row's O and sum are rescaled (p stays below 2^8, and fp32 sums lose
-// nothing by it).
+// nothing by it).  O starts from zero every 64 steps, and its sums so far are kept in the
+// workspace (kRun).
 //
 // What bounds it: the chain from a stream's scores to its weights: tensor memory read,
 // maximum, exponentials and their parts, tensor memory written, three barrier operations.
 // The tensor core works three quarters of the time that the chain takes (head_dim 128).
 // Short contexts pay
 // each item's beginning and end besides (Q, results, 6 or 7 steps' time).  Measured: 8 x 2000
-// queries of 64 / 8 heads of 128 over 4,000..16,384 tokens 5.9 to 6.0 ms, 1.1 PFLOP/s; 7
-// contexts of up to 131,072 with 25 drafted tokens each 656 us, 4.3 TB/s; 32 lognormal
-// contexts with trees of 16..64 nodes 429 us; prompts of 1..448 queries over 1..1500
-// tokens, 20 heads of 64: 208 us.
+// queries of 64 / 8 heads of 128 over 4,000..16,384 tokens 6.2 to 6.8 ms, 0.95 to 1.04 PFLOP/s; 7
+// contexts of up to 131,072 with 25 drafted tokens each 680 to 750 us, 3.8 to 4.2 TB/s; 32 lognormal
+// contexts with trees of 16..64 nodes 445 us; prompts of 1..448 queries over 1..1500
+// tokens, 20 heads of 64: 200 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -47,6 +48,13 @@ namespace {
 
 constexpr int kTile = 128;                 // tokens per tile, and rows per stream
 constexpr int kMmaThreads = 384;
+
+// Steps of a stream whose products meet in tensor memory.  The tensor core cuts a sum off where an addition rounds, 16 tokens
+// and a part of the weights at a time: 2^-25 of it on average, 2^-15 in 64 steps and always towards zero.  So the sums of a
+// run join those of the runs before it in the CTA's part of the workspace, by fp32 additions.  Measured, without runs / of
+// 64 / of 32 steps: 32 lognormal contexts with trees 429 / 443 / 457 us, 7 contexts of up to 131,072 tokens 662 / 679 / 690 (results
+// 1.7 / 0.4 / 0.2 hundredths of a bf16 step towards zero on average), 8 x 2000 queries 5930 / 6210 / 6440.
+constexpr int kRun = 64;
 
 // A tile for both streams takes twice as long as one for one of them where the
 // softmax bounds both (head_dim 64), and no longer where the copies bound the second
@@ -170,6 +178,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// 32 sums join those that a row keeps in memory (times f), if there are any yet.
+__device__ __forceinline__ void keep_sums(float4 *kept, int stride, const float *o, float f, bool any) {
+    float4 y[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) y[c] = any ? __ldcg(kept + c * stride) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        __stcg(kept + c * stride, make_float4(fmaf(y[c].x, f, o[4 * c]), fmaf(y[c].y, f, o[4 * c + 1]),
+                                              fmaf(y[c].z, f, o[4 * c + 2]), fmaf(y[c].w, f, o[4 * c + 3])));
+}
+
 // Shared memory: Q (two tiles), rings of K and V tiles, then the small things.
 template <int HD>
 struct Smem {
@@ -378,7 +397,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                             const uint32_t pa = pt + half * 32;
     #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma_ts(o, pa + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, q >= 2 || half + kk > 0, lead);
+                                mma_ts(o, pa + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, (q >> 1) % kRun > 0 || half + kk > 0, lead);
     #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 mma_ts(o, pa + 64 + kk * 8, vb + kk * (16 * 128 >> 4), kIdescO, true, lead);
@@ -464,6 +483,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             arrive(&ctl.q_full);
             const bool live = (warp & 3) * 32 < rows;   // this warp has rows
             float ref = -INFINITY, sum = 0.f;
+            // Where this row's sums of earlier runs are kept, four columns next to the other rows' same: in the CTA's place for
+            // this item's partial, which is not written before.
+            const auto kept_row = [&] { return static_cast<long long>(it.slot(blockIdx.x)) * p.slot_rows + s * (p.slot_rows / 2); };
             const int tiles = it.tile1 - it.tile0;
             int mine = 0;   // steps of this stream
             for (int t = 0; t < tiles; ++t, v.advance<M::NV>()) {
@@ -489,6 +511,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                         }
                     }
                     fence_proxy_async_smem();
+                }
+                if (live && mine > 0 && mine % kRun == 0) {
+                    // O holds the products of a whole run: these scores were issued behind them.  The next ones start from zero.
+                    const int stride = p.slot_rows / 2;
+                    float4 *kept = reinterpret_cast<float4 *>(p.part_acc + kept_row() * HD) + r;
+                    float *kept_ref = p.part_ml + 2 * (kept_row() + r), f = 0.f;
+                    if (r < rows) {
+                        if (mine > kRun) f = *kept_ref == ref ? 1.f : ex2(*kept_ref - ref);
+                        *kept_ref = ref;
+                    }
+#pragma unroll 1
+                    for (int g = 0; g < HD / 32; ++g, kept += 8 * stride) {
+                        float o[32];
+                        tm_ld32(to + g * 32, o);
+                        tm_wait_ld();
+                        if (r < rows) keep_sums(kept, stride, o, f, mine > kRun);
+                    }
                 }
                 if (live) {
                     float x[kTile];
@@ -571,6 +610,34 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             // may still be reading there.
             if (mine > 0 && !(ok = await_warp(ctl, &ctl.o_full[s], ends++ & 1))) break;
             tm_fence_after();
+            if (live && mine > kRun) {   // the earlier runs' sums join the last one's
+                const int stride = p.slot_rows / 2;
+                const float4 *kept = reinterpret_cast<const float4 *>(p.part_acc + kept_row() * HD) + r;
+                float f = 0.f;
+                if (r < rows) {
+                    const float kept_ref = p.part_ml[2 * (kept_row() + r)];
+                    f = kept_ref == ref ? 1.f : ex2(kept_ref - ref);
+                }
+#pragma unroll 1
+                for (int g = 0; g < HD / 16; ++g, kept += 4 * stride) {
+                    float o[16];
+                    float4 y[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) y[c] = r < rows ? __ldcg(kept + c * stride) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    tm_ld16(to + g * 16, o);
+                    tm_wait_ld();
+                    uint32_t u[16];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        u[4 * c] = __float_as_uint(fmaf(y[c].x, f, o[4 * c]));
+                        u[4 * c + 1] = __float_as_uint(fmaf(y[c].y, f, o[4 * c + 1]));
+                        u[4 * c + 2] = __float_as_uint(fmaf(y[c].z, f, o[4 * c + 2]));
+                        u[4 * c + 3] = __float_as_uint(fmaf(y[c].w, f, o[4 * c + 3]));
+                    }
+                    tm_st16(to + g * 16, u);
+                }
+                tm_wait_st();
+            }
             const uint32_t sums_at = 2 * (item_no & 1);
             if (!both) {
                 tm_st2(ts + sums_at, __float_as_uint(ref), __float_as_uint(sum));
