@@ -548,7 +548,8 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_q_heads, int num_kv_hea
  * args as for pa_decode: num_seqs, max_blocks_per_seq, num_blocks, dtype,
  * max_context_len (longer entries are clamped and flagged), max_query_len (worth giving
  * wherever sequences differ in their queries or q has padding: without it the kernels are
- * picked by num_tokens / num_seqs), dev_status, stream, and
+ * picked by num_tokens / num_seqs, and always by max_context_len, so a close bound is the
+ * better one), dev_status, stream, and
  * a workspace of pa_decode_tree_workspace_size bytes (both calls), which needs no
  * zeros and may be shared with pa_decode under the same rule of one call at a time
  * (its first 256 bytes are left as they are).  phase, simt, partition_size and the

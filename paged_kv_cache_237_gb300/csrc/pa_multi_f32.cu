@@ -20,12 +20,12 @@
 // K and V come by cp.async: the next tile's K while this one's products run, its V
 // while the next scores do; two to four CTAs per SM fill each other's gaps.
 //   MT = 1: few rows per sequence, bound by the copies and their latency.  24
-//   multi-head sequences of up to 4000 tokens with 1 to 12 rows: 337 us, 4.4 TB/s
-//   (0.65 of the copy rate).
+//   multi-head sequences of up to 4000 tokens with 1 to 12 rows: 327 to 339 us,
+//   4.4 to 4.6 TB/s (0.65 to 0.67 of the copy rate).
 //   MT = 2: many rows, bound by the tensor pipe (8 cycles an instruction, three for
 //   each 16 x 8 x 8 products: 98 TFLOP/s, and rows that fill up to 16) and by what lies
-//   between its phases; some 40 % of its cycles busy.  16 sequences of 100 to 1200 tokens, 24
-//   heads of 64, 1 to 300 queries: 282 us.  Four row tiles would need an SM for one CTA.
+//   between its phases; 41 % of its cycles busy.  16 sequences of 100 to 1200 tokens, 24
+//   heads of 64, 1 to 300 queries: 274 to 282 us.  Four row tiles would need an SM for one CTA.
 #include <cuda_runtime.h>
 
 #include <cstdint>

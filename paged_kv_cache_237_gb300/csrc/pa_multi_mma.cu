@@ -18,9 +18,9 @@
 //                  memory as it is cached (tokens x head_dim, the MN-major form)
 //
 // p enters as the sum of two bf16 parts (about 16 significant bits), as in pa_decode and
-// in the pass for few rows: a sequence's result keeps the same bits whatever shares its
-// batch.  One part alone would take a third of the matrix work away (32 contexts with
-// trees 382 us, below; 8 x 2000 queries 4.9 ms) and leave a row off by up to 2^-8 where
+// in the pass for few rows: a sequence's result is as exact whatever shares its batch.
+// One part alone would take a third of the matrix work away (32 contexts with trees 382
+// us, 8 x 2000 queries 4.9 ms) and leave a row off by up to 2^-8 where
 // its weights are alike, as much as the rounding of its result to bf16.
 // Row maxima are references that only move when a tile's maximum is more than 2^8
 // above: then the row's O and sum are rescaled (p stays below 2^8, and fp32 sums lose
@@ -28,14 +28,14 @@
 // workspace (kRun).
 //
 // What bounds it: the chain from a stream's scores to its weights: tensor memory read,
-// maximum, exponentials and their parts, tensor memory written, three barrier operations.
-// The tensor core works three quarters of the time that the chain takes (head_dim 128).
-// Short contexts pay
-// each item's beginning and end besides (Q, results, 6 or 7 steps' time).  Measured: 8 x 2000
-// queries of 64 / 8 heads of 128 over 4,000..16,384 tokens 6.2 to 6.8 ms, 0.95 to 1.04 PFLOP/s; 7
-// contexts of up to 131,072 with 25 drafted tokens each 680 to 750 us, 3.8 to 4.2 TB/s; 32 lognormal
-// contexts with trees of 16..64 nodes 445 us; prompts of 1..448 queries over 1..1500
-// tokens, 20 heads of 64: 200 us.
+// maximum, exponentials and their parts, tensor memory written, three barrier operations;
+// for long prompts, whose steps come one after the other, the tensor core nearly as much
+// (3072 cycles of some 4400 a step of both streams, head_dim 128).  Short contexts pay
+// each item's beginning and end besides (Q, results, 5 or 6 steps' time).  Measured: 8 x 2000
+// queries of 64 / 8 heads of 128 over 4,000..16,384 tokens 6.2 to 7.1 ms, 0.91 to 1.04 PFLOP/s; 7
+// contexts of up to 131,072 with 25 drafted tokens each 680 to 785 us, 3.6 to 4.2 TB/s; 32 lognormal
+// contexts with trees of 16..64 nodes 443 to 465 us; prompts of 1..448 queries over 1..1500
+// tokens, 20 heads of 64: 193 to 200 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
