@@ -30,7 +30,7 @@
 // What bounds it: the chain from a stream's scores to its weights: tensor memory read,
 // maximum, exponentials and their parts, tensor memory written, three barrier operations;
 // for long prompts, whose steps come one after the other, the tensor core nearly as much
-// (3072 cycles of some 4400 a step of both streams, head_dim 128).  Short contexts pay
+// (70 % of a step's cycles, head_dim 128).  Short contexts pay
 // each item's beginning and end besides (Q, results, 5 or 6 steps' time).  Measured: 8 x 2000
 // queries of 64 / 8 heads of 128 over 4,000..16,384 tokens 6.2 to 7.1 ms, 0.91 to 1.04 PFLOP/s; 7
 // contexts of up to 131,072 with 25 drafted tokens each 680 to 785 us, 3.6 to 4.2 TB/s; 32 lognormal
